@@ -68,6 +68,14 @@ typedef int32_t sq_status;
 #define SQ_QUANT_DUAL_AXIS 0      /* row factors sqrt(m / w) + impact-weighted column fit (the method) */
 #define SQ_QUANT_ROW_ABSMAX 1     /* per-row absmax r = m / qmax, column scales 1 (ablation: no fit) */
 
+#define SQ_DTYPE_F32  0            /* element types of the scan's and the norms' row arrays */
+#define SQ_DTYPE_BF16 1
+#define SQ_DTYPE_F16  2
+#define SQ_NORM_RMS 0             /* divide by sqrt(mean(x^2) + eps) */
+#define SQ_NORM_L2  1             /* divide by sqrt(sum(x^2) + eps)  */
+#define SQ_ACT_SILU    0          /* gate g(z) = z sigmoid(z) */
+#define SQ_ACT_SIGMOID 1          /* gate g(z) = sigmoid(z)   */
+
 #define SQ_MAX_WIDTHS 8
 #define SQ_MAX_GRID   8
 #define SQ_PIVOT_BITS 16          /* width reported for a pivot (binary16) unit/row  */
@@ -270,6 +278,104 @@ sq_status sq_copy(const void* d_src, void* d_dst, size_t n_bytes, void* stream);
  * cannot cap residency at waves_per_simd (the per-workgroup LDS limit); asynchronous otherwise. */
 sq_status sq_valu_probe(int32_t waves_per_simd, int32_t n_blocks, float* d_out, uint64_t* n_fma,
                         int32_t* blocks_per_cu, void* stream);
+
+/* ---- scan: the recurrence over whole sequences ---------------------------
+ * The float form of the step's recurrence over packed sequences (a prompt, several drafted tokens,
+ * a training batch): per sequence b and head h, from S = d_s0[b][h] (zero if d_s0 is NULL), for the
+ * tokens t of the sequence in order,
+ *   X = D_t S + beta_t k_t (v_t - (D_t S)^T k_t)^T;  y_t = X^T q_t;  S = X,
+ * and d_s1[b][h] = S at the end (the layout sq_pack takes and sq_unpack and sq_fp32_step have, one layer).
+ * Sequence b holds the tokens [d_seq_start[b], d_seq_start[b + 1]) of the packed arrays (int32, device,
+ * n_seq + 1 values, not decreasing, within [0, n_tokens]; NULL: one sequence of n_tokens).  A sequence
+ * may be empty (its state is copied); tokens outside every sequence are neither read nor written.
+ * Offsets that break these rules give unspecified results and touch nothing outside the arrays.
+ *
+ * Row arrays (sq_rows): element (token, head, j) at d_ptr[token * stride + head * d + j], so that q, k and
+ * v may be parts of one wider array.  q, k: n_heads_k heads (a divisor of n_heads) of d_k elements; head h
+ * reads q and k of head h / (n_heads / n_heads_k).  v, y: n_heads heads of d_v elements.  All four have the
+ * element type cfg->dtype; gates, beta, states and the arithmetic are float32 (products on the bfloat16
+ * matrix units with every float32 operand split into three exact parts), each output rounded once.
+ * d_gate: alpha in [0, 1], [n_tokens][n_heads] (GDN) or [n_tokens][n_heads][d_k] (KDA); d_beta
+ * [n_tokens][n_heads].  (The gradients of q, k and gate count gates below 1e-30 as 1e-30.)
+ * Alignment: q, k and dy 16 bytes, with stride * element size a multiple of 16; d_gate (KDA) 16 bytes;
+ * the workspace 256 bytes.  Strides at least heads * d.
+ * d_s0 and d_s1 may be the same array; no other two arrays may overlap.
+ *
+ * Workspace: sq_delta_scan_bytes bytes of device memory, the caller's, free again when the call's work on
+ * `stream` is done; calls that may overlap (two streams, or two captured graphs whose replays overlap)
+ * need one each.  No call allocates or synchronizes, so all of them can be captured.
+ * The result does not depend on what else runs (no atomics; sums in a fixed order). */
+typedef struct sq_rows {
+    void* d_ptr;
+    int64_t stride;               /* elements from one token (row) to the next */
+} sq_rows;
+
+typedef struct sq_scan_cfg {
+    int32_t form;                 /* SQ_FORM_GDN or SQ_FORM_KDA */
+    int32_t dtype;                /* SQ_DTYPE_*: q, k, v, y and their gradients */
+    int32_t n_heads, n_heads_k;   /* heads of v, y and the states; heads of q and k */
+    int32_t d_k, d_v;             /* a pair of sq_supported_shapes */
+    int32_t n_seq;
+    int64_t n_tokens;             /* tokens of the packed arrays, below 2^31 */
+    const int32_t* d_seq_start;
+} sq_scan_cfg;
+
+/* Bytes of workspace for sq_delta_scan (backward = 0) or sq_delta_scan_bwd (1); d_seq_start is not read. */
+sq_status sq_delta_scan_bytes(const sq_scan_cfg* cfg, int32_t backward, size_t* bytes);
+sq_status sq_delta_scan(const sq_scan_cfg* cfg, const sq_rows* q, const sq_rows* k, const sq_rows* v,
+                        const float* d_gate, const float* d_beta, const float* d_s0, const sq_rows* y,
+                        float* d_s1, void* d_work, size_t work_bytes, void* stream);
+/* Gradients of sq_delta_scan: from dy (the gradient of y) and d_ds1 (of the final states, NULL = zero) the
+ * gradients of q, k, v (dtype; dq and dk summed over the heads that share them), gate, beta and the first
+ * states (float32, the inputs' layouts; d_ds0 may be NULL, and may be d_ds1).  Nothing of the forward call
+ * is needed: the states are computed again.  d_s0 as in the forward call. */
+sq_status sq_delta_scan_bwd(const sq_scan_cfg* cfg, const sq_rows* q, const sq_rows* k, const sq_rows* v,
+                            const float* d_gate, const float* d_beta, const float* d_s0, const sq_rows* dy,
+                            const float* d_ds1, const sq_rows* dq, const sq_rows* dk, const sq_rows* dv,
+                            float* d_dgate, float* d_dbeta, float* d_ds0, void* d_work, size_t work_bytes,
+                            void* stream);
+
+/* ---- norms around the recurrence -----------------------------------------
+ * Rows of d elements: row (i, j), i < n_outer, j < n_inner, at d_ptr[i * stride + j * d] (a token's heads
+ * lie side by side; n_inner = 1 for plain rows), of any length d from 1 to 16384.  Statistics and sums in float32,
+ * each output rounded once.  inv(a) = 1 / sqrt(mean(a^2) + eps) (SQ_NORM_RMS) or 1 / sqrt(sum(a^2) + eps)
+ * (SQ_NORM_L2: rows of unit norm, as the step and the scan take q and k).
+ *   sq_norm_in  (before a block):  h = x + res_scale * chan_scale * r;   n = out_scale * weight * h * inv(h)
+ *   sq_norm_out (after a block):   o = x + res_scale * chan_scale * (weight * y * inv(y) * act(z))
+ * weight and chan_scale: float32 [d], NULL = 1.  r (with h), z and x may be NULL: no residual, no gate.
+ * Types: in: x, r, h cfg->dtype, n cfg->dtype_out; out: y cfg->dtype, z, x, o cfg->dtype_out; gradients have
+ * their array's type, those of weight and chan_scale are float32.
+ * An output may be an input's own array if its type and stride are the same; arrays must not overlap otherwise.
+ * Rows whose arrays all start at 16 bytes, with strides and d multiples of 8, are read 16 bytes at a time.
+ *
+ * sq_norm_in_bwd: from h, dn and (optional) dh, the gradient that reaches h past the norm:
+ *   dx = dh + d(n)/d(h) dn;  dr = res_scale * chan_scale * dx;  dweight = sum over rows of out_scale * dn * h * inv(h);
+ *   dchan_scale = sum over rows of res_scale * dx * r.
+ * sq_norm_out_bwd: from y, z, do: dy, dz, dweight, dchan_scale (the gradient of x is do itself).
+ * dr, dz, d_dweight, d_dchan_scale may be NULL; r is needed for d_dchan_scale only.  With no rows the sums are written as zero.
+ * Sums over rows are taken in a fixed order through a workspace of sq_norm_bytes bytes (used if d_dweight or
+ * d_dchan_scale is given), under the rules of the scan's. */
+typedef struct sq_norm_cfg {
+    int32_t dtype, dtype_out;     /* SQ_DTYPE_* */
+    int32_t kind;                 /* SQ_NORM_RMS or SQ_NORM_L2 */
+    int32_t act;                  /* SQ_ACT_*, sq_norm_out only */
+    int64_t n_outer;
+    int32_t n_inner, d;
+    float eps, res_scale, out_scale;
+} sq_norm_cfg;
+
+sq_status sq_norm_bytes(int64_t n_rows, int32_t d, size_t* bytes);
+sq_status sq_norm_in(const sq_norm_cfg* cfg, const sq_rows* x, const sq_rows* r, const float* d_weight,
+                     const float* d_chan_scale, const sq_rows* h, const sq_rows* n, void* stream);
+sq_status sq_norm_in_bwd(const sq_norm_cfg* cfg, const sq_rows* h, const sq_rows* dn, const sq_rows* dh,
+                         const sq_rows* r, const float* d_weight, const float* d_chan_scale, const sq_rows* dx,
+                         const sq_rows* dr, float* d_dweight, float* d_dchan_scale, void* d_work,
+                         size_t work_bytes, void* stream);
+sq_status sq_norm_out(const sq_norm_cfg* cfg, const sq_rows* y, const sq_rows* z, const sq_rows* x,
+                      const float* d_weight, const float* d_chan_scale, const sq_rows* o, void* stream);
+sq_status sq_norm_out_bwd(const sq_norm_cfg* cfg, const sq_rows* y, const sq_rows* z, const sq_rows* d_o,
+                          const float* d_weight, const float* d_chan_scale, const sq_rows* dy, const sq_rows* dz,
+                          float* d_dweight, float* d_dchan_scale, void* d_work, size_t work_bytes, void* stream);
 
 /* ---- errors / info ------------------------------------------------------ */
 const char* sq_status_str(sq_status s);

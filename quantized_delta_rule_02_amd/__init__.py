@@ -10,11 +10,12 @@ from __future__ import annotations
 
 import ctypes
 from ctypes import POINTER, byref, c_double, c_float, c_int32, c_size_t, c_uint64, c_void_p
+from contextlib import contextmanager
 
 import numpy as np
 
 from . import _lib
-from ._lib import (SQ_FORM_GDN, SQ_FORM_KDA, SQ_PIVOT_BITS, SQ_QUANT_DUAL_AXIS, SQ_QUANT_ROW_ABSMAX,
+from ._lib import (SQ_ACT_SIGMOID, SQ_ACT_SILU, SQ_DTYPE_BF16, SQ_DTYPE_F16, SQ_DTYPE_F32, SQ_NORM_L2, SQ_NORM_RMS, SQ_FORM_GDN, SQ_FORM_KDA, SQ_PIVOT_BITS, SQ_QUANT_DUAL_AXIS, SQ_QUANT_ROW_ABSMAX,
                    SQ_SPLIT_STATIC_MAX_FLOATS, SQ_STEP_NO_JOIN, SQ_STEP_SPLIT, SQ_STEP_VALIDATE, SQ_UNIT_HEAD,
                    SQ_UNIT_ROW)
 
@@ -22,6 +23,8 @@ __all__ = [
     "StepQError", "Plan", "Pool", "sq_plan_create", "sq_plan_describe", "sq_plan_info", "sq_pool_bind", "sq_pool_release", "sq_plan_units", "sq_plan_rows",
     "sq_plan_save", "sq_plan_load", "sq_calib_generate", "sq_pool_bytes", "sq_pool_create", "sq_state_step", "sq_state_step_split_static",
     "sq_pack", "sq_unpack", "sq_export", "sq_import", "sq_int8_step", "sq_fp32_step", "sq_copy", "sq_valu_probe",
+    "sq_delta_scan_bytes", "sq_delta_scan", "sq_delta_scan_bwd", "sq_norm_bytes", "sq_norm_in", "sq_norm_in_bwd", "sq_norm_out", "sq_norm_out_bwd",
+    "SQ_DTYPE_F32", "SQ_DTYPE_BF16", "SQ_DTYPE_F16", "SQ_NORM_RMS", "SQ_NORM_L2", "SQ_ACT_SILU", "SQ_ACT_SIGMOID",
     "sq_supported_shapes", "SQ_FORM_GDN", "SQ_FORM_KDA", "SQ_UNIT_HEAD", "SQ_UNIT_ROW", "SQ_STEP_SPLIT",
     "SQ_STEP_VALIDATE", "SQ_STEP_NO_JOIN", "SQ_SPLIT_STATIC_MAX_FLOATS", "SQ_PIVOT_BITS", "SQ_QUANT_DUAL_AXIS", "SQ_QUANT_ROW_ABSMAX",
 ]
@@ -382,3 +385,228 @@ def sq_valu_probe(waves_per_simd, out, stream=None):
     _check(_lib.load().sq_valu_probe(int(waves_per_simd), n_blocks, c_void_p(out.data_ptr()), byref(n), byref(fit),
                                      _stream(stream)), "sq_valu_probe")
     return n.value, fit.value
+
+
+# ---------------------------------------------------------------- scan and norms
+
+def _dtype_code(dtype) -> int:
+    import torch
+    codes = {torch.float32: SQ_DTYPE_F32, torch.bfloat16: SQ_DTYPE_BF16, torch.float16: SQ_DTYPE_F16}
+    if dtype not in codes:
+        raise TypeError(f"element type {dtype}: float32, bfloat16 or float16")
+    return codes[dtype]
+
+
+@contextmanager
+def _launch_on(device, stream):
+    """The device current, and the handle of `stream` on it (None: the device's current stream)."""
+    import torch
+    if getattr(stream, "device", device) != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    with torch.cuda.device(device):
+        yield _stream(stream)
+
+
+def _workspace(workspace, nbytes, device, stream):
+    """The caller's workspace, checked, or a new one that belongs to the stream of the call."""
+    import torch
+    if workspace is not None:
+        _on(workspace, device, "workspace")
+        return _dev(workspace, torch.uint8, nbytes, "workspace"), workspace.numel(), workspace
+    if stream is None:
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        owner = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(owner):
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return c_void_p(buf.data_ptr()), nbytes, buf
+
+
+def _on(t, device, name):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _row_array(t, shape, dtype, device, name):
+    """sq_rows of a tensor [tokens, heads, d] whose heads lie side by side (any stride between tokens)."""
+    _on(t, device, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    T, H, d = shape
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the elements and heads of a token must be contiguous")
+    return _lib.SqRows(c_void_p(t.data_ptr()), t.stride(0) if T > 1 else H * d)
+
+
+def _plain(t, shape, device, name):
+    """Pointer of a contiguous float32 tensor of exactly this shape (None stays NULL)."""
+    import torch
+    if t is None:
+        return None
+    _on(t, device, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return _dev(t, torch.float32, 0, name)
+
+
+def _scan_cfg(form, q, v, seq_start):
+    import torch
+    for t, name in ((q, "q"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [tokens, heads, d]")
+    T, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    n_seq, start = 1, None
+    if seq_start is not None:
+        _on(seq_start, q.device, "seq_start")
+        if seq_start.dim() != 1 or seq_start.numel() < 1:
+            raise ValueError("seq_start must hold n_seq + 1 offsets")
+        n_seq = seq_start.numel() - 1
+        start = _dev(seq_start, torch.int32, n_seq + 1, "seq_start")
+    return _lib.SqScanCfg(int(form), _dtype_code(q.dtype), H, Hk, dk, dv, n_seq, T, start)
+
+
+def sq_delta_scan_bytes(form, dtype, n_heads, n_heads_k, d_k, d_v, n_seq, n_tokens, backward=False) -> int:
+    """Workspace bytes of sq_delta_scan (or of sq_delta_scan_bwd) for arrays of these sizes."""
+    cfg = _lib.SqScanCfg(int(form), _dtype_code(dtype), n_heads, n_heads_k, d_k, d_v, n_seq, n_tokens, None)
+    n = c_size_t(0)
+    _check(_lib.load().sq_delta_scan_bytes(byref(cfg), int(backward), byref(n)), "sq_delta_scan_bytes")
+    return n.value
+
+
+def _scan_bytes(cfg, backward):
+    n = c_size_t(0)
+    _check(_lib.load().sq_delta_scan_bytes(byref(cfg), backward, byref(n)), "sq_delta_scan_bytes")
+    return n.value
+
+
+def sq_delta_scan(form, q, k, v, gate, beta, y, seq_start=None, s0=None, s1=None, workspace=None, stream=None):
+    """The recurrence over packed sequences: writes y and, if given, the final states s1.
+
+    q, k [tokens, heads_k, d_k], v, y [tokens, heads, d_v] (one type; any token stride); gate [tokens, heads] or
+    [tokens, heads, d_k], beta [tokens, heads], s0, s1 [n_seq, heads, d_k, d_v] float32; seq_start int32 [n_seq + 1].
+    """
+    cfg = _scan_cfg(form, q, v, seq_start)
+    T, H, Hk, dk, dv, dev = cfg.n_tokens, cfg.n_heads, cfg.n_heads_k, cfg.d_k, cfg.d_v, q.device
+    st = (cfg.n_seq, H, dk, dv)
+    rows = lambda t, h, d, name: byref(_row_array(t, (T, h, d), q.dtype, dev, name))  # noqa: E731
+    args = [rows(q, Hk, dk, "q"), rows(k, Hk, dk, "k"), rows(v, H, dv, "v"),
+            _plain(gate, (T, H, dk) if form == SQ_FORM_KDA else (T, H), dev, "gate"), _plain(beta, (T, H), dev, "beta"),
+            _plain(s0, st, dev, "s0"), rows(y, H, dv, "y"), _plain(s1, st, dev, "s1")]
+    with _launch_on(dev, stream) as handle:
+        work, nbytes, keep = _workspace(workspace, _scan_bytes(cfg, 0), dev, stream)
+        _check(_lib.load().sq_delta_scan(byref(cfg), *args, work, nbytes, handle), "sq_delta_scan")
+        del keep
+
+
+def sq_delta_scan_bwd(form, q, k, v, gate, beta, dy, dq, dk, dv, dgate, dbeta, seq_start=None, s0=None, ds1=None,
+                      ds0=None, workspace=None, stream=None):
+    """Gradients of sq_delta_scan, from dy and (optional) ds1, into dq, dk, dv, dgate, dbeta and (optional) ds0."""
+    cfg = _scan_cfg(form, q, v, seq_start)
+    T, H, Hk, nk, nv, dev = cfg.n_tokens, cfg.n_heads, cfg.n_heads_k, cfg.d_k, cfg.d_v, q.device
+    st, gs = (cfg.n_seq, H, nk, nv), ((T, H, nk) if form == SQ_FORM_KDA else (T, H))
+    rows = lambda t, h, d, name: byref(_row_array(t, (T, h, d), q.dtype, dev, name))  # noqa: E731
+    args = [rows(q, Hk, nk, "q"), rows(k, Hk, nk, "k"), rows(v, H, nv, "v"), _plain(gate, gs, dev, "gate"),
+            _plain(beta, (T, H), dev, "beta"), _plain(s0, st, dev, "s0"), rows(dy, H, nv, "dy"), _plain(ds1, st, dev, "ds1"),
+            rows(dq, Hk, nk, "dq"), rows(dk, Hk, nk, "dk"), rows(dv, H, nv, "dv"), _plain(dgate, gs, dev, "dgate"),
+            _plain(dbeta, (T, H), dev, "dbeta"), _plain(ds0, st, dev, "ds0")]
+    with _launch_on(dev, stream) as handle:
+        work, nbytes, keep = _workspace(workspace, _scan_bytes(cfg, 1), dev, stream)
+        _check(_lib.load().sq_delta_scan_bwd(byref(cfg), *args, work, nbytes, handle), "sq_delta_scan_bwd")
+        del keep
+
+
+class _NormCall:
+    """The configuration and row arrays of one norm call; `first` fixes the shape: [rows, d] or [tokens, heads, d]."""
+
+    def __init__(self, first, name):
+        import torch
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if first.dim() not in (2, 3):
+            raise ValueError(f"{name} must be [rows, d] or [tokens, heads, d]")
+        self.shape, self.device = tuple(first.shape), first.device
+        self.outer, self.d = first.shape[0], first.shape[-1]
+        self.inner = first.shape[1] if first.dim() == 3 else 1
+
+    def rows(self, t, dtype, name):
+        if t is None:
+            return None
+        if tuple(t.shape) != self.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.shape}")
+        t = t if t.dim() == 3 else t.unsqueeze(1)
+        return byref(_row_array(t, (self.outer, self.inner, self.d), dtype, self.device, name))
+
+    def vec(self, t, name):
+        return _plain(t, (self.d,), self.device, name)
+
+    def cfg(self, dtype, dtype_out, kind, act, eps, res_scale, out_scale):
+        return byref(_lib.SqNormCfg(_dtype_code(dtype), _dtype_code(dtype_out), int(kind), int(act), self.outer,
+                                    self.inner, self.d, eps, res_scale, out_scale))
+
+    def work(self, workspace, stream, wanted):
+        if not wanted:
+            return None, 0, None
+        return _workspace(workspace, sq_norm_bytes(self.outer * self.inner, self.d), self.device, stream)
+
+
+def sq_norm_bytes(n_rows, d) -> int:
+    """Workspace bytes of the norms' backward passes over n_rows rows of d elements."""
+    n = c_size_t(0)
+    _check(_lib.load().sq_norm_bytes(int(n_rows), int(d), byref(n)), "sq_norm_bytes")
+    return n.value
+
+
+def sq_norm_in(x, n, weight=None, r=None, h=None, chan_scale=None, res_scale=1.0, kind=SQ_NORM_RMS, eps=1e-6,
+               out_scale=1.0, stream=None):
+    """h = x + res_scale chan_scale r (written if given);  n = out_scale weight h / sqrt(mean or sum of h^2 + eps)."""
+    c = _NormCall(x, "x")
+    args = [c.rows(x, x.dtype, "x"), c.rows(r, x.dtype, "r"), c.vec(weight, "weight"), c.vec(chan_scale, "chan_scale"),
+            c.rows(h, x.dtype, "h"), c.rows(n, n.dtype, "n")]
+    with _launch_on(c.device, stream) as handle:
+        _check(_lib.load().sq_norm_in(c.cfg(x.dtype, n.dtype, kind, 0, eps, res_scale, out_scale), *args, handle), "sq_norm_in")
+
+
+def sq_norm_in_bwd(h, dn, dx, weight=None, r=None, dh=None, dr=None, chan_scale=None, res_scale=1.0, dweight=None,
+                   dchan_scale=None, kind=SQ_NORM_RMS, eps=1e-6, out_scale=1.0, workspace=None, stream=None):
+    """Gradients of sq_norm_in from h, dn and (optional) dh: dx and, if given, dr, dweight, dchan_scale (needs r)."""
+    c = _NormCall(h, "h")
+    args = [c.rows(h, h.dtype, "h"), c.rows(dn, dn.dtype, "dn"), c.rows(dh, h.dtype, "dh"), c.rows(r, h.dtype, "r"),
+            c.vec(weight, "weight"), c.vec(chan_scale, "chan_scale"), c.rows(dx, h.dtype, "dx"), c.rows(dr, h.dtype, "dr"),
+            c.vec(dweight, "dweight"), c.vec(dchan_scale, "dchan_scale")]
+    with _launch_on(c.device, stream) as handle:
+        work, nbytes, keep = c.work(workspace, stream, dweight is not None or dchan_scale is not None)
+        _check(_lib.load().sq_norm_in_bwd(c.cfg(h.dtype, dn.dtype, kind, 0, eps, res_scale, out_scale), *args, work, nbytes,
+                                          handle), "sq_norm_in_bwd")
+        del keep
+
+
+def sq_norm_out(y, o, weight=None, z=None, act=SQ_ACT_SILU, x=None, chan_scale=None, res_scale=1.0, eps=1e-6,
+                kind=SQ_NORM_RMS, stream=None):
+    """o = x + res_scale chan_scale (weight y / sqrt(mean y^2 + eps) act(z)); x and z may be left out."""
+    c = _NormCall(y, "y")
+    args = [c.rows(y, y.dtype, "y"), c.rows(z, o.dtype, "z"), c.rows(x, o.dtype, "x"), c.vec(weight, "weight"),
+            c.vec(chan_scale, "chan_scale"), c.rows(o, o.dtype, "o")]
+    with _launch_on(c.device, stream) as handle:
+        _check(_lib.load().sq_norm_out(c.cfg(y.dtype, o.dtype, kind, act, eps, res_scale, 1.0), *args, handle), "sq_norm_out")
+
+
+def sq_norm_out_bwd(y, do, dy, weight=None, z=None, dz=None, act=SQ_ACT_SILU, chan_scale=None, res_scale=1.0,
+                    dweight=None, dchan_scale=None, eps=1e-6, kind=SQ_NORM_RMS, workspace=None, stream=None):
+    """Gradients of sq_norm_out from y, z and do: dy and, if given, dz, dweight, dchan_scale (that of x is do)."""
+    c = _NormCall(y, "y")
+    args = [c.rows(y, y.dtype, "y"), c.rows(z, do.dtype, "z"), c.rows(do, do.dtype, "do"), c.vec(weight, "weight"),
+            c.vec(chan_scale, "chan_scale"), c.rows(dy, y.dtype, "dy"), c.rows(dz, do.dtype, "dz"),
+            c.vec(dweight, "dweight"), c.vec(dchan_scale, "dchan_scale")]
+    with _launch_on(c.device, stream) as handle:
+        work, nbytes, keep = c.work(workspace, stream, dweight is not None or dchan_scale is not None)
+        _check(_lib.load().sq_norm_out_bwd(c.cfg(y.dtype, do.dtype, kind, act, eps, res_scale, 1.0), *args, work, nbytes,
+                                           handle), "sq_norm_out_bwd")
+        del keep

@@ -4,7 +4,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from ctypes import POINTER, c_double, c_float, c_int32, c_size_t, c_uint32, c_uint64, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libstepq.so")
@@ -16,6 +16,9 @@ SQ_UNIT_HEAD, SQ_UNIT_ROW = 0, 1
 SQ_QUANT_DUAL_AXIS, SQ_QUANT_ROW_ABSMAX = 0, 1
 SQ_STEP_SPLIT, SQ_STEP_VALIDATE, SQ_STEP_NO_JOIN = 1, 2, 4
 SQ_PIVOT_BITS = 16
+SQ_DTYPE_F32, SQ_DTYPE_BF16, SQ_DTYPE_F16 = 0, 1, 2
+SQ_NORM_RMS, SQ_NORM_L2 = 0, 1
+SQ_ACT_SILU, SQ_ACT_SIGMOID = 0, 1
 SQ_MAX_WIDTHS, SQ_MAX_GRID = 8, 8
 SQ_SPLIT_STATIC_MAX_FLOATS = 8 << 20
 
@@ -48,7 +51,22 @@ class SqPlanDesc(ctypes.Structure):
     ]
 
 
+class SqRows(ctypes.Structure):
+    _fields_ = [("d_ptr", c_void_p), ("stride", c_int64)]
+
+
+class SqScanCfg(ctypes.Structure):
+    _fields_ = [("form", c_int32), ("dtype", c_int32), ("n_heads", c_int32), ("n_heads_k", c_int32), ("d_k", c_int32),
+                ("d_v", c_int32), ("n_seq", c_int32), ("n_tokens", c_int64), ("d_seq_start", c_void_p)]
+
+
+class SqNormCfg(ctypes.Structure):
+    _fields_ = [("dtype", c_int32), ("dtype_out", c_int32), ("kind", c_int32), ("act", c_int32), ("n_outer", c_int64),
+                ("n_inner", c_int32), ("d", c_int32), ("eps", c_float), ("res_scale", c_float), ("out_scale", c_float)]
+
+
 _P = c_void_p
+_R = POINTER(SqRows)
 _SIGS = {
     "sq_plan_create": (c_int32, [POINTER(SqPlanCfg), POINTER(c_void_p)]),
     "sq_plan_destroy": (None, [_P]),
@@ -77,6 +95,14 @@ _SIGS = {
                                _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "sq_copy": (c_int32, [_P, _P, c_size_t, _P]),
     "sq_valu_probe": (c_int32, [c_int32, c_int32, _P, _P, _P, _P]),
+    "sq_delta_scan_bytes": (c_int32, [POINTER(SqScanCfg), c_int32, POINTER(c_size_t)]),
+    "sq_delta_scan": (c_int32, [POINTER(SqScanCfg), _R, _R, _R, _P, _P, _P, _R, _P, _P, c_size_t, _P]),
+    "sq_delta_scan_bwd": (c_int32, [POINTER(SqScanCfg), _R, _R, _R, _P, _P, _P, _R, _P, _R, _R, _R, _P, _P, _P, _P, c_size_t, _P]),
+    "sq_norm_bytes": (c_int32, [c_int64, c_int32, POINTER(c_size_t)]),
+    "sq_norm_in": (c_int32, [POINTER(SqNormCfg), _R, _R, _P, _P, _R, _R, _P]),
+    "sq_norm_in_bwd": (c_int32, [POINTER(SqNormCfg), _R, _R, _R, _R, _P, _P, _R, _R, _P, _P, _P, c_size_t, _P]),
+    "sq_norm_out": (c_int32, [POINTER(SqNormCfg), _R, _R, _R, _P, _P, _R, _P]),
+    "sq_norm_out_bwd": (c_int32, [POINTER(SqNormCfg), _R, _R, _R, _P, _P, _R, _R, _P, _P, _P, c_size_t, _P]),
     "sq_status_str": (ctypes.c_char_p, [c_int32]),
     "sq_last_error": (ctypes.c_char_p, []),
     "sq_supported_shapes": (c_int32, [POINTER(c_int32), c_int32]),

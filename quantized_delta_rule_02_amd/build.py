@@ -16,7 +16,7 @@ OUT = os.path.join(HERE, "libstepq.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 ARCH = os.environ.get("STEPQ_ARCH", "gfx950")
 
-SOURCES = ["api.cpp", "planner.cpp", "kernels.hip", "probe.hip"]
+SOURCES = ["api.cpp", "ops_api.cpp", "planner.cpp", "kernels.hip", "probe.hip", "norm.hip", "scan.hip", "scan_bwd.hip"]
 
 
 def _hipcc() -> str:
@@ -34,14 +34,16 @@ def build(verbose: bool = False) -> str:
     # packed FP32 (v_pk_*_f32) is disabled for all device code
     # IEEE mode off: no NaN arises on the step's path, and without it fmaxf/fminf compile to one
     # v_max/v_min instead of being preceded by canonicalizing copies of their operands
-    device = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-              "-munsafe-fp-atomics", "-mno-amdgpu-ieee", "-fno-honor-nans"]
+    device = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+    step = ["-munsafe-fp-atomics", "-mno-amdgpu-ieee", "-fno-honor-nans"]
+    # the norms and the scan let NaN and infinities through
+    ieee = {"norm.hip", "scan.hip", "scan_bwd.hip"}
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD_DIR, src.replace(".", "_") + ".o")
         path = os.path.join(CSRC, src)
         if src.endswith(".hip"):
-            cmd = [hipcc, "-x", "hip"] + common + device + ["-c", path, "-o", obj]
+            cmd = [hipcc, "-x", "hip"] + common + device + ([] if src in ieee else step) + ["-c", path, "-o", obj]
         else:
             cmd = [hipcc] + common + ["-pthread", "-c", path, "-o", obj]
         res = subprocess.run(cmd, capture_output=True, text=True)

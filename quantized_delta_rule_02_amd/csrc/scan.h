@@ -1,0 +1,56 @@
+// Launchers of the gated delta scan (scan.hip, scan_bwd.hip), called by the C ABI (ops_api.cpp).
+//
+// Workspace of a call, per chunk slot and head (chunks of 32 tokens, counted from each sequence's start):
+// chunk c of sequence b has the slot (start_b >> 5) + b + c.  Slots of different chunks differ, because
+// ceil(len / 32) <= ((start + len) >> 5) - (start >> 5) + 1, and all lie below (n_tokens >> 5) + n_seq.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace sq {
+
+constexpr int kChunk = 32;
+// One 32 x 32 matrix as MFMA A operands: 2 row tiles x 3 bfloat16 planes x 64 lanes x 8 elements.
+constexpr int kMatShorts = 2 * 3 * 64 * 8;
+
+struct ScanRows {
+    void* p;
+    int64_t stride;                  // elements between tokens
+};
+
+struct ScanParams {
+    int32_t form, dtype, n_heads, n_heads_k, dk, dv, n_seq;
+    int64_t n_tokens, n_slots;
+    const int32_t* seq_start;        // [n_seq + 1], or NULL: one sequence of n_tokens
+    ScanRows q, k, v, y;
+    const float* gate;               // [n_tokens][H] or [n_tokens][H][dk]
+    const float* beta;               // [n_tokens][H]
+    const float* s0;                 // [n_seq][H][dk][dv] or NULL
+    float* s1;                       // or NULL
+    // workspace
+    uint16_t* mat_th;                // [slot][H] That = (I + A diag(beta))^-1
+    uint16_t* mat_p;                 // [slot][H] P (forward)
+    // backward
+    uint16_t* mat_tt;                // [slot][H] T^T, T = (I + diag(beta) A)^-1
+    uint16_t* mat_pt;                // [slot][H] P^T
+    float* mat_ap;                   // [slot][H][2][32][32] A and P in float32 (GDN)
+    float* e;                        // [n_tokens][H][dv]
+    float* du;                       // [n_tokens][H][dv]
+    float* st;                       // [slot][H][dk][dv] state before each chunk
+    float* gt;                       // [slot][H][dk][dv] gradient of the state after each chunk
+    ScanRows dy, dq, dkk, dvv;
+    const float* ds1;
+    float* ds0;
+    float* dgate;
+    float* dbeta;
+};
+
+inline int64_t scan_slots(int64_t n_tokens, int n_seq) { return (n_tokens / kChunk) + n_seq; }
+
+// prep: the chunks' small matrices; forward: the scan (keep = also the states and e that the backward pass reads).
+hipError_t launch_scan_prep(const ScanParams& p, bool backward, hipStream_t s);
+hipError_t launch_scan_fwd(const ScanParams& p, bool keep, hipStream_t s);
+hipError_t launch_scan_rev(const ScanParams& p, hipStream_t s);
+hipError_t launch_scan_grad(const ScanParams& p, hipStream_t s);
+
+}  // namespace sq

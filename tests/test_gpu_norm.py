@@ -1,0 +1,223 @@
+"""The norms before and after a block, and their gradients, on the GPU against float64.
+
+Tolerance.  A row's sum of d squares in float32 has at most (d / threads + log2 threads + 8) * 2^-24 relative error, below
+1e-5 for every width here (d <= 16384 over 256 threads: 64 + 8 + 8 roundings, 5e-6); gradients hold two such sums.  The sums
+over rows are those of at most a few thousand float32 terms per thread and 1024 partial sums: 1e-5 of the sum of the
+terms' magnitudes.  An output in t adds half a step, torch.finfo(t).eps / 2 of its value.
+"""
+import pytest
+import torch
+
+import quantized_delta_rule_02_amd as sq
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+TOL = 1e-5
+
+
+def near(got, ref, what, size=None):
+    """`size`: the magnitude the float32 error goes by (the terms of a sum, a gradient's parts); the value's own if not given."""
+    t = got.dtype
+    got, ref = got.double(), ref.double()
+    assert got.shape == ref.shape and torch.isfinite(got).all(), what
+    half = 0.0 if t == F32 else torch.finfo(t).eps / 2
+    tiny = 2.0 ** -25 if t == F16 else 0.0              # half a step of float16's subnormal numbers
+    off = (got - ref).abs() - half * ref.abs() - tiny - TOL * (ref.abs() if size is None else size)
+    assert not ref.numel() or off.max() <= 0, f"{what}: off by {(got - ref).abs().max():.3e}"
+
+
+def hat(x, kind, eps):
+    s = x.square().mean(-1, keepdim=True) if kind == sq.SQ_NORM_RMS else x.square().sum(-1, keepdim=True)
+    return x / (s + eps).sqrt()
+
+
+def rows(shape, dtype, dev, seed, scale=1.0):
+    return (scale * torch.randn(shape, generator=torch.Generator().manual_seed(seed))).to(dtype).to(dev)
+
+
+# shape, type of the rows, type of the other side
+SHAPES = [((1, 1), F32, F32), ((5, 3), F32, BF16), ((4, 2, 16), BF16, F32), ((7, 3, 64), F16, F16), ((33, 4, 128), BF16, BF16),
+          ((2, 5, 128), F32, BF16), ((9, 1000), BF16, BF16), ((3, 257), F32, F32), ((6, 520), F16, F32), ((70, 2048), BF16, BF16),
+          ((3, 2049), BF16, F32), ((5, 4096), F32, F32), ((2, 8192), BF16, BF16), ((2, 16384), F16, BF16), ((1, 16383), F32, F32),
+          ((300, 8), BF16, F32), ((1500, 2, 24), F32, F16)]
+
+
+@pytest.mark.parametrize("shape,dt,do", SHAPES, ids=lambda v: str(v).replace("torch.", "").replace(" ", ""))
+@pytest.mark.parametrize("kind", (0, 1), ids=("rms", "l2"))
+@pytest.mark.parametrize("full", (True, False), ids=("all", "bare"))
+def test_norm_in(shape, dt, do, kind, full, dev):
+    d, eps, rs, os_ = shape[-1], 1e-5, 0.7, 0.5
+    x, r = rows(shape, dt, dev, 1), rows(shape, dt, dev, 2, 3.0) if full else None
+    w, c = (1 + 0.1 * rows((d,), F32, dev, 3), 1 + 0.1 * rows((d,), F32, dev, 4)) if full else (None, None)
+    n, h = torch.empty(shape, dtype=do, device=dev), torch.empty_like(x) if full else None
+    sq.sq_norm_in(x, n, weight=w, r=r, h=h, chan_scale=c, res_scale=rs, kind=kind, eps=eps, out_scale=os_)
+    h64 = x.double() + rs * c.double() * r.double() if full else x.double()
+    n64 = os_ * hat(h64, kind, eps) * (w.double() if full else 1.0)
+    size = x.double().abs() + r.double().abs() * 2 if full else h64.abs()
+    near(n, n64, "n", n64.abs() + size / h64.square().sum(-1, keepdim=True).sqrt().clamp(min=eps) * n64.norm(dim=-1, keepdim=True))
+    if full:
+        near(h, h64, "h", size)
+    # gradients, from the stored h
+    hh = h if full else x
+    dn, dh = rows(shape, do, dev, 5), rows(shape, dt, dev, 6) if full else None
+    dx, dr = torch.empty_like(hh), torch.empty_like(hh) if full else None
+    dw, dc = torch.empty(d, device=dev), torch.empty(d, device=dev) if full else None
+    sq.sq_norm_in_bwd(hh, dn, dx, weight=w, r=r, dh=dh, dr=dr, chan_scale=c, res_scale=rs, dweight=dw, dchan_scale=dc,
+                      kind=kind, eps=eps, out_scale=os_)
+    g = hh.double().requires_grad_()
+    w64 = (w.double() if full else torch.ones(d, dtype=torch.float64, device=dev)).requires_grad_()
+    out = os_ * hat(g, kind, eps) * w64
+    gx, gw = torch.autograd.grad(out, (g, w64), dn.double())
+    inv = (hat(hh.double(), kind, eps).norm(dim=-1, keepdim=True) / hh.double().norm(dim=-1, keepdim=True))
+    part = os_ * inv * (dn.double() * w64).detach().abs()
+    # the two parts of the derivative: the incoming gradient, and the row times their product
+    size = part + part.norm(dim=-1, keepdim=True) * (hh.double().abs() / hh.double().norm(dim=-1, keepdim=True))
+    if full:
+        gx, size = gx + dh.double(), size + dh.double().abs()
+        near(dr, rs * c.double() * gx, "dr", size)
+        terms = rs * gx * r.double()
+        near(dc, terms.flatten(0, -2).sum(0), "dchan_scale", (rs * size * r.double()).abs().flatten(0, -2).sum(0))
+    near(dx, gx, "dx", size)
+    near(dw, gw.detach(), "dweight", (os_ * dn.double() * hat(hh.double(), kind, eps)).abs().flatten(0, -2).sum(0))
+
+
+@pytest.mark.parametrize("shape,dt,do", SHAPES, ids=lambda v: str(v).replace("torch.", "").replace(" ", ""))
+@pytest.mark.parametrize("act", (0, 1, None), ids=("silu", "sigmoid", "none"))
+def test_norm_out(shape, dt, do, act, dev):
+    d, eps, rs = shape[-1], 1e-5, 1.3
+    full = act is not None
+    y, z = rows(shape, dt, dev, 1), rows(shape, do, dev, 2, 4.0) if full else None
+    x = rows(shape, do, dev, 3) if full else None
+    w, c = (1 + 0.1 * rows((d,), F32, dev, 4), 1 + 0.1 * rows((d,), F32, dev, 5)) if full else (None, None)
+    o = torch.empty(shape, dtype=do, device=dev)
+    kw = dict(weight=w, z=z, act=act or 0, chan_scale=c, res_scale=rs, eps=eps)
+    sq.sq_norm_out(y, o, x=x, **kw)
+    y64 = y.double().requires_grad_()
+    z64 = z.double().requires_grad_() if full else None
+    w64 = (w.double() if full else torch.ones(d, dtype=torch.float64, device=dev)).requires_grad_()
+    c64 = (c.double() if full else torch.ones(d, dtype=torch.float64, device=dev)).requires_grad_()
+    g = 1.0 if not full else z64 * z64.sigmoid() if act == 0 else z64.sigmoid()
+    block = rs * c64 * w64 * hat(y64, 0, eps) * g
+    near(o, (block + x.double() if full else block).detach(), "o", block.detach().abs() + (x.double().abs() if full else 0))
+    do_ = rows(shape, do, dev, 6)
+    dy, dz = torch.empty_like(y), torch.empty_like(o) if full else None
+    dw, dc = torch.empty(d, device=dev), torch.empty(d, device=dev)
+    sq.sq_norm_out_bwd(y, do_, dy, dz=dz, dweight=dw, dchan_scale=dc, **kw)
+    got = torch.autograd.grad(block, (y64, w64, c64) + ((z64,) if full else ()), do_.double())
+    yd = y.double()
+    inv = hat(yd, 0, eps).norm(dim=-1, keepdim=True) / yd.norm(dim=-1, keepdim=True)
+    part = inv * (rs * do_.double() * c64 * w64 * g).detach().abs()
+    near(dy, got[0], "dy", part + part.norm(dim=-1, keepdim=True) * yd.abs() / yd.norm(dim=-1, keepdim=True))
+    terms = (do_.double() * block).detach().abs().flatten(0, -2).sum(0)
+    near(dw, got[1], "dweight", terms / w64.detach().abs())
+    near(dc, got[2], "dchan_scale", terms / c64.detach().abs())
+    if full:
+        zd = z.double()
+        s = zd.sigmoid()
+        dact = s * (1 + zd.abs() * (1 - s)) if act == 0 else s
+        near(dz, got[3], "dz", (rs * do_.double() * c64 * w64 * hat(yd, 0, eps)).detach().abs() * dact)
+
+
+@pytest.mark.parametrize("d", (40, 37), ids=("vector", "scalar"))
+def test_strides_offsets_and_untouched_neighbours(d, dev):
+    """Heads of a wider array, odd starts, output written between bytes that must stay."""
+    T, H = 11, 3
+    wide = rows((T, 2 * H * d + 9), BF16, dev, 1)
+    x = wide[:, 1:1 + H * d].unflatten(1, (H, d))
+    out = torch.full((T, H * d + 16), 7.0, device=dev)
+    n = out[:, 8:8 + H * d].unflatten(1, (H, d))
+    sq.sq_norm_in(x, n, kind=sq.SQ_NORM_L2)
+    near(n, hat(x.double(), 1, 1e-6), "n")
+    assert (out[:, :8] == 7).all() and (out[:, 8 + H * d:] == 7).all()
+    dx_wide = torch.full_like(wide, 7.0)
+    dx = dx_wide[:, 1:1 + H * d].unflatten(1, (H, d))
+    dw = torch.empty(d, device=dev)
+    sq.sq_norm_in_bwd(x, n, dx, dweight=dw, kind=sq.SQ_NORM_L2)
+    assert (dx_wide[:, :1] == 7).all() and (dx_wide[:, 1 + H * d:] == 7).all()
+    near(dw, (n.double() * hat(x.double(), 1, 1e-6)).sum((0, 1)), "dweight")
+
+
+def test_in_place(dev):
+    """n over x and h over r (same type and stride) give what separate arrays give."""
+    x, r = rows((40, 512), BF16, dev, 1), rows((40, 512), BF16, dev, 2)
+    n, h = torch.empty_like(x), torch.empty_like(x)
+    sq.sq_norm_in(x, n, r=r, h=h, res_scale=0.5)
+    sq.sq_norm_in(x, x, r=r, h=r, res_scale=0.5)
+    assert torch.equal(n, x) and torch.equal(h, r)
+    y, z = rows((40, 512), BF16, dev, 3), rows((40, 512), BF16, dev, 4)
+    o = torch.empty_like(y)
+    sq.sq_norm_out(y, o, z=z, x=x)
+    sq.sq_norm_out(y, x, z=z, x=x)
+    assert torch.equal(o, x)
+
+
+def test_rows_of_zero_and_extreme_gates(dev):
+    """A zero row: 0 / sqrt(eps); gates of +-100 and a row that holds NaN leave the other rows as they are."""
+    y = rows((4, 128), F32, dev, 1)
+    y[1] = 0
+    z = rows((4, 128), F32, dev, 2)
+    z[0, :64], z[0, 64:] = 100.0, -100.0
+    y[3, 5] = float("nan")
+    o, dy, dz, do = (torch.zeros_like(y) for _ in range(4))
+    do.fill_(1.0)
+    sq.sq_norm_out(y, o, z=z)
+    sq.sq_norm_out_bwd(y, do, dy, z=z, dz=dz)
+    assert not o[1].any() and torch.isfinite(o[:3]).all() and torch.isnan(o[3]).all()
+    assert torch.isfinite(dy[:3]).all() and torch.isfinite(dz[:3]).all() and not o[0, 64:].abs().gt(1e-30).any()
+    near(o[0, :64], 100 * hat(y[0].double(), 0, 1e-6)[:64], "open gate")
+
+
+def test_no_rows(dev):
+    e = torch.empty(0, 64, device=dev)
+    dw = torch.full((64,), 5.0, device=dev)
+    sq.sq_norm_in(e, e)
+    sq.sq_norm_in_bwd(e, e, e, dweight=dw)
+    assert not dw.any()
+    sq.sq_norm_out(e, e)
+
+
+def test_captured_and_other_stream(dev):
+    """Captured gradients (partial sums in a caller's workspace), replayed with other inputs; a call on a side stream."""
+    h, dn = rows((3000, 128), BF16, dev, 1), rows((3000, 128), BF16, dev, 2)
+    dx, dw = torch.empty_like(h), torch.empty(128, device=dev)
+    work = torch.empty(sq.sq_norm_bytes(3000, 128), dtype=torch.uint8, device=dev)
+    call = lambda: sq.sq_norm_in_bwd(h, dn, dx, dweight=dw, workspace=work)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    side = torch.cuda.Stream()
+    for i in range(3):
+        h.copy_(rows((3000, 128), BF16, dev, 10 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        ex, ew = torch.empty_like(h), torch.empty(128, device=dev)
+        torch.cuda.synchronize()
+        sq.sq_norm_in_bwd(h, dn, ex, dweight=ew, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(dx, ex) and torch.equal(dw, ew)
+
+
+def test_gradients_against_differences(dev):
+    """Central differences of the forward calls along random directions."""
+    y, z, do = rows((6, 96), F32, dev, 1), rows((6, 96), F32, dev, 2), rows((6, 96), F32, dev, 3)
+    dy, dz = torch.empty_like(y), torch.empty_like(z)
+    sq.sq_norm_out_bwd(y, do, dy, z=z, dz=dz)
+
+    def loss(a, b):
+        o = torch.empty_like(a)
+        sq.sq_norm_out(a, o, z=b)
+        return (o.double() * do.double()).sum().item()
+
+    step = 1e-2
+    for i, g in enumerate((dy, dz)):
+        u = rows((6, 96), F32, dev, 20 + i)
+        u = u / u.norm()
+        hi, lo = [y, z], [y, z]
+        hi[i], lo[i] = hi[i] + step * u, lo[i] - step * u
+        num = (loss(*hi) - loss(*lo)) / (2 * step)
+        ana = (g.double() * (hi[i].double() - lo[i].double())).sum().item() / (2 * step)
+        # float32 outputs: 2^-24 of each of 576 terms of the losses; the third derivative: step^2 of the gradient's size
+        assert abs(num - ana) <= 2e-6 * do.norm().item() * y.norm().item() / step * 0.1 + 4 * step ** 2 * g.norm().item()

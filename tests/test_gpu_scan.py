@@ -1,0 +1,337 @@
+"""The gated delta scan and its gradients on the GPU against float64 references, token by token.
+
+Tolerance.  Products split every float32 operand exactly into three bfloat16 parts (8 bits each, truncated) and leave
+out the terms below 2 * 2^-7 * 2^-15 = 2^-21 of |a||b|; float32 accumulation adds some 2^-24 per term.  A result passes
+through at most five such products within a chunk (state, That, P, update; one more for gradients), and the states hand
+errors on, damped by the gates: 5 * 2^-21 = 2.4e-6 of the operands' size, with a factor 4 for terms that cancel:
+1e-5 of an output's largest value.  An output in t adds half a step: torch.finfo(t).eps / 2 of its value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import quantized_delta_rule_02_amd as sq
+from _ops_ref import scan_grad_ref, scan_inputs, scan_ref
+
+pytestmark = pytest.mark.gpu
+
+TOL = 1e-5
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+GRADS = ("dq", "dk", "dv", "dgate", "dbeta", "ds0")
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def starts(lens, dev, lead=0):
+    return torch.tensor(np.concatenate([[lead], lead + np.cumsum(lens)]), dtype=torch.int32, device=dev)
+
+
+def near(got, ref, what, tol=TOL):
+    t = got.dtype
+    got, ref = got.double().cpu(), ref.double()
+    assert got.shape == ref.shape, what
+    assert torch.isfinite(got).all(), what
+    if not ref.numel():
+        return
+    half = 0.0 if t == F32 else torch.finfo(t).eps / 2
+    off = (got - ref).abs() - half * ref.abs() - tol * ref.abs().max()
+    assert off.max() <= 0, f"{what}: off by {(got - ref).abs().max():.3e}, largest {ref.abs().max():.3e}"
+
+
+def forward(form, x, lens, dev, s0=True, **kw):
+    d = {n: t.to(dev) for n, t in x.items()}
+    y, s1 = torch.zeros_like(d["v"]), torch.zeros_like(d["s0"])
+    sq.sq_delta_scan(form, d["q"], d["k"], d["v"], d["gate"], d["beta"], y, seq_start=starts(lens, dev),
+                     s0=d["s0"] if s0 else None, s1=s1, **kw)
+    return y, s1
+
+
+def backward(form, x, lens, dev, s0=True, ds1=True, **kw):
+    d = {n: t.to(dev) for n, t in x.items()}
+    g = {"d" + n: torch.zeros_like(d[n]) for n in ("q", "k", "v", "gate", "beta", "s0")}
+    sq.sq_delta_scan_bwd(form, d["q"], d["k"], d["v"], d["gate"], d["beta"], d["dy"], g["dq"], g["dk"], g["dv"],
+                         g["dgate"], g["dbeta"], seq_start=starts(lens, dev), s0=d["s0"] if s0 else None,
+                         ds1=d["ds1"] if ds1 else None, ds0=g["ds0"], **kw)
+    return g
+
+
+# form, dtype, heads, q/k heads, d_k, d_v, lengths, gates
+CASES = [
+    (0, F32, 2, 2, 16, 16, [5], "usual"),
+    (0, F32, 2, 1, 16, 16, [1, 0, 33], "strong"),
+    (1, F32, 2, 2, 16, 16, [40, 1], "usual"),
+    (0, F32, 2, 1, 64, 64, [1, 16, 0, 70], "usual"),
+    (1, F32, 2, 2, 64, 64, [31, 32, 33], "strong"),
+    (0, BF16, 4, 2, 128, 128, [65, 1, 97], "usual"),
+    (0, F16, 2, 2, 128, 128, [17, 64], "resets"),
+    (0, F32, 3, 1, 128, 128, [50, 15], "resets"),
+    (1, BF16, 4, 2, 128, 128, [65, 0, 30], "usual"),
+    (1, F16, 2, 1, 128, 128, [33], "resets"),
+    (1, F32, 1, 1, 128, 256, [47], "usual"),
+    (0, BF16, 2, 1, 128, 256, [64, 2], "one"),
+    (1, BF16, 2, 2, 64, 64, [96], "one"),
+]
+IDS = [f"{'kda' if c[0] else 'gdn'}-{str(c[1])[6:]}-{c[2]}h{c[3]}-{c[4]}x{c[5]}-{'_'.join(map(str, c[6]))}-{c[7]}" for c in CASES]
+
+
+@pytest.mark.parametrize("c", CASES, ids=IDS)
+def test_forward(c, dev):
+    form, dt, H, Hk, dk, dv, lens, gate = c
+    say("scan", c)
+    x = scan_inputs(form, H, Hk, dk, dv, lens, 11, dt, gate)
+    for s0 in (True, False):
+        y, s1 = forward(form, x, lens, dev, s0)
+        yr, sr = scan_ref(x, lens, s0)
+        near(y, yr, "y")
+        near(s1, sr, "s1")
+
+
+@pytest.mark.parametrize("c", CASES, ids=IDS)
+def test_backward(c, dev):
+    form, dt, H, Hk, dk, dv, lens, gate = c
+    say("scan bwd", c)
+    x = scan_inputs(form, H, Hk, dk, dv, lens, 23, dt, gate)
+    for states in (True, False):
+        g = backward(form, x, lens, dev, states, states)
+        r = scan_grad_ref(x, lens, states, states)
+        for n in GRADS:
+            if n == "ds0" and not states:
+                continue                    # the reference has no first state to differentiate by
+            near(g[n], r[n], n)
+
+
+@pytest.mark.parametrize("form", (0, 1), ids=("gdn", "kda"))
+def test_equal_keys_and_extreme_beta(form, dev):
+    """One key for all tokens, no decay, beta 1 or 0: (I + A)^-1 has rows that sum large terms; beta = 0 divides nowhere."""
+    lens, H, dk, dv = [64, 7], 2, 64, 64
+    x = scan_inputs(form, H, H, dk, dv, lens, 5, F32, "one")
+    x["k"] = x["k"][:1].expand_as(x["k"]).contiguous()
+    x["beta"] = torch.ones_like(x["beta"])
+    x["beta"][3::5] = 0.0
+    y, s1 = forward(form, x, lens, dev)
+    yr, sr = scan_ref(x, lens)
+    near(y, yr, "y")
+    near(s1, sr, "s1")
+    g, r = backward(form, x, lens, dev), scan_grad_ref(x, lens)
+    for n in GRADS:
+        near(g[n], r[n], n)
+    x["beta"].zero_()
+    g, r = backward(form, x, lens, dev), scan_grad_ref(x, lens)
+    for n in GRADS:
+        near(g[n], r[n], n)
+    assert not g["dv"].any()
+
+
+@pytest.mark.parametrize("form", (0, 1), ids=("gdn", "kda"))
+def test_gates_of_zero(form, dev):
+    """A zero gate forgets the state; its gradient stays that of the formula (no quotient by it)."""
+    lens, H, dk, dv = [70], 2, 64, 64
+    x = scan_inputs(form, H, H, dk, dv, lens, 8, F32, "usual")
+    x["gate"][::9] = 0.0
+    x["gate"][40] = 1e-38
+    y, s1 = forward(form, x, lens, dev)
+    yr, sr = scan_ref(x, lens)
+    near(y, yr, "y")
+    near(s1, sr, "s1")
+    g, r = backward(form, x, lens, dev), scan_grad_ref(x, lens)
+    for n in GRADS:
+        near(g[n], r[n], n)
+    near(g["dgate"][::9], r["dgate"][::9], "dgate of the zero gates")
+
+
+def test_gradients_against_differences(dev):
+    """Central differences of the forward call itself, along random directions of each input, in float32."""
+    form, lens, H, dk, dv = 1, [45, 3], 2, 64, 64
+    x = scan_inputs(form, H, 1, dk, dv, lens, 31, F32)
+    g = backward(form, x, lens, dev)
+
+    def loss(z):
+        y, s1 = forward(form, z, lens, dev)
+        return ((y.double().cpu() * x["dy"].double()).sum() + (s1.double().cpu() * x["ds1"].double()).sum()).item()
+
+    step = 1e-2
+    for i, n in enumerate(("q", "k", "v", "gate", "beta", "s0")):
+        d = torch.randn(x[n].shape, generator=torch.Generator().manual_seed(50 + i))
+        d = (d / d.norm()).float() * (0.05 if n == "gate" else 1.0)
+        hi, lo = dict(x), dict(x)
+        hi[n], lo[n] = x[n] + step * d, x[n] - step * d
+        d64 = (hi[n].double() - lo[n].double()) / (2 * step)
+        num = (loss(hi) - loss(lo)) / (2 * step)
+        ana = (g["d" + n].double().cpu() * d64).sum().item()
+        scale = g["d" + n].double().norm().item() * d64.norm().item()
+        # float32 losses of size |loss| carry 1e-5 |loss| / step; the third derivative adds step^2 of the gradient's size
+        assert abs(num - ana) <= 1e-5 * abs(loss(x)) / step + 4 * step ** 2 * scale + 1e-5 * scale, (n, num, ana, scale)
+
+
+def test_cut_sequence_equals_whole(dev):
+    """A sequence in pieces of odd lengths, states handed on in place, gives the whole sequence's outputs."""
+    form, H, dk, dv, T = 0, 4, 128, 128, 150
+    x = scan_inputs(form, H, 2, dk, dv, [T], 3, BF16)
+    d = {n: t.to(dev) for n, t in x.items()}
+    yr, sr = scan_ref(x, [T])
+    st, y, t0 = d["s0"].clone(), torch.zeros_like(d["v"]), 0
+    for n in (1, 40, 32, 0, 70, 7):
+        s = slice(t0, t0 + n)
+        sq.sq_delta_scan(form, d["q"][s], d["k"][s], d["v"][s], d["gate"][s], d["beta"][s], y[s], s0=st, s1=st)
+        t0 += n
+    near(y, yr, "y")
+    near(st, sr, "s1")
+
+
+def test_one_token_is_the_decode_step(dev):
+    """One token per request is what sq_fp32_step computes (float32 inputs, same state)."""
+    H, dk, dv, B = 4, 128, 128, 9
+    x = scan_inputs(1, H, H, dk, dv, [1] * B, 17, F32)
+    d = {n: t.to(dev) for n, t in x.items()}
+    y, s1 = forward(1, x, [1] * B, dev)
+    S, y2 = d["s0"].clone(), torch.zeros(B * H * dv, device=dev)
+    slots = torch.arange(B, dtype=torch.int32, device=dev)
+    sq.sq_fp32_step(1, H, dk, dv, B, 0, 1, B, slots, S, d["q"], d["k"], d["v"], d["gate"], d["beta"], y2)
+    near(y.view(-1), y2.cpu(), "y")
+    near(s1, S.cpu(), "state")
+
+
+def test_parts_of_wider_arrays_and_rows_outside(dev):
+    """q, k, v, y and their gradients as parts of wider arrays; tokens before, between and behind stay untouched."""
+    form, H, Hk, dk, dv, lens = 0, 4, 2, 128, 128, [33, 20]
+    lead, tail = 3, 5
+    x = scan_inputs(form, H, Hk, dk, dv, lens, 41, BF16)
+    T = sum(lens)
+    N = lead + T + tail
+    wide = torch.full((N, 2 * Hk * dk + H * dv + 8), float("nan"), dtype=BF16, device=dev)
+    part = lambda a, at, h, w: a[:, at:at + h * w].unflatten(1, (h, w))  # noqa: E731
+    cut = lambda a: (part(a, 0, Hk, dk), part(a, Hk * dk, Hk, dk), part(a, 2 * Hk * dk, H, dv))  # noqa: E731
+    for a, n in zip(cut(wide), ("q", "k", "v")):
+        a[lead:lead + T] = x[n].to(dev)
+    pad = lambda t: torch.cat([torch.full((lead, *t.shape[1:]), float("nan")), t.float(),  # noqa: E731
+                               torch.full((tail, *t.shape[1:]), float("nan"))]).to(dev)
+    gate, beta = pad(x["gate"]), pad(x["beta"])
+    out = torch.full((N, H * dv + 8), 7.0, dtype=BF16, device=dev)
+    y, s1 = part(out, 0, H, dv), torch.zeros(2, H, dk, dv, device=dev)
+    q, k, v = cut(wide)
+    sq.sq_delta_scan(form, q, k, v, gate, beta, y, seq_start=starts(lens, dev, lead), s0=x["s0"].to(dev), s1=s1)
+    yr, sr = scan_ref(x, lens)
+    near(y[lead:lead + T], yr, "y")
+    near(s1, sr, "s1")
+    assert (out[:lead] == 7).all() and (out[lead + T:] == 7).all() and (out[:, H * dv:] == 7).all()
+    gw = torch.full_like(wide, 7.0)
+    dq, dk_, dv_ = cut(gw)
+    dgate, dbeta = torch.full_like(gate, 7.0), torch.full_like(beta, 7.0)
+    dy = pad(x["dy"]).to(BF16)
+    sq.sq_delta_scan_bwd(form, q, k, v, gate, beta, dy, dq, dk_, dv_, dgate, dbeta, seq_start=starts(lens, dev, lead),
+                         s0=x["s0"].to(dev))
+    r = scan_grad_ref(x, lens, True, False)
+    for n, t in (("dq", dq), ("dk", dk_), ("dv", dv_), ("dgate", dgate), ("dbeta", dbeta)):
+        near(t[lead:lead + T], r[n], n)
+        assert (t[:lead] == 7).all() and (t[lead + T:] == 7).all(), n
+    assert (gw[:, -8:] == 7).all()
+
+
+def test_empty_sequences_only(dev):
+    s0 = torch.randn(3, 2, 64, 64, device=dev)
+    e = lambda *s: torch.zeros(*s, device=dev)  # noqa: E731
+    s1 = e(3, 2, 64, 64)
+    sq.sq_delta_scan(0, e(0, 2, 64), e(0, 2, 64), e(0, 2, 64), e(0, 2), e(0, 2), e(0, 2, 64),
+                     seq_start=starts([0, 0, 0], dev), s0=s0, s1=s1)
+    assert torch.equal(s0, s1)
+    ds0 = e(3, 2, 64, 64)
+    sq.sq_delta_scan_bwd(0, e(0, 2, 64), e(0, 2, 64), e(0, 2, 64), e(0, 2), e(0, 2), e(0, 2, 64), e(0, 2, 64), e(0, 2, 64),
+                         e(0, 2, 64), e(0, 2), e(0, 2), seq_start=starts([0, 0, 0], dev), ds1=s0, ds0=ds0)
+    assert torch.equal(s0, ds0)
+    sq.sq_delta_scan(0, e(0, 2, 64), e(0, 2, 64), e(0, 2, 64), e(0, 2), e(0, 2), e(0, 2, 64), seq_start=starts([], dev))
+
+
+def test_runs_are_bitwise_equal_and_streams_are_kept(dev):
+    """Repeated calls, one on another stream with its own workspace, give the same bits."""
+    form, H, dk, dv, lens = 1, 4, 128, 128, [90, 33]
+    x = scan_inputs(form, H, 2, dk, dv, lens, 77, BF16)
+    a = (*forward(form, x, lens, dev), *backward(form, x, lens, dev).values())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    d = {n: t.to(dev) for n, t in x.items()}
+    torch.cuda.synchronize()
+    y, s1 = torch.zeros_like(d["v"]), torch.zeros_like(d["s0"])
+    g = {"d" + n: torch.zeros_like(d[n]) for n in ("q", "k", "v", "gate", "beta", "s0")}
+    at = starts(lens, dev)
+    torch.cuda.synchronize()
+    sq.sq_delta_scan(form, d["q"], d["k"], d["v"], d["gate"], d["beta"], y, seq_start=at, s0=d["s0"], s1=s1, stream=side)
+    sq.sq_delta_scan_bwd(form, d["q"], d["k"], d["v"], d["gate"], d["beta"], d["dy"], g["dq"], g["dk"], g["dv"], g["dgate"],
+                         g["dbeta"], seq_start=at, s0=d["s0"], ds1=d["ds1"], ds0=g["ds0"], stream=side)
+    torch.cuda.synchronize()
+    for u, w in zip(a, (y, s1, *g.values())):
+        assert torch.equal(u, w)
+
+
+def test_captured_and_replayed(dev):
+    """Scan and gradients captured into one graph; replays with changed inputs equal the eager calls."""
+    form, H, dk, dv, lens = 0, 4, 128, 128, [70, 5]
+    x = scan_inputs(form, H, 2, dk, dv, lens, 91, BF16)
+    d = {n: t.to(dev) for n, t in x.items()}
+    at = starts(lens, dev)
+    y, s1 = torch.zeros_like(d["v"]), torch.zeros_like(d["s0"])
+    g = {"d" + n: torch.zeros_like(d[n]) for n in ("q", "k", "v", "gate", "beta", "s0")}
+    nb = sq.sq_delta_scan_bytes(form, BF16, H, 2, dk, dv, 2, sum(lens), backward=True)
+    work = torch.empty(nb, dtype=torch.uint8, device=dev)
+
+    def both():
+        sq.sq_delta_scan(form, d["q"], d["k"], d["v"], d["gate"], d["beta"], y, seq_start=at, s0=d["s0"], s1=s1, workspace=work)
+        sq.sq_delta_scan_bwd(form, d["q"], d["k"], d["v"], d["gate"], d["beta"], d["dy"], g["dq"], g["dk"], g["dv"], g["dgate"],
+                             g["dbeta"], seq_start=at, s0=d["s0"], ds1=d["ds1"], ds0=g["ds0"], workspace=work)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for i in range(3):
+        z = scan_inputs(form, H, 2, dk, dv, lens, 200 + i, BF16)
+        for n in d:
+            d[n].copy_(z[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (y, s1, *g.values())]
+        ey, es = forward(form, z, lens, dev)
+        for u, w in zip(got, (ey, es, *backward(form, z, lens, dev).values())):
+            assert torch.equal(u, w)
+
+
+def test_prompt_then_packed_decode(dev):
+    """The whole path: unit-norm rows, scan of a prompt, sq_pack, decode steps, sq_unpack, scan again, gated norm."""
+    H, dk, dv, T = 2, 64, 64, 75
+    raw = torch.randn(T, 2, H, dk, device=dev)
+    q, k = torch.empty(T, H, dk, device=dev), torch.empty(T, H, dk, device=dev)
+    sq.sq_norm_in(raw[:, 0], q, kind=sq.SQ_NORM_L2)
+    sq.sq_norm_in(raw[:, 1], k, kind=sq.SQ_NORM_L2)
+    x = scan_inputs(0, H, H, dk, dv, [T], 61, F32)
+    x["q"], x["k"] = q.cpu(), k.cpu()
+    d = {n: t.to(dev) for n, t in x.items()}
+    y, s1 = forward(0, x, [T], dev, s0=False)
+    near(y, scan_ref(x, [T], False)[0], "prompt")
+    plan = sq.sq_plan_create(form=0, unit=0, n_layers=1, n_heads=H, d_k=dk, d_v=dv, widths=(8,), budget_milli=8000,
+                             pivot_ppm=0, grid=(1.0, 0.875), gate=np.full((1, H), 0.95, np.float32),
+                             impact=np.ones((1, H, dk), np.float32), unit_bits=np.full(H, 8, np.int32))
+    mem = torch.zeros(sq.sq_pool_bytes(plan, 1), dtype=torch.uint8, device=dev)
+    pool = sq.sq_pool_create(plan, mem, 1)
+    slot = torch.zeros(1, dtype=torch.int32, device=dev)
+    sq.sq_pack(pool, 0, 1, 1, slot, s1)
+    back = torch.empty_like(s1)
+    sq.sq_unpack(pool, 0, 1, 1, slot, back)
+    z = scan_inputs(0, H, H, dk, dv, [1], 62, F32)
+    z["s0"] = back.cpu()
+    ys = torch.zeros(H * dv, device=dev)
+    sq.sq_state_step(pool, 0, 1, 1, slot, *(z[n].to(dev) for n in ("q", "k", "v", "gate", "beta")), ys)
+    y1, _ = forward(0, z, [1], dev)
+    near(y1.view(-1), ys.cpu(), "decode step against a scan from the unpacked state")
+    assert (back - s1).norm() < 0.02 * s1.norm()          # 8-bit codes: 1/254 of a row-and-column scale each
+    o = torch.empty(1, H, dv, dtype=BF16, device=dev)
+    gate = torch.randn(1, H, dv, device=dev).to(BF16)
+    sq.sq_norm_out(ys.view(1, H, dv), o, z=gate)
+    yd = ys.double().cpu().view(1, H, dv)
+    near(o, yd / (yd.square().mean(-1, keepdim=True) + 1e-6).sqrt() * torch.nn.functional.silu(gate.double().cpu()), "gated norm")
+    pool.close()
+    plan.close()
