@@ -24,7 +24,7 @@ static bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintp
 namespace {
 
 struct ScanWork {                    // byte offsets of the workspace's parts
-    size_t th, p, tt, pt, ap, e, du, st, gt, total;
+    size_t th, p, gb, tt, pt, ap, e, du, st, gt, total;
 };
 
 ScanWork scan_work(const sq_scan_cfg& c, bool backward) {
@@ -34,6 +34,7 @@ ScanWork scan_work(const sq_scan_cfg& c, bool backward) {
     const size_t mats = size_t(scan_slots(c.n_tokens, c.n_seq)) * size_t(c.n_heads);
     const size_t vals = size_t(c.n_tokens) * size_t(c.n_heads) * size_t(c.d_v) * 4;
     w.th = take(mats * kMatShorts * 2);
+    if (c.form == SQ_FORM_GDN) w.gb = take(mats * 2 * kChunk * 4);
     if (!backward) {
         w.p = take(mats * kMatShorts * 2);
     } else {
@@ -77,7 +78,7 @@ sq_status check_scan_cfg(const sq_scan_cfg* c) {
 sq_status check_rows(const sq_rows* a, const char* name, int64_t heads, int64_t d, int32_t dt, bool wide) {
     if (!a || !a->d_ptr) { set_error("%s is NULL", name); return SQ_ERR_ARG; }
     if (a->stride < heads * d) { set_error("%s: stride %lld below %lld", name, (long long)a->stride, (long long)(heads * d)); return SQ_ERR_SHAPE; }
-    if (a->stride > (int64_t(1) << 40)) { set_error("%s: stride %lld", name, (long long)a->stride); return SQ_ERR_SHAPE; }
+    if (a->stride >= (int64_t(1) << 24)) { set_error("%s: stride %lld, below 2^24 elements is supported", name, (long long)a->stride); return SQ_ERR_SHAPE; }
     if (!aligned(a->d_ptr, wide ? 16 : uintptr_t(esize(dt))) || (wide && a->stride * esize(dt) % 16 != 0)) {
         set_error("%s: address and stride must be multiples of 16 bytes", name);
         return SQ_ERR_ARG;
@@ -107,6 +108,7 @@ ScanParams scan_params(const sq_scan_cfg& c, const ScanWork& w, void* work, bool
     auto u16 = [base](size_t o) { return reinterpret_cast<uint16_t*>(base + o); };
     auto f32 = [base](size_t o) { return reinterpret_cast<float*>(base + o); };
     p.mat_th = u16(w.th);
+    p.mat_gb = f32(w.gb);
     if (!backward) {
         p.mat_p = u16(w.p);
     } else {
@@ -158,7 +160,7 @@ extern "C" sq_status sq_delta_scan(const sq_scan_cfg* cfg, const sq_rows* q, con
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = cfg->n_tokens > 0 ? launch_scan_prep(p, false, s) : hipSuccess;
     if (e != hipSuccess) return fail_hip(e, "scan preparation launch");
-    e = launch_scan_fwd(p, false, s);
+    e = launch_scan(p, false, s);
     return e == hipSuccess ? SQ_OK : fail_hip(e, "scan launch");
 }
 
@@ -189,11 +191,9 @@ extern "C" sq_status sq_delta_scan_bwd(const sq_scan_cfg* cfg, const sq_rows* q,
     if (cfg->n_tokens > 0) {
         e = launch_scan_prep(p, true, s);
         if (e != hipSuccess) return fail_hip(e, "scan preparation launch");
-        e = launch_scan_fwd(p, true, s);
-        if (e != hipSuccess) return fail_hip(e, "scan launch");
     }
-    e = launch_scan_rev(p, s);
-    if (e != hipSuccess) return fail_hip(e, "reverse scan launch");
+    e = launch_scan(p, true, s);
+    if (e != hipSuccess) return fail_hip(e, "scan launch");
     if (cfg->n_tokens > 0) e = launch_scan_grad(p, s);
     return e == hipSuccess ? SQ_OK : fail_hip(e, "scan gradient launch");
 }

@@ -30,6 +30,7 @@ struct ScanParams {
     // workspace
     uint16_t* mat_th;                // [slot][H] That = (I + A diag(beta))^-1
     uint16_t* mat_p;                 // [slot][H] P (forward)
+    float* mat_gb;                   // [slot][H][2][32] products of the gates up to and after each token (GDN)
     // backward
     uint16_t* mat_tt;                // [slot][H] T^T, T = (I + diag(beta) A)^-1
     uint16_t* mat_pt;                // [slot][H] P^T
@@ -47,10 +48,10 @@ struct ScanParams {
 
 inline int64_t scan_slots(int64_t n_tokens, int n_seq) { return (n_tokens / kChunk) + n_seq; }
 
-// prep: the chunks' small matrices; forward: the scan (keep = also the states and e that the backward pass reads).
+// prep: the chunks' small matrices; scan: forward with outputs, or for the backward pass the forward scan that keeps the
+// states and e, beside the reverse scan of the state's gradient; grad: the gradients, all chunks at once.
 hipError_t launch_scan_prep(const ScanParams& p, bool backward, hipStream_t s);
-hipError_t launch_scan_fwd(const ScanParams& p, bool keep, hipStream_t s);
-hipError_t launch_scan_rev(const ScanParams& p, hipStream_t s);
+hipError_t launch_scan(const ScanParams& p, bool backward, hipStream_t s);
 hipError_t launch_scan_grad(const ScanParams& p, hipStream_t s);
 
 }  // namespace sq

@@ -17,57 +17,53 @@
 
 namespace sq {
 
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // ---------------------------------------------------------------- prep
 
 constexpr int kPrepWaves = 4;
 constexpr int kPrepLd = 36;          // 16-byte aligned rows, 4 banks apart
 
-template <int DK, int NPL, bool KDA, bool BWD>
+// One wave per chunk and head.  Its LDS is one 32 x 32 matrix (two for the backward pass), used in turn for I + N, for
+// its inverse and for P, so that four and more waves fit on a SIMD: with all of them side by side (18 KiB a wave, two
+// waves) the launch took 118 us where it now takes 61 (12301 tokens, 32 heads, bfloat16).
+template <int DK, int DT, bool KDA, bool BWD>
 __global__ void __launch_bounds__(kPrepWaves * 64) k_prep(const ScanParams p) {
-    constexpr int NKB = (DK + 31) / 32;
-    __shared__ __align__(16) float s_n[kPrepWaves][2][32][kPrepLd];
-    __shared__ __align__(16) float s_p[kPrepWaves][32][kPrepLd];
-    __shared__ float s_g[KDA ? 1 : kPrepWaves][32][33];
+    constexpr int NKB = (DK + 31) / 32, NPL = planes_of(DT), NM = BWD ? 2 : 1, ES = DT == SQ_DTYPE_F32 ? 4 : 2;
+    __shared__ __align__(16) float s_m[kPrepWaves][NM][32][kPrepLd];
+    __shared__ float s_gt[KDA ? 1 : kPrepWaves][2][5][32];
     __shared__ float s_b[kPrepWaves][32];
-    const int wave = (int)threadIdx.x >> 6, l = (int)threadIdx.x & 63, n = l & 15, g = l >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), l = (int)threadIdx.x & 63, n = l & 15, g = l >> 4;
     const int64_t id = (int64_t)blockIdx.x * kPrepWaves + wave;
     if (id >= p.n_slots * p.n_heads) return;         // no workgroup barrier below: each wave works alone
     const int h = (int)(id % p.n_heads);
-    const int64_t slot = id / p.n_heads;
-    // the sequence whose first slot is the last one not above this slot
-    int lo = 0, hi = p.n_seq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first_slot(sequence(p, mid), mid) <= slot) lo = mid;
-        else hi = mid - 1;
-    }
-    const Seq sq_ = sequence(p, lo);
-    const int64_t c0 = (slot - first_slot(sq_, lo)) * kChunk;
-    if (c0 < 0 || c0 >= sq_.len) return;             // a slot that no chunk uses
-    const int rem = (int)(sq_.len - c0 < kChunk ? sq_.len - c0 : kChunk);
-    const int64_t tok0 = sq_.start + c0;
-    const int hk = h / (p.n_heads / p.n_heads_k);
+    const ChunkAt ck = chunk_of_slot(p, id / p.n_heads);
+    if (ck.rem <= 0) return;                         // a slot that no chunk uses
+    const int rem = ck.rem, H = p.n_heads, hk = h / (H / p.n_heads_k);
+    const int64_t tok0 = ck.tok0;
     constexpr float gmin = BWD ? kGateMin : 0.f;
 
-    float(&N)[2][32][kPrepLd] = s_n[wave];
-    float(&Pm)[32][kPrepLd] = s_p[wave];
-    if (l < 32) s_b[wave][l] = l < rem ? p.beta[(tok0 + l) * p.n_heads + h] : 0.f;
+    float(&M)[NM][32][kPrepLd] = s_m[wave];
+    if (l < 32) s_b[wave][l] = l < rem ? p.beta[(tok0 + l) * H + h] : 0.f;
     if constexpr (!KDA) {
-        // column j of Gamma: a running product down the rows
-        const float al = (l & 31) < rem ? fmaxf(p.gate[(tok0 + (l & 31)) * p.n_heads + h], gmin) : 1.f;
-        if (l < 32) {
-            float x = 0.f;
-            for (int i = 0; i < 32; ++i) {
-                const float ai = __shfl(al, i, 32);
-                x = i == l ? 1.f : x * ai;
-                s_g[wave][i][l] = x;
+        const int t = l & 31;
+        const float a = t < rem ? p.gate[(tok0 + t) * H + h] : 1.f;
+        GateLevels<float> lv(fmaxf(a, gmin));
+#pragma unroll
+        for (int lev = 0; lev < 5; ++lev) {
+            if (l < 32) {
+                s_gt[wave][0][lev][t] = lv.pre;
+                s_gt[wave][1][lev][t] = lv.suf;
             }
+            lv.grow((t >> lev) & 1, __shfl_xor(lv.full, 1 << lev));
+        }
+        // the gates' products up to each token and after it, for the scan (which takes the gates as they are)
+        if constexpr (BWD) {
+            lv = GateLevels<float>(a);
+#pragma unroll
+            for (int lev = 0; lev < 5; ++lev) lv.grow((t >> lev) & 1, __shfl_xor(lv.full, 1 << lev));
+        }
+        if (l < 32) {
+            p.mat_gb[id * 64 + t] = lv.pre;
+            p.mat_gb[id * 64 + 32 + t] = lv.suf;
         }
     }
 
@@ -75,24 +71,42 @@ __global__ void __launch_bounds__(kPrepWaves * 64) k_prep(const ScanParams p) {
 #pragma unroll
     for (int t = 0; t < 3; ++t) aA[t] = aP[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     [[maybe_unused]] float diag[2] = {0.f, 0.f};
-    for (int kb = 0; kb < NKB; ++kb) {
-        float kx[2][8], qx[2][8], ax[2][8];
+    const uint32_t ks = (uint32_t)p.k.stride * ES, qs = (uint32_t)p.q.stride * ES, gs = (uint32_t)H * DK * 4;
+    const Window wk(static_cast<const char*>(p.k.p) + tok0 * ks, rem * ks), wq(static_cast<const char*>(p.q.p) + tok0 * qs, rem * qs);
+    const Window wg(reinterpret_cast<const char*>(p.gate) + tok0 * gs, KDA ? rem * gs : 0);
+    constexpr int RW = DT == SQ_DTYPE_F32 ? 2 : 1;   // 16-byte loads of 8 elements
+    struct Rows { Raw<DT, 8 / RW> k[2][RW], q[2][RW]; Raw<SQ_DTYPE_F32, 4> a[2][KDA ? 2 : 1]; };
+    auto fetch = [&](int kb) {                       // key rows 32 kb + 8 g .. + 7 of tokens 16 t + n
+        Rows r;
+        const int ch = 32 * kb + 8 * g;
+        auto at = [&](uint32_t off) { return DK < 32 && ch >= DK ? 0xfffffff0u : off; };   // beyond the rows: zeros
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int tok = 16 * t + n, ch = 32 * kb + 8 * g;
-            const bool on = tok < rem && ch < DK;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) { kx[t][j] = qx[t][j] = 0.f; ax[t][j] = 1.f; }
-            if (on) {
-                load8(p.k.p, p.dtype, (tok0 + tok) * p.k.stride + hk * DK + ch, kx[t]);
-                load8(p.q.p, p.dtype, (tok0 + tok) * p.q.stride + hk * DK + ch, qx[t]);
-                if constexpr (KDA) {
-                    load8(p.gate, SQ_DTYPE_F32, ((tok0 + tok) * p.n_heads + h) * DK + ch, ax[t]);
+            for (int i = 0; i < RW; ++i) {
+                r.k[t][i].load(wk, at((16 * t + n) * ks + (hk * DK + ch + 4 * i) * ES));
+                r.q[t][i].load(wq, at((16 * t + n) * qs + (hk * DK + ch + 4 * i) * ES));
+            }
+            if constexpr (KDA) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ax[t][j] = fmaxf(ax[t][j], gmin);
-                }
+                for (int i = 0; i < 2; ++i) r.a[t][i].load(wg, at((16 * t + n) * gs + (h * DK + ch + 4 * i) * 4));
             }
         }
+        return r;
+    };
+    Rows next = fetch(0);
+#pragma unroll(KDA ? 1 : NKB)
+    for (int kb = 0; kb < NKB; ++kb) {
+        const Rows cur = next;
+        if (kb + 1 < NKB) next = fetch(kb + 1);
+        float kx[2][8], qx[2][8];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                kx[t][j] = RW == 2 ? cur.k[t][RW - 1 ? j >> 2 : 0].at(j & 3) : cur.k[t][0].at(j);
+                qx[t][j] = RW == 2 ? cur.q[t][RW - 1 ? j >> 2 : 0].at(j & 3) : cur.q[t][0].at(j);
+            }
         if constexpr (!KDA) {
             Frag<NPL> kf[2], qf[2];
 #pragma unroll
@@ -103,53 +117,49 @@ __global__ void __launch_bounds__(kPrepWaves * 64) k_prep(const ScanParams p) {
         } else {
             // Pairs (i, j), j < i, by the highest bit in which i and j differ: with blocks of 2^lev tokens, i lies in an odd
             // block and j in the even one before it, and Gamma_ij is (gates of i's block up to i) x (gates of j's block
-            // after j), both at most 1.  Five levels cover the triangle.
-            float pre[2][8], suf[2][8], full[2][8];
+            // after j), both at most 1.  Five levels cover the triangle.  At a level a token is a row or a column, never
+            // both: one scaled and split k serves as either operand.
+            GateLevels<float> lv[2][8];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     diag[t] = fmaf(qx[t][j], kx[t][j], diag[t]);
-                    pre[t][j] = full[t][j] = ax[t][j];
-                    suf[t][j] = 1.f;
+                    const bool on = 16 * t + n < rem && (DK >= 32 || 32 * kb + 8 * g < DK);
+                    lv[t][j] = GateLevels<float>(on ? fmaxf(cur.a[t][KDA ? j >> 2 : 0].at(j & 3), gmin) : 1.f);
                 }
 #pragma unroll
             for (int lev = 0; lev < 4; ++lev) {
                 const bool odd = (n >> lev) & 1;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    float kr[8], qr[8], kc[8];
+                    float ku[8], qu[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        kr[j] = odd ? kx[t][j] * pre[t][j] : 0.f;
-                        qr[j] = odd ? qx[t][j] * pre[t][j] : 0.f;
-                        kc[j] = odd ? 0.f : kx[t][j] * suf[t][j];
+                        ku[j] = kx[t][j] * (odd ? lv[t][j].pre : lv[t][j].suf);
+                        qu[j] = qx[t][j] * lv[t][j].pre;
                     }
-                    const Frag<3> fk = split8<3>(kr), fq = split8<3>(qr), fc = split8<3>(kc);
+                    const Frag<3> fk = split8<3>(ku), fq = split8<3>(qu);
                     f32x4 ta{0.f, 0.f, 0.f, 0.f}, tp{0.f, 0.f, 0.f, 0.f};
-                    mma(ta, fk, fc);
-                    mma(tp, fq, fc);
+                    mma(ta, fk, fk);
+                    mma(tp, fq, fk);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const bool pair = ((4 * g + r) >> (lev + 1)) == (n >> (lev + 1));
+                        const int i = 4 * g + r;
+                        const bool pair = ((i ^ n) >> lev) == 1 && i > n;
                         aA[2 * t][r] += pair ? ta[r] : 0.f;
                         aP[2 * t][r] += pair ? tp[r] : 0.f;
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float other = __shfl_xor(full[t][j], 1 << lev);
-                        if (odd) pre[t][j] *= other;
-                        else suf[t][j] *= other;
-                        full[t][j] *= other;
-                    }
+                    for (int j = 0; j < 8; ++j) lv[t][j].grow(odd, __shfl_xor(lv[t][j].full, 1 << lev));
                 }
             }
             float kr[8], qr[8], kc[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                kr[j] = kx[1][j] * pre[1][j];
-                qr[j] = qx[1][j] * pre[1][j];
-                kc[j] = kx[0][j] * suf[0][j];
+                kr[j] = kx[1][j] * lv[1][j].pre;
+                qr[j] = qx[1][j] * lv[1][j].pre;
+                kc[j] = kx[0][j] * lv[0][j].suf;
             }
             const Frag<3> fk = split8<3>(kr), fq = split8<3>(qr), fc = split8<3>(kc);
             mma(aA[1], fk, fc);
@@ -159,6 +169,13 @@ __global__ void __launch_bounds__(kPrepWaves * 64) k_prep(const ScanParams p) {
     wave_sync();
     float* ap = nullptr;
     if constexpr (BWD && !KDA) ap = p.mat_ap + id * 2 * 32 * 32;
+    if constexpr (KDA) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            diag[t] += __shfl_xor(diag[t], 16);      // lane n: q_i . k_i of token 16 t + n
+            diag[t] += __shfl_xor(diag[t], 32);
+        }
+    }
 #pragma unroll
     for (int tl = 0; tl < 3; ++tl) {
         const int ti = tl > 0, tj = tl > 1;
@@ -167,31 +184,22 @@ __global__ void __launch_bounds__(kPrepWaves * 64) k_prep(const ScanParams p) {
             const int i = 16 * ti + 4 * g + r, j = 16 * tj + n;
             float a = aA[tl][r], pv = aP[tl][r];
             if constexpr (!KDA) {
-                const float gm = s_g[wave][i][j];
+                const int lev = j < i ? 31 - __builtin_clz(i ^ j) : 0;
+                const float gm = s_gt[wave][0][lev][i] * s_gt[wave][1][lev][j];
                 a *= gm;
-                pv *= gm;
+                pv *= i == j ? 1.f : gm;
+            } else if (ti == tj) {
+                pv = i == j ? diag[ti] : pv;
             }
             a = j < i ? a : 0.f;
             pv = j <= i ? pv : 0.f;
-            N[0][i][j] = a * s_b[wave][j];
-            if constexpr (BWD) N[1][i][j] = a * s_b[wave][i];
-            Pm[i][j] = pv;
+            aP[tl][r] = pv;
+            M[0][i][j] = a * s_b[wave][j];
+            if constexpr (BWD) M[NM - 1][i][j] = a * s_b[wave][i];
             if constexpr (BWD && !KDA) {
                 ap[i * 32 + j] = a;
                 ap[1024 + i * 32 + j] = pv;
             }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) Pm[4 * g + r][16 + n] = 0.f;     // the tile above the diagonal
-    if constexpr (KDA) {
-        wave_sync();
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            float x = diag[t];
-            x += __shfl_xor(x, 16);
-            x += __shfl_xor(x, 32);
-            if (g == 0) Pm[16 * t + n][16 * t + n] = x;
         }
     }
     wave_sync();
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(kPrepWaves * 64) k_prep(const ScanParams p) {
         float s0 = i == cl ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
         for (int jj = 0; jj < (i + 3) / 4; ++jj) {
-            const f32x4 row = *reinterpret_cast<const f32x4*>(&N[which][i][4 * jj]);
+            const f32x4 row = *reinterpret_cast<const f32x4*>(&M[which][i][4 * jj]);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (4 * jj + j < i) {
@@ -215,37 +223,35 @@ __global__ void __launch_bounds__(kPrepWaves * 64) k_prep(const ScanParams p) {
     }
     wave_sync();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) N[which][i][cl] = x[i];         // without BWD both halves write the same values
+    for (int i = 0; i < 32; ++i) M[which][i][cl] = x[i];         // without BWD both halves write the same values
     wave_sync();
     const size_t mo = (size_t)id * kMatShorts;
-    auto put = [&](uint16_t* mat, int ti, const float* v) {
-        const Frag<3> f = split8<3>(v);
+    auto put = [&](uint16_t* mat, const float (&m)[32][kPrepLd], bool transposed) {
 #pragma unroll
-        for (int pl = 0; pl < 3; ++pl)
-            *reinterpret_cast<u32x4v*>(mat + mo + ((ti * 3 + pl) * 64 + l) * 8) = f.p[pl];
-    };
-#pragma unroll
-    for (int ti = 0; ti < 2; ++ti) {
-        float v[8], w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = 16 * (e >> 2) + 4 * g + (e & 3);
-            v[e] = N[0][16 * ti + n][c];
-            w[e] = Pm[16 * ti + n][c];
-        }
-        put(p.mat_th, ti, v);
-        if constexpr (!BWD) put(p.mat_p, ti, w);
-        if constexpr (BWD) {
+        for (int ti = 0; ti < 2; ++ti) {
+            float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = 16 * (e >> 2) + 4 * g + (e & 3);
-                v[e] = N[1][c][16 * ti + n];
-                w[e] = Pm[c][16 * ti + n];
+                v[e] = transposed ? m[c][16 * ti + n] : m[16 * ti + n][c];
             }
-            put(p.mat_tt, ti, v);
-            put(p.mat_pt, ti, w);
+            const Frag<3> f = split8<3>(v);
+#pragma unroll
+            for (int pl = 0; pl < 3; ++pl)
+                *reinterpret_cast<u32x4v*>(mat + mo + ((ti * 3 + pl) * 64 + l) * 8) = f.p[pl];
         }
-    }
+    };
+    put(p.mat_th, M[0], false);
+    if constexpr (BWD) put(p.mat_tt, M[NM - 1], true);
+    wave_sync();
+#pragma unroll
+    for (int tl = 0; tl < 3; ++tl)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) M[0][16 * (tl > 0) + 4 * g + r][16 * (tl > 1) + n] = aP[tl][r];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) M[0][4 * g + r][16 + n] = 0.f;   // the tile above the diagonal
+    wave_sync();
+    put(BWD ? p.mat_pt : p.mat_p, M[0], BWD);
 }
 
 // ---------------------------------------------------------------- scan
@@ -254,59 +260,43 @@ __global__ void __launch_bounds__(kPrepWaves * 64) k_prep(const ScanParams p) {
 // reverse (the gradient of the state from the last chunk to the first).
 enum : int { kScanOut = 0, kScanKeep = 1, kScanRev = 2 };
 
-template <int NP>
-__device__ __forceinline__ Frag<NP> lds_frag(const uint16_t* base, int plane_stride, int off) {
-    Frag<NP> f;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) f.p[i] = *reinterpret_cast<const u32x4v*>(base + i * plane_stride + off);
-    return f;
-}
+// The scan's LDS: operands of one chunk.  Token-major rows are 4 banks apart, key-major ones 20.
+template <int DK, int NP, int MODE>
+struct ScanLds {
+    static constexpr bool REV = MODE == kScanRev;
+    static constexpr int NKB = (DK + 31) / 32, LDK = 32 * NKB + 8, LDT = 40, NMAT = MODE == kScanKeep ? 1 : 2;
+    uint16_t k[NP][32][LDK];                             // token-major: gamma K forward, (gamma_C / gamma) K in reverse
+    uint16_t q[MODE == kScanOut ? NP : 1][MODE == kScanOut ? 32 : 1][LDK];
+    uint16_t kt[NP][DK][LDT];                            // key-major: the other of the two
+    uint16_t qt[REV ? NP : 1][REV ? DK : 1][LDT];
+    uint16_t m[NMAT][kMatShorts];                        // That, P (forward); T^T, P^T (reverse)
+    float pre[32], suf[32], beta[32], last[DK];
+};
 
-__device__ __forceinline__ Frag<3> mat_frag(const uint16_t* mat, size_t id, int ti, int l) {
-    Frag<3> f;
-#pragma unroll
-    for (int pl = 0; pl < 3; ++pl)
-        f.p[pl] = *reinterpret_cast<const u32x4v*>(mat + id * kMatShorts + ((ti * 3 + pl) * 64 + l) * 8);
-    return f;
-}
-
-__device__ __forceinline__ void load4(const void* p, int dt, int64_t i, float* x) {
-    if (dt == SQ_DTYPE_F32) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = a[j];
-        return;
-    }
-    const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + i);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        x[2 * j] = dt == SQ_DTYPE_BF16 ? bf16_lo(w[j]) : f16_val(w[j] & 0xffffu);
-        x[2 * j + 1] = dt == SQ_DTYPE_BF16 ? bf16_hi(w[j]) : f16_val(w[j] >> 16);
-    }
-}
-
-template <int DK, int NPL, bool KDA, int MODE>
-__global__ void __launch_bounds__(512) k_scan(const ScanParams p) {
-    constexpr bool REV = MODE == kScanRev;
+// One workgroup of DK / 16 waves per DK value columns of a state, so that each thread stages 4 tokens x 2 key rows of a
+// chunk.  The loads of the next chunk are in flight while this one is computed.
+template <int DK, int DT, bool KDA, int MODE>
+__device__ __forceinline__ void scan_body(const ScanParams& p, unsigned block, ScanLds<DK, KDA ? 3 : planes_of(DT), MODE>& s) {
+    constexpr bool REV = MODE == kScanRev, OUT = MODE == kScanOut;
+    constexpr int NPL = planes_of(DT);
     constexpr int NP = KDA ? 3 : NPL;                // planes of the staged operands (gates make them float32)
-    constexpr int NT = DK / 16, NKB = (DK + 31) / 32;
-    constexpr int LDK = 32 * NKB + 8, LDT = 40;      // rows 4 (resp. 20) banks apart
-    constexpr bool kTwoT = REV;                      // the reverse scan needs K^T and Q^T, the forward one Q and K^T
-    __shared__ __align__(16) uint16_t s_k[NP][32][LDK];          // token-major operands
-    __shared__ __align__(16) uint16_t s_q[kTwoT || MODE == kScanKeep ? 1 : NP][32][LDK];
-    __shared__ __align__(16) uint16_t s_kt[NP][DK][LDT];         // key-major operands
-    __shared__ __align__(16) uint16_t s_qt[kTwoT ? NP : 1][DK][LDT];
-    __shared__ __align__(16) float s_pre[32], s_suf[32], s_beta[32], s_last[KDA ? DK : 4];
+    using Lds = ScanLds<DK, NP, MODE>;
+    constexpr int NT = DK / 16, NKB = Lds::NKB, LDK = Lds::LDK, LDT = Lds::LDT, NMAT = Lds::NMAT;
+    constexpr int NW = DK / 16, NTHR = NW * 64, CH = 8 * DK / NTHR, ES = DT == SQ_DTYPE_F32 ? 4 : 2;
+    static_assert(CH == 2);
 
-    const int tid = (int)threadIdx.x, nthr = (int)blockDim.x;
+    const int tid = (int)threadIdx.x;
     const int wave = tid >> 6, l = tid & 63, n = l & 15, g = l >> 4;
     const int H = p.n_heads, dv = p.dv;
-    const int bh = (int)(blockIdx.x % (unsigned)(H * p.n_seq)), sg = (int)(blockIdx.x / (unsigned)(H * p.n_seq));
+    const int bh = (int)(block % (unsigned)(H * p.n_seq)), sg = (int)(block / (unsigned)(H * p.n_seq));
     const int b = bh / H, h = bh % H, hk = h / (H / p.n_heads_k);
-    const Seq seq = sequence(p, b);
-    const int64_t slot0 = first_slot(seq, b);
-    const int col = (sg * (nthr >> 6) + wave) * 16 + n;          // this lane's value column
-    const int64_t nc = (seq.len + kChunk - 1) / kChunk;
+    const Seq sv = sequence(p, b);
+    const int start = __builtin_amdgcn_readfirstlane((int)sv.start), len = __builtin_amdgcn_readfirstlane((int)sv.len);
+    const int64_t slot0 = (start >> 5) + b;
+    const int col = (sg * NW + wave) * 16 + n;                   // this lane's value column
+    const int nc = (len + kChunk - 1) / kChunk;
+    // staging: token quad and key rows of this thread; the gates' products run over the quads, eight neighbouring lanes
+    const int tq = KDA ? tid & 7 : tid / (DK / CH), cq = KDA ? tid >> 3 : tid % (DK / CH);
 
     f32x4 S[NT];
     const float* init = REV ? p.ds1 : p.s0;
@@ -316,72 +306,86 @@ __global__ void __launch_bounds__(512) k_scan(const ScanParams p) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[t][r] = init ? init[sbase + (size_t)(16 * t + 4 * g + r) * dv] : 0.f;
     if constexpr (DK < 32) {                         // the unused half of a block of 32 key rows stays zero
-        for (int i = tid; i < NP * 32 * LDK; i += nthr) (&s_k[0][0][0])[i] = 0;
-        if constexpr (MODE == kScanOut)
-            for (int i = tid; i < NP * 32 * LDK; i += nthr) (&s_q[0][0][0])[i] = 0;
+        for (int i = tid; i < NP * 32 * LDK; i += NTHR) (&s.k[0][0][0])[i] = 0;
+        if constexpr (OUT)
+            for (int i = tid; i < NP * 32 * LDK; i += NTHR) (&s.q[0][0][0])[i] = 0;
     }
 
-    for (int64_t ci = 0; ci < nc; ++ci) {
-        const int64_t c = REV ? nc - 1 - ci : ci;
-        const int64_t tok0 = seq.start + c * kChunk;
-        const int rem = (int)(seq.len - c * kChunk < kChunk ? seq.len - c * kChunk : kChunk);
+    constexpr int MU = (NMAT * kMatShorts / 8 + NTHR - 1) / NTHR;   // 16-byte units of the chunk's matrices per thread
+    Raw<DT, CH> kx[4], qx[4];
+    Raw<SQ_DTYPE_F32, CH> ax[4];
+    u32x4v mx[MU];
+    uint32_t xn[2][4];
+    float gb0 = 0.f, gb1 = 0.f;
+    const ScanRows& xr = REV ? p.dy : p.v;
+    const uint32_t ks = (uint32_t)p.k.stride * ES, qs = (uint32_t)p.q.stride * ES, xs = (uint32_t)xr.stride * ES;
+    const uint32_t gs = (uint32_t)H * DK * 4;
+    const uint32_t ko = 4 * tq * ks + (hk * DK + CH * cq) * ES, qo = 4 * tq * qs + (hk * DK + CH * cq) * ES;
+    const uint32_t go = 4 * tq * gs + (h * DK + CH * cq) * 4, xo = 4 * g * xs + (h * dv + col) * ES;
+    auto fetch = [&](int c) {                        // chunk c into registers
+        const int64_t tok0 = start + (int64_t)c * kChunk;
+        const uint32_t rem = len - c * kChunk < kChunk ? len - c * kChunk : kChunk;
         const size_t id = (size_t)(slot0 + c) * H + h;
-        const Frag<3> m0[2] = {mat_frag(REV ? p.mat_tt : p.mat_th, id, 0, l), mat_frag(REV ? p.mat_tt : p.mat_th, id, 1, l)};
-        float xin[2][4];                             // v (forward) or dy (reverse)
-        const ScanRows& xr = REV ? p.dy : p.v;
+        const Window wk(static_cast<const char*>(p.k.p) + tok0 * ks, rem * ks);
+        const Window wx(static_cast<const char*>(xr.p) + tok0 * xs, rem * xs);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kx[j].load(wk, ko + j * ks);
+        if constexpr (MODE != kScanKeep) {
+            const Window wq(static_cast<const char*>(p.q.p) + tok0 * qs, rem * qs);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) qx[j].load(wq, qo + j * qs);
+        }
+        if constexpr (KDA) {
+            const Window wg(reinterpret_cast<const char*>(p.gate) + tok0 * gs, rem * gs);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ax[j].load(wg, go + j * gs);
+        } else if (tid < 64) {
+            gb0 = p.mat_gb[id * 64 + tid];           // the products of the gates, from k_prep
+        }
+        if (tid < 32) {
+            const Window wb(p.beta + tok0 * H, rem * H * 4);
+            gb1 = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(wb.r, (tid * H + h) * 4, 0, 0));
+        }
+#pragma unroll
+        for (int u = 0; u < MU; ++u) {
+            const int i = tid + u * NTHR, which = i / (kMatShorts / 8);
+            if (NMAT * kMatShorts / 8 % NTHR == 0 || i < NMAT * kMatShorts / 8) {
+                const uint16_t* m = which ? (REV ? p.mat_pt : p.mat_p) : (REV ? p.mat_tt : p.mat_th);
+                mx[u] = *reinterpret_cast<const u32x4v*>(m + id * kMatShorts + (i - which * (kMatShorts / 8)) * 8);
+            }
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int tok = 16 * t + 4 * g + r;
-                xin[t][r] = tok < rem ? load1(xr.p, p.dtype, (tok0 + tok) * xr.stride + (int64_t)h * dv + col) : 0.f;
-            }
-        __syncthreads();                             // the previous chunk's operands have been read
-        if (tid < 64) {
-            const int t = l & 31;
-            if (l < 32) s_beta[t] = t < rem ? p.beta[(tok0 + t) * H + h] : 0.f;
-            if constexpr (!KDA) {
-                float pr = t < rem ? p.gate[(tok0 + t) * H + h] : 1.f, sf = pr;
+            for (int r = 0; r < 4; ++r) xn[t][r] = win_load1<DT>(wx, xo + (16 * t + r) * xs);
+    };
+    if (nc > 0) fetch(REV ? nc - 1 : 0);
+
+    for (int ci = 0; ci < nc; ++ci) {
+        const int c = REV ? nc - 1 - ci : ci;
+        const int64_t tok0 = start + (int64_t)c * kChunk;
+        const int rem = len - c * kChunk < kChunk ? len - c * kChunk : kChunk;
+        const size_t id = (size_t)(slot0 + c) * H + h;
+        lds_barrier();                               // the previous chunk's operands have been read
+        if (!KDA && tid < 64) (&s.pre[0])[tid] = gb0;            // pre, then suf
+        if (tid < 32) s.beta[tid] = gb1;
+        if (!KDA && tid == 31) s.last[0] = gb0;                  // pre of the last token: all gates
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float a = __shfl_up(pr, o, 32), z = __shfl_down(sf, o, 32);
-                    if (t >= o) pr *= a;
-                    if (t + o < 32) sf *= z;
-                }
-                sf = __shfl_down(sf, 1, 32);
-                if (l < 32) {
-                    s_pre[t] = pr;
-                    s_suf[t] = t == 31 ? 1.f : sf;
-                    if (t == 31) s_last[0] = pr;
-                }
-            }
+        for (int u = 0; u < MU; ++u) {
+            const int i = tid + u * NTHR;
+            if (NMAT * kMatShorts / 8 % NTHR == 0 || i < NMAT * kMatShorts / 8)
+                *reinterpret_cast<u32x4v*>(&s.m[0][0] + i * 8) = mx[u];
         }
-        for (int u = tid; u < 8 * DK / 4; u += nthr) {           // 4 tokens x 4 key rows each
-            const int tq = u & 7, cq = u >> 3;
-            float kx[4][4], qx[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int tok = 4 * tq + j;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) kx[j][i] = qx[j][i] = 0.f;
-                if (tok < rem) {
-                    load4(p.k.p, p.dtype, (tok0 + tok) * p.k.stride + hk * DK + 4 * cq, kx[j]);
-                    if constexpr (MODE != kScanKeep)
-                        load4(p.q.p, p.dtype, (tok0 + tok) * p.q.stride + hk * DK + 4 * cq, qx[j]);
-                }
-            }
-            float pre[4][4], suf[4][4];
+        {
+            float pre[4][CH], suf[4][CH];
             if constexpr (KDA) {
-                float al[4][4];
+                float al[4][CH];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) al[j][i] = 1.f;
-                    if (4 * tq + j < rem)
-                        load4(p.gate, SQ_DTYPE_F32, ((tok0 + 4 * tq + j) * H + h) * DK + 4 * cq, al[j]);
-                }
+                    for (int i = 0; i < CH; ++i) al[j][i] = 4 * tq + j < rem ? ax[j].at(i) : 1.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < CH; ++i) {
                     pre[0][i] = al[0][i];
                     suf[3][i] = 1.f;
 #pragma unroll
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(512) k_scan(const ScanParams p) {
                         if (tq >= o) up *= a;
                         if (tq + o < 8) dn *= z;
                     }
-                    if (tq == 7) s_last[4 * cq + i] = up;
+                    if (tq == 7) s.last[CH * cq + i] = up;
                     float before = __shfl_up(up, 1, 8), after = __shfl_down(dn, 1, 8);
                     before = tq == 0 ? 1.f : before;
                     after = tq == 7 ? 1.f : after;
@@ -404,46 +408,59 @@ __global__ void __launch_bounds__(512) k_scan(const ScanParams p) {
                 }
             }
             // token-major: forward gamma K (and gamma Q), reverse (gamma_C / gamma) K; key-major: the other way round
-            float a[4][4], bq[4][4], kt[4][4];
+            const int pc = kpos(CH * cq), pt = kpos(4 * tq);
+            auto put_row = [&](auto& arr, const float* x, int row) {        // CH adjacent key rows of a token
+                float m[CH];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int i = 0; i < CH; ++i) m[i] = x[i];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a[j][i] = kx[j][i] * (KDA ? (REV ? suf[j][i] : pre[j][i]) : 1.f);
-                    bq[j][i] = qx[j][i] * (KDA ? pre[j][i] : 1.f);
-                    kt[i][j] = kx[j][i] * (KDA ? (REV ? pre[j][i] : suf[j][i]) : 1.f);
+                for (int pl = 0; pl < NP; ++pl) {
+                    uint32_t* at = reinterpret_cast<uint32_t*>(&arr[pl][row][pc]);
+                    at[0] = hi16_pair(m[0], m[1]);
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) m[i] -= trunc_bf16(m[i]);
                 }
-            const int pc = kpos(4 * cq), pt = kpos(4 * tq);
+            };
+            auto put_col = [&](auto& arr, const float* x, int row) {        // four tokens of a key row
+                u32x2 w[NP];
+                split4<NP>(x, w);
+#pragma unroll
+                for (int i = 0; i < NP; ++i) *reinterpret_cast<u32x2*>(&arr[i][row][pt]) = w[i];
+            };
+            float kt[CH][4], qt[CH][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                u32x2 w[NP];
-                split4<NP>(a[j], w);
+                float a[CH], bq[CH];
 #pragma unroll
-                for (int i = 0; i < NP; ++i) *reinterpret_cast<u32x2*>(&s_k[i][4 * tq + j][pc]) = w[i];
-                split4<NP>(kt[j], w);
-#pragma unroll
-                for (int i = 0; i < NP; ++i) *reinterpret_cast<u32x2*>(&s_kt[i][4 * cq + j][pt]) = w[i];
-                if constexpr (MODE == kScanOut) {
-                    split4<NP>(bq[j], w);
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) *reinterpret_cast<u32x2*>(&s_q[i][4 * tq + j][pc]) = w[i];
+                for (int i = 0; i < CH; ++i) {
+                    const float kv = kx[j].at(i);
+                    a[i] = kv * (KDA ? (REV ? suf[j][i] : pre[j][i]) : 1.f);
+                    kt[i][j] = kv * (KDA ? (REV ? pre[j][i] : suf[j][i]) : 1.f);
+                    if constexpr (MODE != kScanKeep) bq[i] = qt[i][j] = qx[j].at(i) * (KDA ? pre[j][i] : 1.f);
                 }
-                if constexpr (REV) {
-                    const float qt[4] = {bq[0][j], bq[1][j], bq[2][j], bq[3][j]};
-                    split4<NP>(qt, w);
+                put_row(s.k, a, 4 * tq + j);
+                if constexpr (OUT) put_row(s.q, bq, 4 * tq + j);
+            }
 #pragma unroll
-                    for (int i = 0; i < NP; ++i) *reinterpret_cast<u32x2*>(&s_qt[i][4 * cq + j][pt]) = w[i];
-                }
+            for (int i = 0; i < CH; ++i) {
+                put_col(s.kt, kt[i], CH * cq + i);
+                if constexpr (REV) put_col(s.qt, qt[i], CH * cq + i);
             }
         }
-        __syncthreads();
+        float xin[2][4];                             // v (forward) or dy (reverse)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) xin[t][r] = val1<DT>(xn[t][r]);
+        lds_barrier();
+        if (ci + 1 < nc) fetch(REV ? c - 1 : c + 1);
 
-        if constexpr (MODE != kScanOut) {            // the backward pass reads the states at the chunk borders
-            float* keep = (REV ? p.gt : p.st) + id * (size_t)DK * dv + col;
+        if constexpr (!OUT) {                        // the backward pass reads the states at the chunk borders
+            float* keep = (REV ? p.gt : p.st) + id * (size_t)DK * dv;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) keep[(size_t)(16 * t + 4 * g + r) * dv] = S[t][r];
+                for (int r = 0; r < 4; ++r) keep[(uint32_t)((16 * t + 4 * g + r) * dv + col)] = S[t][r];
         }
         const f32x4 zero{0.f, 0.f, 0.f, 0.f};
         f32x4 z[2] = {zero, zero}, yq[2] = {zero, zero};
@@ -456,8 +473,8 @@ __global__ void __launch_bounds__(512) k_scan(const ScanParams p) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int off = (16 * t + n) * LDK + 32 * kb + 8 * g;
-                mma(z[t], lds_frag<NP>(&s_k[0][0][0], 32 * LDK, off), sf);
-                if constexpr (MODE == kScanOut) mma(yq[t], lds_frag<NP>(&s_q[0][0][0], 32 * LDK, off), sf);
+                mma(z[t], lds_frag<NP>(&s.k[0][0][0], 32 * LDK, off), sf);
+                if constexpr (OUT) mma(yq[t], lds_frag<NP>(&s.q[0][0][0], 32 * LDK, off), sf);
             }
         }
         float pre[2][4], suf[2][4], be[2][4];
@@ -465,10 +482,11 @@ __global__ void __launch_bounds__(512) k_scan(const ScanParams p) {
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                pre[t][r] = KDA ? 1.f : s_pre[16 * t + 4 * g + r];
-                suf[t][r] = KDA ? 1.f : s_suf[16 * t + 4 * g + r];
-                be[t][r] = s_beta[16 * t + 4 * g + r];
+                pre[t][r] = KDA ? 1.f : s.pre[16 * t + 4 * g + r];
+                suf[t][r] = KDA ? 1.f : s.suf[16 * t + 4 * g + r];
+                be[t][r] = s.beta[16 * t + 4 * g + r];
             }
+        auto mat = [&](int which, int t) { return lds_frag<3>(&s.m[0][0], 512, which * kMatShorts + t * 1536 + 8 * l); };
         float w8[8];
         if constexpr (!REV) {
 #pragma unroll
@@ -476,31 +494,29 @@ __global__ void __launch_bounds__(512) k_scan(const ScanParams p) {
             const Frag<3> rf = split8<3>(w8);
             f32x4 ev[2] = {zero, zero};
 #pragma unroll
-            for (int t = 0; t < 2; ++t) mma(ev[t], m0[t], rf);
+            for (int t = 0; t < 2; ++t) mma(ev[t], mat(0, t), rf);
             if constexpr (MODE == kScanKeep) {
+                const Window we(p.e + tok0 * H * dv, (uint32_t)rem * H * dv * 4);
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int tok = 16 * t + 4 * g + r;
-                        if (tok < rem) p.e[((tok0 + tok) * H + h) * dv + col] = ev[t][r];
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        win_store1<SQ_DTYPE_F32>(we, ((16 * t + 4 * g + r) * H * dv + h * dv + col) * 4, ev[t][r]);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) w8[e] = ev[e >> 2][e & 3] * be[e >> 2][e & 3];
-            if constexpr (MODE == kScanOut) {
+            if constexpr (OUT) {
                 const Frag<3> uf = split8<3>(w8);
+                const uint32_t ys = (uint32_t)p.y.stride * ES, yo = 4 * g * ys + (h * dv + col) * ES;
+                const Window wy(static_cast<const char*>(p.y.p) + tok0 * ys, (uint32_t)rem * ys);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     f32x4 y;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) y[r] = yq[t][r] * pre[t][r];
-                    mma(y, mat_frag(p.mat_p, id, t, l), uf);
+                    mma(y, mat(1, t), uf);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int tok = 16 * t + 4 * g + r;
-                        if (tok < rem) store1(p.y.p, p.dtype, (tok0 + tok) * p.y.stride + (int64_t)h * dv + col, y[r]);
-                    }
+                    for (int r = 0; r < 4; ++r) win_store1<DT>(wy, yo + (16 * t + r) * ys, y[r]);
                 }
             }
             if constexpr (!KDA) {
@@ -511,52 +527,53 @@ __global__ void __launch_bounds__(512) k_scan(const ScanParams p) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[t][r] *= s_last[KDA ? 16 * t + 4 * g + r : 0];
-                mma(S[t], lds_frag<NP>(&s_kt[0][0][0], DK * LDT, (16 * t + n) * LDT + 8 * g), uf);
+                for (int r = 0; r < 4; ++r) S[t][r] *= s.last[KDA ? 16 * t + 4 * g + r : 0];
+                mma(S[t], lds_frag<NP>(&s.kt[0][0][0], DK * LDT, (16 * t + n) * LDT + 8 * g), uf);
             }
         } else {
             // R = (gamma_C / gamma) K G + P^T dy;  du = T^T R;  G <- gamma_C G + (gamma Q)^T dy - (gamma K)^T (beta du)
 #pragma unroll
             for (int e = 0; e < 8; ++e) w8[e] = xin[e >> 2][e & 3];
-            const Frag<3> dyf = split8<3>(w8);
+            const Frag<NPL> dyf = split8<NPL>(w8);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) z[t][r] *= suf[t][r];
-                mma(z[t], mat_frag(p.mat_pt, id, t, l), dyf);
+                mma(z[t], mat(1, t), dyf);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) w8[e] = z[e >> 2][e & 3];
             const Frag<3> rf = split8<3>(w8);
             f32x4 du[2] = {zero, zero};
 #pragma unroll
-            for (int t = 0; t < 2; ++t) mma(du[t], m0[t], rf);
+            for (int t = 0; t < 2; ++t) mma(du[t], mat(0, t), rf);
             float q8[8];
+            const uint32_t vs = (uint32_t)p.dvv.stride * ES, vo = 4 * g * vs + (h * dv + col) * ES;
+            const Window wd(p.du + tok0 * H * dv, (uint32_t)rem * H * dv * 4);
+            const Window wv(static_cast<const char*>(p.dvv.p) + tok0 * vs, (uint32_t)rem * vs);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int tok = 16 * t + 4 * g + r;
                     const float w = du[t][r] * be[t][r];
-                    if (tok < rem) {
-                        p.du[((tok0 + tok) * H + h) * dv + col] = du[t][r];
-                        store1(p.dvv.p, p.dtype, (tok0 + tok) * p.dvv.stride + (int64_t)h * dv + col, w);
-                    }
+                    win_store1<SQ_DTYPE_F32>(wd, ((16 * t + 4 * g + r) * H * dv + h * dv + col) * 4, du[t][r]);
+                    win_store1<DT>(wv, vo + (16 * t + r) * vs, w);
                     w8[4 * t + r] = -w * pre[t][r];
                     q8[4 * t + r] = xin[t][r] * pre[t][r];
                 }
-            const Frag<3> wf = split8<3>(w8), qf = split8<3>(q8);
+            const Frag<3> wf = split8<3>(w8);
+            const Frag<KDA ? NPL : 3> qf = split8<KDA ? NPL : 3>(q8);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[t][r] *= s_last[KDA ? 16 * t + 4 * g + r : 0];
+                for (int r = 0; r < 4; ++r) S[t][r] *= s.last[KDA ? 16 * t + 4 * g + r : 0];
                 const int off = (16 * t + n) * LDT + 8 * g;
-                mma(S[t], lds_frag<NP>(&s_kt[0][0][0], DK * LDT, off), wf);
-                mma(S[t], lds_frag<NP>(&s_qt[0][0][0], DK * LDT, off), qf);
+                mma(S[t], lds_frag<NP>(&s.qt[0][0][0], DK * LDT, off), qf);
+                mma(S[t], lds_frag<NP>(&s.kt[0][0][0], DK * LDT, off), wf);
             }
         }
     }
-    float* fin = REV ? p.ds0 : MODE == kScanOut ? p.s1 : nullptr;
+    float* fin = REV ? p.ds0 : OUT ? p.s1 : nullptr;
     if (fin) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -565,37 +582,49 @@ __global__ void __launch_bounds__(512) k_scan(const ScanParams p) {
     }
 }
 
+template <int DK, int DT, bool KDA>
+__global__ void __launch_bounds__(4 * DK) k_scan(const ScanParams p) {
+    __shared__ __align__(16) ScanLds<DK, KDA ? 3 : planes_of(DT), kScanOut> s;
+    scan_body<DK, DT, KDA, kScanOut>(p, blockIdx.x, s);
+}
+
+// The two scans of the backward pass, which do not depend on each other, side by side in one launch.
+template <int DK, int DT, bool KDA>
+__global__ void __launch_bounds__(4 * DK) k_scan_both(const ScanParams p, unsigned n_rev) {
+    constexpr int NP = KDA ? 3 : planes_of(DT);
+    __shared__ __align__(16) union U {
+        ScanLds<DK, NP, kScanKeep> f;
+        ScanLds<DK, NP, kScanRev> r;
+    } s;
+    // the reverse scans are the longer ones: they start first
+    if (blockIdx.x < n_rev) scan_body<DK, DT, KDA, kScanRev>(p, blockIdx.x, s.r);
+    else scan_body<DK, DT, KDA, kScanKeep>(p, blockIdx.x - n_rev, s.f);
+}
+
 // ---------------------------------------------------------------- launchers
 
-template <int DK, int NPL, bool KDA>
+template <int DK, int DT, bool KDA>
 static hipError_t prep_t(const ScanParams& p, bool backward, hipStream_t s) {
     const int64_t blocks = (p.n_slots * p.n_heads + kPrepWaves - 1) / kPrepWaves;
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks), blk(kPrepWaves * 64);
-    if (backward) k_prep<DK, NPL, KDA, true><<<grid, blk, 0, s>>>(p);
-    else k_prep<DK, NPL, KDA, false><<<grid, blk, 0, s>>>(p);
+    if (backward) k_prep<DK, DT, KDA, true><<<grid, blk, 0, s>>>(p);
+    else k_prep<DK, DT, KDA, false><<<grid, blk, 0, s>>>(p);
     return hipGetLastError();
 }
 
-template <int DK, int NPL, bool KDA>
-static hipError_t scan_t(const ScanParams& p, int mode, hipStream_t s) {
-    const int slices = p.dv / 16, nw = slices < 8 ? slices : 8;
-    const int64_t blocks = (int64_t)p.n_seq * p.n_heads * (slices / nw);
+template <int DK, int DT, bool KDA>
+static hipError_t scan_t(const ScanParams& p, bool backward, hipStream_t s) {
+    if (p.dv % DK != 0) return hipErrorInvalidValue;
+    const int64_t blocks = (int64_t)p.n_seq * p.n_heads * (p.dv / DK) * (backward ? 2 : 1);
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), blk(nw * 64);
-    switch (mode) {
-        case kScanOut: k_scan<DK, NPL, KDA, kScanOut><<<grid, blk, 0, s>>>(p); break;
-        case kScanKeep: k_scan<DK, NPL, KDA, kScanKeep><<<grid, blk, 0, s>>>(p); break;
-        default: k_scan<DK, NPL, KDA, kScanRev><<<grid, blk, 0, s>>>(p); break;
-    }
+    const dim3 grid((unsigned)blocks), blk(4 * DK);
+    if (backward) k_scan_both<DK, DT, KDA><<<grid, blk, 0, s>>>(p, (unsigned)(blocks / 2));
+    else k_scan<DK, DT, KDA><<<grid, blk, 0, s>>>(p);
     return hipGetLastError();
 }
 
 hipError_t launch_scan_prep(const ScanParams& p, bool backward, hipStream_t s) { SQ_SCAN_DISPATCH(prep_t, p, backward, s); }
-hipError_t launch_scan_fwd(const ScanParams& p, bool keep, hipStream_t s) {
-    const int mode = keep ? kScanKeep : kScanOut;
-    SQ_SCAN_DISPATCH(scan_t, p, mode, s);
-}
-hipError_t launch_scan_rev(const ScanParams& p, hipStream_t s) { SQ_SCAN_DISPATCH(scan_t, p, kScanRev, s); }
+hipError_t launch_scan(const ScanParams& p, bool backward, hipStream_t s) { SQ_SCAN_DISPATCH(scan_t, p, backward, s); }
 
 }  // namespace sq

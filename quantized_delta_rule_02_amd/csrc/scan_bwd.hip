@@ -475,8 +475,9 @@ __global__ void __launch_bounds__(DK * 4) k_grad(const ScanParams p) {
         }
 }
 
-template <int DK, int NPL, bool KDA>
+template <int DK, int DT, bool KDA>
 static hipError_t grad_t(const ScanParams& p, hipStream_t s) {
+    constexpr int NPL = DT == SQ_DTYPE_BF16 ? 1 : DT == SQ_DTYPE_F16 ? 2 : 3;
     const int64_t blocks = p.n_slots * p.n_heads_k;
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
     k_grad<DK, NPL, KDA><<<dim3((unsigned)blocks), dim3(DK * 4), 0, s>>>(p);

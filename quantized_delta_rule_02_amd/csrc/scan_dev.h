@@ -105,20 +105,128 @@ __device__ __forceinline__ int64_t first_slot(const Seq& q, int b) { return (q.s
 // either way, and the quotient stays one of normal numbers, also for a gate of zero.  The states take the gates as they are.
 constexpr float kGateMin = 1e-30f;
 
-// gate per key row: float32 operands whatever the inputs' type (three planes); one gate per head: the inputs' own planes
-#define SQ_SCAN_DISPATCH(fn, ...)                                                            \
-    do {                                                                                     \
-        const int np = p.dtype == SQ_DTYPE_BF16 ? 1 : p.dtype == SQ_DTYPE_F16 ? 2 : 3;       \
-        if (p.form == SQ_FORM_KDA) {                                                         \
-            if (p.dk == 16) return fn<16, 3, true>(__VA_ARGS__);                             \
-            if (p.dk == 64) return fn<64, 3, true>(__VA_ARGS__);                             \
-            if (p.dk == 128) return fn<128, 3, true>(__VA_ARGS__);                           \
-        } else {                                                                             \
-            if (p.dk == 16) return np == 1 ? fn<16, 1, false>(__VA_ARGS__) : np == 2 ? fn<16, 2, false>(__VA_ARGS__) : fn<16, 3, false>(__VA_ARGS__);       \
-            if (p.dk == 64) return np == 1 ? fn<64, 1, false>(__VA_ARGS__) : np == 2 ? fn<64, 2, false>(__VA_ARGS__) : fn<64, 3, false>(__VA_ARGS__);       \
-            if (p.dk == 128) return np == 1 ? fn<128, 1, false>(__VA_ARGS__) : np == 2 ? fn<128, 2, false>(__VA_ARGS__) : fn<128, 3, false>(__VA_ARGS__);   \
-        }                                                                                    \
-        return hipErrorInvalidValue;                                                         \
+// The chunk of a slot: its first token and how many it has (0: no chunk uses the slot).  A binary search for the sequence
+// whose first slot is the last one not above the slot.
+struct ChunkAt {
+    int64_t tok0;
+    int rem;
+};
+__device__ __forceinline__ ChunkAt chunk_of_slot(const ScanParams& p, int64_t slot) {
+    int lo = 0, hi = p.n_seq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first_slot(sequence(p, mid), mid) <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    const Seq q = sequence(p, lo);
+    const int64_t c0 = (slot - first_slot(q, lo)) * kChunk;
+    const int start = __builtin_amdgcn_readfirstlane((int)(q.start + c0));
+    int64_t rem = c0 < 0 ? 0 : q.len - c0;
+    rem = rem < 0 ? 0 : rem > kChunk ? kChunk : rem;
+    return ChunkAt{start, __builtin_amdgcn_readfirstlane((int)rem)};
+}
+
+// Products of one token's gates within its block of 2^lev tokens: up to it, after it, and of the whole block.
+template <typename T>
+struct GateLevels {
+    T pre, suf, full;
+    GateLevels() = default;
+    __device__ __forceinline__ explicit GateLevels(T a) : pre(a), suf(1), full(a) {}
+    // joins the sibling block, whose gates multiply to `other`; odd: this token lies in the second of the two
+    __device__ __forceinline__ void grow(bool odd, T other) {
+        pre = odd ? pre * other : pre;
+        suf = odd ? suf : suf * other;
+        full *= other;
+    }
+};
+
+// Orders a wave's own LDS accesses.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <int NP>
+__device__ __forceinline__ Frag<NP> lds_frag(const uint16_t* base, int plane_stride, int off) {
+    Frag<NP> f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) f.p[i] = *reinterpret_cast<const u32x4v*>(base + i * plane_stride + off);
+    return f;
+}
+
+// A barrier for LDS contents only: loads from memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// A window of memory whose loads give 0 and whose stores do nothing beyond `bytes`: the rows behind a sequence's end need
+// no branch.  The base is the same for the whole wave; offsets are 32 bits (the stride limit keeps a chunk below 4 GiB).
+struct Window {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ Window(const void* base, uint32_t bytes)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000)) {}
+};
+template <int DT>
+__device__ __forceinline__ uint32_t win_load1(const Window& w, uint32_t off) {
+    if constexpr (DT == SQ_DTYPE_F32) return __builtin_amdgcn_raw_buffer_load_b32(w.r, off, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b16(w.r, off, 0, 0);
+}
+template <int DT>
+__device__ __forceinline__ float val1(uint32_t x) {
+    return DT == SQ_DTYPE_F32 ? __uint_as_float(x) : DT == SQ_DTYPE_BF16 ? bf16_lo(x) : f16_val(x);
+}
+template <int DT>
+__device__ __forceinline__ void win_store1(const Window& w, uint32_t off, float x) {
+    if constexpr (DT == SQ_DTYPE_F32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), w.r, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(DT == SQ_DTYPE_BF16 ? bf16_bits(x) : f16_bits(x)), w.r, off, 0, 0);
+}
+
+// N adjacent elements as loaded, and their values.
+template <int DT, int N>
+struct Raw {
+    static constexpr int W = N * (DT == SQ_DTYPE_F32 ? 4 : 2) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const Window& b, uint32_t off) {
+        if constexpr (W == 1) {
+            w[0] = __builtin_amdgcn_raw_buffer_load_b32(b.r, off, 0, 0);
+        } else if constexpr (W == 2) {
+            const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(b.r, off, 0, 0);
+            w[0] = x[0];
+            w[1] = x[1];
+        } else {
+            static_assert(W == 4);
+            const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(b.r, off, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = x[i];
+        }
+    }
+    __device__ __forceinline__ float at(int j) const {
+        if constexpr (DT == SQ_DTYPE_F32) return __uint_as_float(w[j]);
+        else return val1<DT>((j & 1) ? w[j / 2] >> 16 : w[j / 2] & 0xffffu);
+    }
+};
+
+constexpr int planes_of(int dt) { return dt == SQ_DTYPE_BF16 ? 1 : dt == SQ_DTYPE_F16 ? 2 : 3; }   // that hold it exactly
+
+#define SQ_SCAN_DISPATCH_DT(fn, DK, KDA, ...)                                                    \
+    do {                                                                                         \
+        if (p.dtype == SQ_DTYPE_BF16) return fn<DK, SQ_DTYPE_BF16, KDA>(__VA_ARGS__);             \
+        if (p.dtype == SQ_DTYPE_F16) return fn<DK, SQ_DTYPE_F16, KDA>(__VA_ARGS__);               \
+        return fn<DK, SQ_DTYPE_F32, KDA>(__VA_ARGS__);                                           \
+    } while (0)
+#define SQ_SCAN_DISPATCH(fn, ...)                                                                \
+    do {                                                                                         \
+        const bool kda = p.form == SQ_FORM_KDA;                                                  \
+        if (p.dk == 16 && kda) SQ_SCAN_DISPATCH_DT(fn, 16, true, __VA_ARGS__);                    \
+        if (p.dk == 16) SQ_SCAN_DISPATCH_DT(fn, 16, false, __VA_ARGS__);                          \
+        if (p.dk == 64 && kda) SQ_SCAN_DISPATCH_DT(fn, 64, true, __VA_ARGS__);                    \
+        if (p.dk == 64) SQ_SCAN_DISPATCH_DT(fn, 64, false, __VA_ARGS__);                          \
+        if (p.dk == 128 && kda) SQ_SCAN_DISPATCH_DT(fn, 128, true, __VA_ARGS__);                  \
+        if (p.dk == 128) SQ_SCAN_DISPATCH_DT(fn, 128, false, __VA_ARGS__);                        \
+        return hipErrorInvalidValue;                                                             \
     } while (0)
 
 }  // namespace sq

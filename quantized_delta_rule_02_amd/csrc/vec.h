@@ -16,11 +16,12 @@ inline int dtype_bytes(int dt) { return dt == SQ_DTYPE_F32 ? 4 : 2; }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Round to nearest, ties to even; NaN stays NaN.
+// Round to nearest, ties to even; NaN stays NaN (one conversion instruction on gfx950).
 __device__ __forceinline__ uint32_t bf16_bits(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const uint32_t r = u + 0x7fffu + ((u >> 16) & 1u);
-    return (x != x) ? (u >> 16) | 0x40u : r >> 16;
+    const __bf16 v = (__bf16)x;
+    uint16_t b;
+    __builtin_memcpy(&b, &v, 2);
+    return b;
 }
 
 __device__ __forceinline__ float f16_val(uint32_t h) {
