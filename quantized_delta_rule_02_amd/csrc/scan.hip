@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kPrepWaves * 64) k_prep(const ScanParams p) {
                     float ku[8], qu[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        ku[j] = kx[t][j] * (odd ? lv[t][j].pre : lv[t][j].suf);
+                        ku[j] = kx[t][j] * pick(odd, lv[t][j].pre, lv[t][j].suf);
                         qu[j] = qx[t][j] * lv[t][j].pre;
                     }
                     const Frag<3> fk = split8<3>(ku), fq = split8<3>(qu);

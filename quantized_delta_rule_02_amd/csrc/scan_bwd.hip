@@ -14,7 +14,7 @@
 // The last sum is taken over exactly those terms, not as a difference of running sums over all of them: each term is
 // proportional to alpha_t, so that the quotient by alpha_t keeps its relative accuracy for small gates.
 //
-// One workgroup per (chunk, q/k head), a wave per 16 key rows; the value heads that share q and k follow one another and
+// One workgroup per (chunk, q/k head), a wave per 32 key rows; the value heads that share q and k follow one another and
 // their dq and dk add up in registers, in a fixed order.
 #include <hip/hip_runtime.h>
 
@@ -84,403 +84,595 @@ __device__ __forceinline__ void prefix_before(float (&v)[2][4], int g) {
     }
 }
 
-template <int DK, int NPL, bool KDA>
-__global__ void __launch_bounds__(DK * 4) k_grad(const ScanParams p) {
-    constexpr int NW = DK / 16, NT = NW * 64;
-    constexpr int VB = DK == 16 ? 16 : 64, VBP = VB < 32 ? 32 : VB, LDV = VBP + 8;   // value columns staged at a time
-    constexpr int OCT = VB / 8, JOBS = (6 + NW - 1) / NW;
-    static_assert(32 * OCT <= NT, "one staging unit per thread");
-    __shared__ __align__(16) uint16_t s_dy[NPL][32][LDV], s_u[3][32][LDV], s_w[3][32][LDV];
-    __shared__ __align__(16) float s_b1[32][36], s_b2[32][36];
-    __shared__ float s_e[KDA ? 1 : 32][33], s_gam[KDA ? 1 : 32][33];
-    __shared__ float s_row[NW][32], s_col[NW][32], s_corner[NW], s_pre[32], s_suf[32];
+template <int DK, int DT, bool KDA>
+struct GradLds {
+    static constexpr int NPL = planes_of(DT), NW = DK >= 64 ? DK / 32 : 1;
+    static constexpr int VB = DK, VBP = VB < 32 ? 32 : VB, LDV = VBP + 8;    // value columns staged at a time
+    union {
+        struct { uint16_t dy[NPL][32][LDV], u[3][32][LDV], w[3][32][LDV]; };
+        // rows as A operands, three planes each.  GDN: M1 = Gamma B1, M1^T, -(M2 + M2^T) with M2 = Gamma B2;
+        // KDA: B1 below the diagonal, its transpose, B2 and its transpose
+        uint16_t m[KDA ? 4 : 3][3][32][40];
+    };
+    float b1[32][36], b2[32][36], e[KDA ? 1 : 32][36];
+    float gt[2][KDA ? 1 : 6][32], row[NW][32], col[NW][32], corner[NW];
+};
 
-    const int tid = (int)threadIdx.x, wave = tid >> 6, l = tid & 63, n = l & 15, g = l >> 4;
+// Sixteen values of each of 16 neighbouring lanes n: lane n gets the lanes' sum of value n.
+__device__ __forceinline__ float transpose_sum16(float (&v)[16], int n) {
+#pragma unroll
+    for (int m = 8; m > 0; m >>= 1) {
+        const bool up = n & m;
+#pragma unroll
+        for (int i = 0; i < m; ++i) {
+            const float a = pick(up, v[i + m], v[i]), b = pick(up, v[i], v[i + m]);
+            v[i] = a + __shfl_xor(b, m);
+        }
+    }
+    return v[0];
+}
+
+template <int DK, int DT, bool KDA>
+__global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const ScanParams p) {
+    using Lds = GradLds<DK, DT, KDA>;
+    constexpr int NPL = Lds::NPL, NW = Lds::NW, ND = DK / 16 / NW, NTHR = NW * 64, ES = DT == SQ_DTYPE_F32 ? 4 : 2;
+    constexpr int VB = Lds::VB, VBP = Lds::VBP, LDV = Lds::LDV, OCT = VB / 8, UPT = 32 * OCT / NTHR, JOBS = (6 + NW - 1) / NW;
+    __shared__ __align__(16) Lds s;
+
+    const int tid = (int)threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int H = p.n_heads, Hk = p.n_heads_k, dv = p.dv, grp = H / Hk;
     const int hk = (int)(blockIdx.x % (unsigned)Hk);
     const int64_t slot = blockIdx.x / (unsigned)Hk;
-    int lo = 0, hi = p.n_seq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first_slot(sequence(p, mid), mid) <= slot) lo = mid;
-        else hi = mid - 1;
-    }
-    const Seq seq = sequence(p, lo);
-    const int64_t c0 = (slot - first_slot(seq, lo)) * kChunk;
-    if (c0 < 0 || c0 >= seq.len) return;             // a slot that no chunk uses (the whole workgroup leaves)
-    const int rem = (int)(seq.len - c0 < kChunk ? seq.len - c0 : kChunk);
-    const int64_t tok0 = seq.start + c0;
-    const int d = 16 * wave + n;                     // this lane's key row
-
-    float kv[2][4], qv[2][4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int tok = 16 * t + 4 * g + r;
-            kv[t][r] = tok < rem ? load1(p.k.p, p.dtype, (tok0 + tok) * p.k.stride + hk * DK + d) : 0.f;
-            qv[t][r] = tok < rem ? load1(p.q.p, p.dtype, (tok0 + tok) * p.q.stride + hk * DK + d) : 0.f;
-        }
+    const ChunkAt ck = chunk_of_slot(p, slot);
+    if (ck.rem <= 0) return;                         // a slot that no chunk uses (the whole workgroup leaves)
+    const int rem = ck.rem;
+    const int64_t tok0 = ck.tok0;
+    const uint32_t ks = (uint32_t)p.k.stride * ES, qs = (uint32_t)p.q.stride * ES;
+    const Window wk(static_cast<const char*>(p.k.p) + tok0 * ks, rem * ks), wq(static_cast<const char*>(p.q.p) + tok0 * qs, rem * qs);
+    uint32_t kraw[ND][2][4], qraw[ND][2][4];
+    auto kv = [&](int nd, int t, int r) { return val1<DT>(kraw[nd][t][r]); };
+    auto qv = [&](int nd, int t, int r) { return val1<DT>(qraw[nd][t][r]); };
     const f32x4 zero{0.f, 0.f, 0.f, 0.f};
-    f32x4 dq[2] = {zero, zero}, dk[2] = {zero, zero};
+    f32x4 dq[ND][2], dk[ND][2];
+#pragma unroll
+    for (int nd = 0; nd < ND; ++nd) dq[nd][0] = dq[nd][1] = dk[nd][0] = dk[nd][1] = zero;
     if constexpr (VB < 32) {                         // the unused half of a block of 32 value columns stays zero
-        for (int i = tid; i < 3 * 32 * LDV; i += NT) {
-            (&s_u[0][0][0])[i] = 0;
-            (&s_w[0][0][0])[i] = 0;
-            if (i < NPL * 32 * LDV) (&s_dy[0][0][0])[i] = 0;
+        for (int i = tid; i < 3 * 32 * LDV; i += NTHR) {
+            (&s.u[0][0][0])[i] = 0;
+            (&s.w[0][0][0])[i] = 0;
+            if (i < NPL * 32 * LDV) (&s.dy[0][0][0])[i] = 0;
         }
     }
 
     for (int gi = 0; gi < grp; ++gi) {
         const int h = hk * grp + gi;
-        const size_t id = (size_t)slot * H + h;
-        __syncthreads();                             // the previous head's LDS contents have been read
-        float pre[2][4], suf[2][4], al[2][4], last = 1.f;
+        const int64_t id = slot * H + h;
+        const int l = opaque(tid & 63), n = l & 15, g = l >> 4;
+        const int d0 = 16 * ND * wave + n;           // this lane's key rows: d0 + 16 nd
+        const Window ws(p.st + id * DK * dv, (uint32_t)(DK * dv) * 4), wg(p.gt + id * DK * dv, (uint32_t)(DK * dv) * 4);
+        Raw<SQ_DTYPE_F32, 4> sn[ND][2], gn[ND][2];   // the next 32 value columns of S and G
+        auto fetch_states = [&](int v0) {
+            const int at = opaque(d0 * dv + 8 * g) + v0;
+#pragma unroll
+            for (int nd = 0; nd < ND; ++nd)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t off = (at + 16 * nd * dv + 4 * i) * 4;
+                    if (VB < 32 && 8 * g >= VB) off = 0xfffffff0u;
+                    sn[nd][i].load(ws, off);
+                    gn[nd][i].load(wg, off);
+                }
+        };
+        fetch_states(0);
+        uint32_t araw[KDA ? ND : 1][2][4];
+        // k, q and the gates of this lane's key rows: needed after the products over the value columns, loaded during the last
+        auto fetch_rows = [&] {
+            const int g4 = opaque(4 * g);
+            const Window wa(p.gate + tok0 * H * (KDA ? DK : 1), KDA ? (uint32_t)rem * H * DK * 4 : 0);
+#pragma unroll
+            for (int nd = 0; nd < ND; ++nd)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t tok = 16 * t + g4 + r, c = d0 + 16 * nd;
+                        kraw[nd][t][r] = win_load1<DT>(wk, tok * ks + (hk * DK + c) * ES);
+                        qraw[nd][t][r] = win_load1<DT>(wq, tok * qs + (hk * DK + c) * ES);
+                        if constexpr (KDA) araw[KDA ? nd : 0][t][r] = win_load1<SQ_DTYPE_F32>(wa, (tok * H * DK + h * DK + c) * 4);
+                    }
+        };
+        float alpha = 1.f;
+        if (!KDA && wave == 0) {
+            const int t = l & 31;
+            alpha = t < rem ? fmaxf(p.gate[(tok0 + t) * H + h], kGateMin) : 1.f;
+        }
+        lds_barrier();                               // the previous head's LDS contents have been read
+        if (VB < 32 && gi > 0) {                     // the unused halves were overwritten by the small matrices
+            for (int i = tid; i < 3 * 32 * LDV; i += NTHR) {
+                (&s.u[0][0][0])[i] = 0;
+                (&s.w[0][0][0])[i] = 0;
+                if (i < NPL * 32 * LDV) (&s.dy[0][0][0])[i] = 0;
+            }
+            lds_barrier();
+        }
         if constexpr (!KDA) {
             if (wave == 0) {
                 const int t = l & 31;
-                const float a = t < rem ? fmaxf(p.gate[(tok0 + t) * H + h], kGateMin) : 1.f;
-                float pr = a, sf = a, x = 0.f;
+                GateLevels<float> lv(alpha);
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float up = __shfl_up(pr, o, 32), dn = __shfl_down(sf, o, 32);
-                    if (t >= o) pr *= up;
-                    if (t + o < 32) sf *= dn;
-                }
-                sf = __shfl_down(sf, 1, 32);
-                for (int i = 0; i < 32; ++i) {
-                    const float ai = __shfl(a, i, 32);
-                    x = i == t ? 1.f : x * ai;
-                    if (l < 32) s_gam[i][t] = x;
-                }
-                if (l < 32) {
-                    s_pre[t] = pr;
-                    s_suf[t] = t == 31 ? 1.f : sf;
+                for (int lev = 0; lev < 6; ++lev) {
+                    if (l < 32) {
+                        s.gt[0][lev][t] = lv.pre;
+                        s.gt[1][lev][t] = lv.suf;
+                    }
+                    if (lev < 5) lv.grow((t >> lev) & 1, __shfl_xor(lv.full, 1 << lev));
                 }
             }
-        } else {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int tok = 16 * t + 4 * g + r;
-                    al[t][r] = tok < rem ? fmaxf(p.gate[((tok0 + tok) * H + h) * DK + d], kGateMin) : 1.f;
-                }
         }
-        f32x4 x1[2] = {zero, zero}, x2[2] = {zero, zero}, x3[2] = {zero, zero}, bj[JOBS];
+        f32x4 x1[ND][2], x2[ND][2], x3[ND][2], bj[JOBS];
+#pragma unroll
+        for (int nd = 0; nd < ND; ++nd)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) x1[nd][t] = x2[nd][t] = x3[nd][t] = zero;
 #pragma unroll
         for (int j = 0; j < JOBS; ++j) bj[j] = zero;
-        float corner = 0.f, dbeta = 0.f;
-        const int oct = tid % OCT, stok = tid / OCT;             // staging: token and eight value columns of this thread
-        const bool stage = tid < 32 * OCT, slive = stage && stok < rem;
-        const float sbeta = slive ? p.beta[(tok0 + stok) * H + h] : 0.f;
+        float corner[ND] = {}, dbeta[UPT] = {};
+        const int oct = tid % OCT, stok = tid / OCT;             // staging: eight value columns of tokens stok + u NTHR / OCT
+        const uint32_t ds = (uint32_t)p.dy.stride * ES, es = (uint32_t)H * dv * 4;
+        const Window wy(static_cast<const char*>(p.dy.p) + tok0 * ds, rem * ds), we(p.e + tok0 * H * dv, rem * es),
+            wu(p.du + tok0 * H * dv, rem * es), wb(p.beta + tok0 * H, (uint32_t)rem * H * 4);
+        float sbeta[UPT];
+#pragma unroll
+        for (int u = 0; u < UPT; ++u)
+            sbeta[u] = __uint_as_float(win_load1<SQ_DTYPE_F32>(wb, ((stok + u * (NTHR / OCT)) * H + h) * 4));
         for (int vb = 0; vb < dv; vb += VB) {
-            if (vb) __syncthreads();
-            if (stage) {
+            constexpr int RW = DT == SQ_DTYPE_F32 ? 2 : 1;
+            Raw<DT, 8 / RW> yr[UPT][RW];
+            Raw<SQ_DTYPE_F32, 4> er[UPT][2], ur[UPT][2];
+#pragma unroll
+            for (int u = 0; u < UPT; ++u) {
+                const uint32_t tok = stok + u * (NTHR / OCT), c = h * dv + vb + 8 * oct;
+#pragma unroll
+                for (int i = 0; i < RW; ++i) yr[u][i].load(wy, tok * ds + (c + 4 * i) * ES);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    er[u][i].load(we, tok * es + (c + 4 * i) * 4);
+                    ur[u][i].load(wu, tok * es + (c + 4 * i) * 4);
+                }
+            }
+            if (vb) lds_barrier();
+#pragma unroll
+            for (int u = 0; u < UPT; ++u) {
+                const int tok = stok + u * (NTHR / OCT);
                 float y8[8], e8[8], u8[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y8[j] = e8[j] = u8[j] = 0.f;
-                if (slive) {
-                    const int64_t at = ((tok0 + stok) * H + h) * dv + vb + 8 * oct;
-                    load8(p.dy.p, p.dtype, (tok0 + stok) * p.dy.stride + (int64_t)h * dv + vb + 8 * oct, y8);
-                    load8(p.e, SQ_DTYPE_F32, at, e8);
-                    load8(p.du, SQ_DTYPE_F32, at, u8);
-                }
-#pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    dbeta = fmaf(e8[j], u8[j], dbeta);
-                    e8[j] *= sbeta;
-                    u8[j] *= sbeta;
+                    y8[j] = RW == 2 ? yr[u][RW - 1 ? j >> 2 : 0].at(j & 3) : yr[u][0].at(j);
+                    e8[j] = er[u][j >> 2].at(j & 3);
+                    u8[j] = ur[u][j >> 2].at(j & 3);
+                    dbeta[u] = fmaf(e8[j], u8[j], dbeta[u]);
+                    e8[j] *= sbeta[u];
+                    u8[j] *= sbeta[u];
                 }
                 const Frag<NPL> fy = split8<NPL>(y8);
                 const Frag<3> fu = split8<3>(e8), fw = split8<3>(u8);
 #pragma unroll
+                for (int i = 0; i < NPL; ++i) *reinterpret_cast<u32x4v*>(&s.dy[i][tok][8 * oct]) = fy.p[i];
+#pragma unroll
                 for (int i = 0; i < 3; ++i) {
-                    if (i < NPL) *reinterpret_cast<u32x4v*>(&s_dy[i < NPL ? i : 0][stok][8 * oct]) = fy.p[i < NPL ? i : 0];
-                    *reinterpret_cast<u32x4v*>(&s_u[i][stok][8 * oct]) = fu.p[i];
-                    *reinterpret_cast<u32x4v*>(&s_w[i][stok][8 * oct]) = fw.p[i];
+                    *reinterpret_cast<u32x4v*>(&s.u[i][tok][8 * oct]) = fu.p[i];
+                    *reinterpret_cast<u32x4v*>(&s.w[i][tok][8 * oct]) = fw.p[i];
                 }
             }
-            __syncthreads();
-#pragma unroll
+            lds_barrier();
+#pragma unroll 1
             for (int kb = 0; kb < VBP / 32; ++kb) {
-                auto frag = [&](auto& arr, int t) {
-                    constexpr int N = sizeof(arr) / (32 * LDV * 2);
-                    Frag<N> f;
+                __builtin_amdgcn_sched_barrier(0);
+                Raw<SQ_DTYPE_F32, 4> sc[ND][2], gc[ND][2];
 #pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        f.p[i] = *reinterpret_cast<const u32x4v*>(&arr[i][16 * t + n][32 * kb + 8 * g]);
-                    return f;
-                };
-                float sv[8], gv[8];
+                for (int nd = 0; nd < ND; ++nd)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sv[j] = gv[j] = 0.f;
-                if (32 * kb + 8 * g < VB) {
-                    const int64_t at = ((int64_t)id * DK + d) * dv + vb + 32 * kb + 8 * g;
-                    load8(p.st, SQ_DTYPE_F32, at, sv);
-                    load8(p.gt, SQ_DTYPE_F32, at, gv);
+                    for (int i = 0; i < 2; ++i) {
+                        sc[nd][i] = sn[nd][i];
+                        gc[nd][i] = gn[nd][i];
+                    }
+                const int v1 = vb + 32 * (kb + 1);
+                if (v1 < dv) fetch_states(v1);
+                else fetch_rows();
+                const int off = n * LDV + 32 * kb + 8 * g;
+                {
+                    Frag<3> f[ND];
+#pragma unroll
+                    for (int nd = 0; nd < ND; ++nd) {
+                        float v[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            v[j] = sc[nd][j >> 2].at(j & 3);
+                            corner[nd] = fmaf(v[j], gc[nd][j >> 2].at(j & 3), corner[nd]);
+                        }
+                        f[nd] = split8<3>(v);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const Frag<NPL> fy = lds_frag<NPL>(&s.dy[0][0][0], 32 * LDV, off + 16 * t * LDV);
+#pragma unroll
+                        for (int nd = 0; nd < ND; ++nd) mma(x1[nd][t], fy, f[nd]);
+                        const Frag<3> fw = lds_frag<3>(&s.w[0][0][0], 32 * LDV, off + 16 * t * LDV);
+#pragma unroll
+                        for (int nd = 0; nd < ND; ++nd) mma(x2[nd][t], fw, f[nd]);
+                    }
                 }
+                __builtin_amdgcn_sched_barrier(0);   // keeps the registers of the two halves apart
+                {
+                    Frag<3> f[ND];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) corner = fmaf(sv[j], gv[j], corner);
-                const Frag<3> sf = split8<3>(sv), gf = split8<3>(gv);
+                    for (int nd = 0; nd < ND; ++nd) {
+                        float v[8];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    mma(x1[t], frag(s_dy, t), sf);
-                    mma(x2[t], frag(s_w, t), sf);
-                    mma(x3[t], frag(s_u, t), gf);
+                        for (int j = 0; j < 8; ++j) v[j] = gc[nd][j >> 2].at(j & 3);
+                        f[nd] = split8<3>(v);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const Frag<3> fu = lds_frag<3>(&s.u[0][0][0], 32 * LDV, off + 16 * t * LDV);
+#pragma unroll
+                        for (int nd = 0; nd < ND; ++nd) mma(x3[nd][t], fu, f[nd]);
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < JOBS; ++j) {
-                    const int jb = wave + NW * j;                // tiles (0,0), (1,0), (1,1) of B1, then of B2
+                    const int jb = wave + NW * j;                // tiles (0,0), (1,0), (1,1) of B2, then of B1
                     if (jb < 6) {
                         const int tl = jb % 3, ti = tl > 0, tj = tl > 1;
-                        const Frag<3> uf = frag(s_u, tj);
-                        if (jb < 3) mma(bj[j], frag(s_dy, ti), uf);
-                        else mma(bj[j], frag(s_w, ti), uf);
+                        const Frag<3> fu = lds_frag<3>(&s.u[0][0][0], 32 * LDV, off + 16 * tj * LDV);
+                        const int oi = off + 16 * ti * LDV;
+                        if (jb < 3) mma(bj[j], lds_frag<3>(&s.w[0][0][0], 32 * LDV, oi), fu);
+                        else mma(bj[j], lds_frag<NPL>(&s.dy[0][0][0], 32 * LDV, oi), fu);
                     }
                 }
             }
         }
-        if (stage) {
 #pragma unroll
-            for (int o = 1; o < OCT; o <<= 1) dbeta += __shfl_xor(dbeta, o);
-            if (slive && oct == 0) p.dbeta[(tok0 + stok) * H + h] = dbeta;
+        for (int u = 0; u < UPT; ++u) {
+#pragma unroll
+            for (int o = 1; o < OCT; o <<= 1) dbeta[u] += __shfl_xor(dbeta[u], o);
+            const int tok = stok + u * (NTHR / OCT);
+            if (oct == 0 && tok < rem) p.dbeta[(tok0 + tok) * H + h] = dbeta[u];
         }
 #pragma unroll
         for (int j = 0; j < JOBS; ++j) {
             const int jb = wave + NW * j;
             if (jb < 6) {
                 const int tl = jb % 3, ti = tl > 0, tj = tl > 1;
-                float(&out)[32][36] = jb < 3 ? s_b1 : s_b2;
+                float(&out)[32][36] = jb < 3 ? s.b2 : s.b1;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) out[16 * ti + 4 * g + r][16 * tj + n] = bj[j][r];
             }
         }
+        constexpr int MPT = 256 / NTHR;              // units (row, four columns) per thread
         if constexpr (!KDA) {
             // sums over the key rows of the terms with the chunk's first state and last gradient
-            float rowv[2][4], colv[2][4];
+            float sums[16];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    rowv[t][r] = qv[t][r] * x1[t][r] - kv[t][r] * x2[t][r];
-                    colv[t][r] = kv[t][r] * x3[t][r];
+                    float a = 0.f, c = 0.f;
 #pragma unroll
-                    for (int o = 1; o < 16; o <<= 1) {
-                        rowv[t][r] += __shfl_xor(rowv[t][r], o);
-                        colv[t][r] += __shfl_xor(colv[t][r], o);
+                    for (int nd = 0; nd < ND; ++nd) {
+                        a += qv(nd, t, r) * x1[nd][t][r] - kv(nd, t, r) * x2[nd][t][r];
+                        c += kv(nd, t, r) * x3[nd][t][r];
                     }
-                    if (n == 0) {
-                        s_row[wave][16 * t + 4 * g + r] = rowv[t][r];
-                        s_col[wave][16 * t + 4 * g + r] = colv[t][r];
-                    }
+                    sums[4 * t + r] = a;
+                    sums[8 + 4 * t + r] = c;
                 }
+            const float mine = transpose_sum16(sums, n);
+            (n < 8 ? s.row : s.col)[wave][16 * ((n >> 2) & 1) + 4 * g + (n & 3)] = mine;
+            float cor = 0.f;
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) corner += __shfl_xor(corner, o);
-            if (l == 0) s_corner[wave] = corner;
-            __syncthreads();
+            for (int nd = 0; nd < ND; ++nd) cor += corner[nd];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int o = 1; o < 64; o <<= 1) cor += __shfl_xor(cor, o);
+            if (l == 0) s.corner[wave] = cor;
+        }
+        lds_barrier();
+        // the small matrices as A operands, over the staged rows
+#pragma unroll 1
+        for (int u = 0; u < MPT; ++u) {
+            const int i = (tid + u * NTHR) >> 3, j0 = 4 * ((tid + u * NTHR) & 7);
+            if constexpr (!KDA) {
+                const float* ap = p.mat_ap + id * 2048 + i * 32 + j0;
+                const f32x4 a4 = *reinterpret_cast<const f32x4*>(ap), p4 = *reinterpret_cast<const f32x4*>(ap + 1024);
+                float m1[4], mt[4], ms[4];
+                f32x4 e4;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    pre[t][r] = s_pre[16 * t + 4 * g + r];
-                    suf[t][r] = s_suf[16 * t + 4 * g + r];
+                for (int c = 0; c < 4; ++c) {
+                    const int j = j0 + c, hi = i > j ? i : j, lo = i > j ? j : i;
+                    const int lev = i == j ? 0 : 31 - __builtin_clz(i ^ j);
+                    const float gm = i == j ? 1.f : s.gt[0][lev][hi] * s.gt[1][lev][lo];
+                    const float v1 = s.b1[hi][lo], v2 = s.b2[hi][lo];
+                    m1[c] = j <= i ? v1 * gm : 0.f;
+                    mt[c] = j >= i ? v1 * gm : 0.f;
+                    ms[c] = i == j ? 0.f : -v2 * gm;
+                    e4[c] = j < i ? p4[c] * v1 - a4[c] * v2 : 0.f;
                 }
-            const float* ap = p.mat_ap + id * 2048;
-            for (int i = tid; i < 1024; i += NT) {   // E below the diagonal; B1 and B2 times Gamma, zero above it
-                const int a = i >> 5, c = i & 31;
-                const float gm = s_gam[a][c], b1 = c <= a ? s_b1[a][c] : 0.f, b2 = c < a ? s_b2[a][c] : 0.f;
-                s_e[a][c] = c < a ? ap[1024 + i] * b1 - ap[i] * b2 : 0.f;
-                s_b1[a][c] = b1 * gm;
-                s_b2[a][c] = b2 * gm;
+                *reinterpret_cast<f32x4*>(&s.e[i][j0]) = e4;
+                u32x2 w[3];
+                auto put = [&](int which, const float* v) {
+                    split4<3>(v, w);
+#pragma unroll
+                    for (int pl = 0; pl < 3; ++pl) *reinterpret_cast<u32x2*>(&s.m[which][pl][i][kpos(j0)]) = w[pl];
+                };
+                put(0, m1);
+                put(1, mt);
+                put(2, ms);
+            } else {
+                float m[4][4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int j = j0 + c, hi = i > j ? i : j, lo = i > j ? j : i;
+                    const float v1 = s.b1[hi][lo], v2 = s.b2[hi][lo];
+                    m[0][c] = j < i ? v1 : 0.f;
+                    m[1][c] = j > i ? v1 : 0.f;
+                    m[2][c] = j < i ? v2 : 0.f;
+                    m[3][c] = j > i ? v2 : 0.f;
+                }
+                u32x2 w[3];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    split4<3>(m[q], w);
+#pragma unroll
+                    for (int pl = 0; pl < 3; ++pl) *reinterpret_cast<u32x2*>(&s.m[KDA ? q : 0][pl][i][kpos(j0)]) = w[pl];
+                }
             }
-            __syncthreads();
-            const Frag<3> kf = split8<3>(&kv[0][0]), qf = split8<3>(&qv[0][0]);
+        }
+        lds_barrier();
+        auto mfrag = [&](int which, int t) { return lds_frag<3>(&s.m[which][0][0][0], 32 * 40, (16 * t + n) * 40 + 8 * g); };
+        if constexpr (!KDA) {
+            float pre[2][4], suf[2][4];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float m1[8], m1t[8], ms[8];
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    pre[t][r] = s.gt[0][5][16 * t + 4 * g + r];
+                    suf[t][r] = s.gt[1][5][16 * t + 4 * g + r];
+                }
+            Frag<NPL> kf[ND], qf[ND];
+#pragma unroll
+            for (int nd = 0; nd < ND; ++nd) {
+                float k8[8], q8[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int i = 16 * t + n, j = 16 * (e >> 2) + 4 * g + (e & 3);
-                    m1[e] = s_b1[i][j];
-                    m1t[e] = s_b1[j][i];
-                    ms[e] = -(s_b2[i][j] + s_b2[j][i]);          // one of the two is zero
+                    k8[e] = kv(nd, e >> 2, e & 3);
+                    q8[e] = qv(nd, e >> 2, e & 3);
                 }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    dq[t][r] = fmaf(pre[t][r], x1[t][r], dq[t][r]);
-                    dk[t][r] += suf[t][r] * x3[t][r] - pre[t][r] * x2[t][r];
-                }
-                mma(dq[t], split8<3>(m1), kf);
-                mma(dk[t], split8<3>(m1t), qf);
-                mma(dk[t], split8<3>(ms), kf);
+                kf[nd] = split8<NPL>(k8);
+                qf[nd] = split8<NPL>(q8);
             }
-            if (wave == 0 && l < 32) {
-                float row = 0.f, colt = 0.f, cor = 0.f;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) { row += s_row[w][l]; colt += s_col[w][l]; cor += s_corner[w]; }
-                row *= s_pre[l];
-                colt *= s_suf[l];
-                cor *= s_pre[31];
-                // row l: sums of E over the columns before each t, with the row's own term
-                float f = row;
-                for (int t = 0; t < 32; ++t) {
-                    const float e = s_e[l][t];
-                    s_e[l][t] = f;
-                    f += e;
-                }
-                s_col[0][l] = colt;
-                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-                float a = cor;
-                for (int i = 0; i < 32; ++i) {
-                    if (i >= l) a += s_e[i][l];
-                    else a += s_col[0][i];
-                }
-                if (l < rem) {
-                    const float alpha = fmaxf(p.gate[(tok0 + l) * H + h], kGateMin);
-                    p.dgate[(tok0 + l) * H + h] = a / alpha;
-                }
-            }
-        } else {
-            corner += __shfl_xor(corner, 16);
-            corner += __shfl_xor(corner, 32);
-            __syncthreads();
-            float full[2][4], dlog[2][4];
+            for (int t = 0; t < 2; ++t) {
+                const Frag<3> m1 = mfrag(0, t), mt = mfrag(1, t), ms = mfrag(2, t);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    pre[t][r] = full[t][r] = al[t][r];
-                    suf[t][r] = 1.f;
-                    dlog[t][r] = 0.f;
-                    const int tok = 16 * t + 4 * g + r;          // the diagonal has no gate
-                    const float b = s_b1[tok][tok];
-                    dq[t][r] = fmaf(b, kv[t][r], dq[t][r]);
-                    dk[t][r] = fmaf(b, qv[t][r], dk[t][r]);
-                }
-            // Pairs by the highest differing bit of their tokens (see k_prep): at level lev the rows of odd blocks of 2^lev
-            // tokens meet the columns of the even block before.
-            auto level = [&](auto tag) {
-                constexpr int LEV = decltype(tag)::value;
-                float kc[8], qr[8], kr[8];
-                bool odd[2][4];
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int nd = 0; nd < ND; ++nd) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        odd[t][r] = ((16 * t + 4 * g + r) >> LEV) & 1;
-                        kc[4 * t + r] = odd[t][r] ? 0.f : kv[t][r] * suf[t][r];
-                        qr[4 * t + r] = odd[t][r] ? qv[t][r] * pre[t][r] : 0.f;
-                        kr[4 * t + r] = odd[t][r] ? -kv[t][r] * pre[t][r] : 0.f;
+                        dq[nd][t][r] = fmaf(pre[t][r], x1[nd][t][r], dq[nd][t][r]);
+                        dk[nd][t][r] += suf[t][r] * x3[nd][t][r] - pre[t][r] * x2[nd][t][r];
                     }
-                const Frag<3> fc = split8<3>(kc), fq = split8<3>(qr), fr = split8<3>(kr);
-                float rowv[2][4], colv[2][4];
+                    mma(dq[nd][t], m1, kf[nd]);
+                    mma(dk[nd][t], mt, qf[nd]);
+                    mma(dk[nd][t], ms, kf[nd]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (wave == 0) {
+                // Sums of E over j < t: a product with the matrix of ones above the diagonal; then over i >= t
+                Frag<3> ef[2];
+                Frag<1> ones[2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    float r1[8], r2[8], c1[8], c2[8];
+                    float v[8];
+                    const f32x4 lo = *reinterpret_cast<const f32x4*>(&s.e[16 * t + n][8 * g]);
+                    const f32x4 hi = *reinterpret_cast<const f32x4*>(&s.e[16 * t + n][8 * g + 4]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int i = 16 * t + n, j = 16 * (e >> 2) + 4 * g + (e & 3);
-                        const bool pair = ((i ^ j) >> LEV) == 1;
-                        const bool lower = pair && j < i, upper = pair && j > i;
-                        r1[e] = lower ? s_b1[i][j] : 0.f;
-                        r2[e] = lower ? s_b2[i][j] : 0.f;
-                        c1[e] = upper ? s_b1[j][i] : 0.f;
-                        c2[e] = upper ? s_b2[j][i] : 0.f;
-                    }
-                    f32x4 d1 = zero, d2 = zero, d3 = zero;
-                    mma(d1, split8<3>(r1), fc);
-                    mma(d2, split8<3>(r2), fc);
-                    mma(d3, split8<3>(c1), fq);
-                    mma(d3, split8<3>(c2), fr);
+                    for (int j = 0; j < 4; ++j) { v[j] = lo[j]; v[4 + j] = hi[j]; }
+                    ef[t] = split8<3>(v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = 8 * g + j < 16 * t + n ? 1.f : 0.f;
+                    ones[t] = split8<1>(v);
+                }
+                float out[2] = {0.f, 0.f}, cor = 0.f;
+                const float last = s.gt[0][5][31];
+#pragma unroll
+                for (int w = 0; w < NW; ++w) cor += s.corner[w];
+#pragma unroll
+                for (int ti = 0; ti < 2; ++ti) {
+                    float row[4], col[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float a = pre[t][r] * d1[r], b = pre[t][r] * d2[r], c = suf[t][r] * d3[r];
-                        if (odd[t][r]) {
-                            dq[t][r] += a;
-                            dk[t][r] -= b;
-                        } else {
-                            dk[t][r] += c;
-                        }
-                        rowv[t][r] = odd[t][r] ? qv[t][r] * a - kv[t][r] * b : 0.f;
-                        colv[t][r] = odd[t][r] ? 0.f : kv[t][r] * c;
+                        const int i = 16 * ti + 4 * g + r;
+                        row[r] = col[r] = 0.f;
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) { row[r] += s.row[w][i]; col[r] += s.col[w][i]; }
+                        row[r] *= pre[ti][r];
+                        col[r] *= suf[ti][r];
+                    }
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt) {
+                        f32x4 f = zero;
+                        mma(f, ef[ti], ones[tt]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) out[tt] += pick(16 * ti + 4 * g + r >= 16 * tt + n, f[r] + row[r], col[r]);
                     }
                 }
-                suffix_in<LEV>(rowv, g);
-                prefix_before<LEV>(colv, g);
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt) {
+                    out[tt] += __shfl_xor(out[tt], 16);
+                    out[tt] += __shfl_xor(out[tt], 32);
+                }
+                // lane t < 32 holds the gate of token t and writes its gradient
+                if (l < rem) p.dgate[(tok0 + l) * H + h] = (pick(l < 16, out[0], out[1]) + cor * last) / alpha;
+            }
+        } else {
+            // Pairs by the highest differing bit of their tokens (see k_prep): at level lev the rows of odd blocks of 2^lev
+            // tokens meet the columns of the even block before.
+            float dlog[ND][2][4], al[2][4];
+            GateLevels<float> lv[2][4];
+            auto gates = [&](int nd) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) dlog[t][r] += odd[t][r] ? rowv[t][r] : colv[t][r];
-                // blocks of twice the size
+                    for (int r = 0; r < 4; ++r) {
+                        al[t][r] = 16 * t + 4 * g + r < rem ? fmaxf(__uint_as_float(araw[KDA ? nd : 0][t][r]), kGateMin) : 1.f;
+                        lv[t][r] = GateLevels<float>(al[t][r]);
+                    }
+            };
+            auto odd = [&](int lev, int t, int r) { return ((16 * t + 4 * g + r) >> lev) & 1; };
+            auto grow = [&](auto tag) {              // from blocks of 2^LEV tokens to twice that
+                constexpr int LEV = decltype(tag)::value;
                 float other[2][4];
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        if constexpr (LEV < 2) other[t][r] = full[t][r ^ (1 << LEV)];
-                        else if constexpr (LEV < 4) other[t][r] = __shfl_xor(full[t][r], 4 << LEV);
-                        else other[t][r] = full[t ^ 1][r];
+                        if constexpr (LEV < 2) other[t][r] = lv[t][r ^ (1 << (LEV & 1))].full;
+                        else if constexpr (LEV < 4) other[t][r] = __shfl_xor(lv[t][r].full, 4 << LEV);
+                        else other[t][r] = lv[t ^ 1][r].full;
                     }
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if (odd[t][r]) pre[t][r] *= other[t][r];
-                        else suf[t][r] *= other[t][r];
-                        full[t][r] *= other[t][r];
-                    }
+                    for (int r = 0; r < 4; ++r) lv[t][r].grow(odd(LEV, t, r), other[t][r]);
             };
-            level(std::integral_constant<int, 0>{});
-            level(std::integral_constant<int, 1>{});
-            level(std::integral_constant<int, 2>{});
-            level(std::integral_constant<int, 3>{});
-            level(std::integral_constant<int, 4>{});
-            last = full[0][0];
-            float rowv[2][4], colv[2][4];
+            // the terms with the chunk's first state and last gradient, and the diagonal (which has no gate)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int nd = 0; nd < ND; ++nd) {
+                gates(nd);
+                grow(std::integral_constant<int, 0>{});
+                grow(std::integral_constant<int, 1>{});
+                grow(std::integral_constant<int, 2>{});
+                grow(std::integral_constant<int, 3>{});
+                grow(std::integral_constant<int, 4>{});
+                float cor = corner[nd], rowv[2][4], colv[2][4];
+                cor += __shfl_xor(cor, 16);
+                cor += __shfl_xor(cor, 32);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float a = pre[t][r] * x1[t][r], b = pre[t][r] * x2[t][r], c = suf[t][r] * x3[t][r];
-                    dq[t][r] += a;
-                    dk[t][r] += c - b;
-                    rowv[t][r] = qv[t][r] * a - kv[t][r] * b;
-                    colv[t][r] = kv[t][r] * c;
-                }
-            suffix_in<5>(rowv, g);
-            prefix_before<5>(colv, g);
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                    for (int r = 0; r < 4; ++r) {
+                        const float a = lv[t][r].pre * x1[nd][t][r], b = lv[t][r].pre * x2[nd][t][r];
+                        const float c = lv[t][r].suf * x3[nd][t][r], e = s.b1[16 * t + 4 * g + r][16 * t + 4 * g + r];
+                        dq[nd][t][r] += fmaf(e, kv(nd, t, r), a);
+                        dk[nd][t][r] += fmaf(e, qv(nd, t, r), c - b);
+                        rowv[t][r] = qv(nd, t, r) * a - kv(nd, t, r) * b;
+                        colv[t][r] = kv(nd, t, r) * c;
+                    }
+                suffix_in<5>(rowv, g);
+                prefix_before<5>(colv, g);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int tok = 16 * t + 4 * g + r;
-                    if (tok < rem)
-                        p.dgate[((tok0 + tok) * H + h) * DK + d] =
-                            (dlog[t][r] + rowv[t][r] + colv[t][r] + last * corner) / al[t][r];
-                }
-        }
-    }
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+                    for (int r = 0; r < 4; ++r) dlog[nd][t][r] = rowv[t][r] + colv[t][r] + lv[0][0].full * cor;
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int tok = 16 * t + 4 * g + r;
-            if (tok < rem) {
-                store1(p.dq.p, p.dtype, (tok0 + tok) * p.dq.stride + hk * DK + d, dq[t][r]);
-                store1(p.dkk.p, p.dtype, (tok0 + tok) * p.dkk.stride + hk * DK + d, dk[t][r]);
+            for (int nd = 0; nd < ND; ++nd) {
+                gates(nd);
+                auto level = [&](auto tag) {
+                    constexpr int LEV = decltype(tag)::value;
+                    // rows come from odd blocks only, columns from even ones: the masks of the matrices leave nothing else
+                    float kc[8], qr[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int t = e >> 2, r = e & 3;
+                        kc[e] = kv(nd, t, r) * pick(odd(LEV, t, r), -lv[t][r].pre, lv[t][r].suf);
+                        qr[e] = qv(nd, t, r) * lv[t][r].pre;
+                    }
+                    const Frag<3> fc = split8<3>(kc), fq = split8<3>(qr);
+                    // which columns of this lane's row pair with it at this level: within its own 16 tokens below
+                    // level 4, all of the other 16 at level 4
+                    const int y = n ^ (4 * g);
+                    auto on = [&](int r) { return ((y ^ r) >> (LEV < 4 ? LEV : 0)) == 1; };
+                    const uint32_t k0 = (on(0) ? 0xffffu : 0u) | (on(1) ? 0xffff0000u : 0u);
+                    const uint32_t k1 = (on(2) ? 0xffffu : 0u) | (on(3) ? 0xffff0000u : 0u);
+                    auto frag = [&](int which, int t) {
+                        Frag<3> f = mfrag(which, t);
+#pragma unroll
+                        for (int pl = 0; pl < 3; ++pl) {
+                            const int keep = LEV < 4 ? t : 1 - t;
+                            f.p[pl][2 * keep] &= LEV < 4 ? k0 : ~0u;
+                            f.p[pl][2 * keep + 1] &= LEV < 4 ? k1 : ~0u;
+                            f.p[pl][2 * (1 - keep)] = f.p[pl][2 * (1 - keep) + 1] = 0;
+                        }
+                        return f;
+                    };
+                    float rowv[2][4], colv[2][4];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        f32x4 da = zero, db = zero, dc = zero;
+                        if (LEV < 4 || t == 1) {
+                            mma(da, frag(0, t), fc);
+                            mma(db, frag(KDA ? 2 : 0, t), fc);
+                        }
+                        if (LEV < 4 || t == 0) {
+                            mma(dc, frag(1, t), fq);
+                            mma(dc, frag(KDA ? 3 : 0, t), fc);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float a = lv[t][r].pre * da[r], b = lv[t][r].pre * db[r], c = lv[t][r].suf * dc[r];
+                            const bool o = odd(LEV, t, r);
+                            dq[nd][t][r] += o ? a : 0.f;
+                            dk[nd][t][r] += o ? -b : c;
+                            rowv[t][r] = o ? qv(nd, t, r) * a - kv(nd, t, r) * b : 0.f;
+                            colv[t][r] = o ? 0.f : kv(nd, t, r) * c;
+                        }
+                    }
+                    suffix_in<LEV>(rowv, g);
+                    prefix_before<LEV>(colv, g);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) dlog[nd][t][r] += pick(odd(LEV, t, r), rowv[t][r], colv[t][r]);
+                    if constexpr (LEV < 4) grow(tag);
+                    __builtin_amdgcn_sched_barrier(0);
+                };
+                level(std::integral_constant<int, 0>{});
+                level(std::integral_constant<int, 1>{});
+                level(std::integral_constant<int, 2>{});
+                level(std::integral_constant<int, 3>{});
+                level(std::integral_constant<int, 4>{});
+                const Window wo(p.dgate + tok0 * H * DK, (uint32_t)rem * H * DK * 4);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        win_store1<SQ_DTYPE_F32>(wo, ((16 * t + 4 * g + r) * H * DK + h * DK + d0 + 16 * nd) * 4,
+                                                 dlog[nd][t][r] / al[t][r]);
             }
         }
+    }
+    const int l = tid & 63, n = l & 15, g = l >> 4, d0 = 16 * ND * wave + n;
+    const uint32_t os = (uint32_t)p.dq.stride * ES, oks = (uint32_t)p.dkk.stride * ES;
+    const Window wdq(static_cast<const char*>(p.dq.p) + tok0 * os, rem * os);
+    const Window wdk(static_cast<const char*>(p.dkk.p) + tok0 * oks, rem * oks);
+#pragma unroll
+    for (int nd = 0; nd < ND; ++nd)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t c = (hk * DK + d0 + 16 * nd) * ES;
+                win_store1<DT>(wdq, (16 * t + 4 * g + r) * os + c, dq[nd][t][r]);
+                win_store1<DT>(wdk, (16 * t + 4 * g + r) * oks + c, dk[nd][t][r]);
+            }
 }
 
 template <int DK, int DT, bool KDA>
 static hipError_t grad_t(const ScanParams& p, hipStream_t s) {
-    constexpr int NPL = DT == SQ_DTYPE_BF16 ? 1 : DT == SQ_DTYPE_F16 ? 2 : 3;
     const int64_t blocks = p.n_slots * p.n_heads_k;
-    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-    k_grad<DK, NPL, KDA><<<dim3((unsigned)blocks), dim3(DK * 4), 0, s>>>(p);
+    if (blocks > 0x7fffffff || p.dv % DK != 0) return hipErrorInvalidValue;
+    k_grad<DK, DT, KDA><<<dim3((unsigned)blocks), dim3(DK >= 64 ? 2 * DK : 64), 0, s>>>(p);
     return hipGetLastError();
 }
 

@@ -51,6 +51,17 @@ __device__ __forceinline__ Frag<N> split8(const float* x) {
     return f;
 }
 
+// A choice between two values (a ?: of two array elements is a choice of their addresses, which takes an array out of the
+// registers).
+__device__ __forceinline__ float pick(bool c, float a, float b) { return c ? a : b; }
+
+// The value, of which the compiler knows nothing: addresses formed from it are formed where they are used and not kept in
+// registers over a loop.
+__device__ __forceinline__ int opaque(int x) {
+    __asm__ volatile("" : "+v"(x));
+    return x;
+}
+
 // Four elements: the dwords of plane n.
 template <int N>
 __device__ __forceinline__ void split4(const float* x, u32x2* out) {
