@@ -297,7 +297,7 @@ sq_status sq_valu_probe(int32_t waves_per_simd, int32_t n_blocks, float* d_out, 
  * matrix units with every float32 operand split into three exact parts), each output rounded once.
  * d_gate: alpha in [0, 1], [n_tokens][n_heads] (GDN) or [n_tokens][n_heads][d_k] (KDA); d_beta
  * [n_tokens][n_heads].  (The gradients of q, k and gate count gates below 1e-30 as 1e-30.)
- * Alignment: q, k and dy 16 bytes, with stride * element size a multiple of 16; d_gate (KDA) 16 bytes;
+ * Alignment: row arrays 16 bytes, with stride * element size a multiple of 16; d_gate (KDA) 16 bytes;
  * the workspace 256 bytes.  Strides at least heads * d and below 2^24 elements.
  * d_s0 and d_s1 may be the same array; no other two arrays may overlap.
  *

@@ -24,7 +24,7 @@ static bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintp
 namespace {
 
 struct ScanWork {                    // byte offsets of the workspace's parts
-    size_t th, p, gb, tt, pt, ap, e, du, st, gt, total;
+    size_t mf, gb, mr, ap, e, du, st, gt, total;
 };
 
 ScanWork scan_work(const sq_scan_cfg& c, bool backward) {
@@ -32,14 +32,11 @@ ScanWork scan_work(const sq_scan_cfg& c, bool backward) {
     size_t at = 0;
     auto take = [&at](size_t bytes) { const size_t o = at; at += (bytes + 255) & ~size_t(255); return o; };
     const size_t mats = size_t(scan_slots(c.n_tokens, c.n_seq)) * size_t(c.n_heads);
-    const size_t vals = size_t(c.n_tokens) * size_t(c.n_heads) * size_t(c.d_v) * 4;
-    w.th = take(mats * kMatShorts * 2);
+    const size_t vals = mats * kChunk * size_t(c.d_v) * 4;
+    w.mf = take(mats * kMatShorts * (backward ? 2 : 4));
     if (c.form == SQ_FORM_GDN) w.gb = take(mats * 2 * kChunk * 4);
-    if (!backward) {
-        w.p = take(mats * kMatShorts * 2);
-    } else {
-        w.tt = take(mats * kMatShorts * 2);
-        w.pt = take(mats * kMatShorts * 2);
+    if (backward) {
+        w.mr = take(mats * kMatShorts * 4);
         if (c.form == SQ_FORM_GDN) w.ap = take(mats * 2 * kChunk * kChunk * 4);
         w.e = take(vals);
         w.du = take(vals);
@@ -74,12 +71,12 @@ sq_status check_scan_cfg(const sq_scan_cfg* c) {
     return SQ_OK;
 }
 
-// A row array of `heads` x d elements of type dt per token; `wide`: read 16 bytes at a time.
-sq_status check_rows(const sq_rows* a, const char* name, int64_t heads, int64_t d, int32_t dt, bool wide) {
+// A row array of `heads` x d elements of type dt per token (accessed up to 16 bytes at a time).
+sq_status check_rows(const sq_rows* a, const char* name, int64_t heads, int64_t d, int32_t dt) {
     if (!a || !a->d_ptr) { set_error("%s is NULL", name); return SQ_ERR_ARG; }
     if (a->stride < heads * d) { set_error("%s: stride %lld below %lld", name, (long long)a->stride, (long long)(heads * d)); return SQ_ERR_SHAPE; }
     if (a->stride >= (int64_t(1) << 24)) { set_error("%s: stride %lld, below 2^24 elements is supported", name, (long long)a->stride); return SQ_ERR_SHAPE; }
-    if (!aligned(a->d_ptr, wide ? 16 : uintptr_t(esize(dt))) || (wide && a->stride * esize(dt) % 16 != 0)) {
+    if (!aligned(a->d_ptr, 16) || a->stride * esize(dt) % 16 != 0) {
         set_error("%s: address and stride must be multiples of 16 bytes", name);
         return SQ_ERR_ARG;
     }
@@ -107,12 +104,10 @@ ScanParams scan_params(const sq_scan_cfg& c, const ScanWork& w, void* work, bool
     char* base = static_cast<char*>(work);
     auto u16 = [base](size_t o) { return reinterpret_cast<uint16_t*>(base + o); };
     auto f32 = [base](size_t o) { return reinterpret_cast<float*>(base + o); };
-    p.mat_th = u16(w.th);
+    p.mat_f = u16(w.mf);
     p.mat_gb = f32(w.gb);
-    if (!backward) {
-        p.mat_p = u16(w.p);
-    } else {
-        p.mat_tt = u16(w.tt); p.mat_pt = u16(w.pt); p.mat_ap = f32(w.ap);
+    if (backward) {
+        p.mat_r = u16(w.mr); p.mat_ap = f32(w.ap);
         p.e = f32(w.e); p.du = f32(w.du); p.st = f32(w.st); p.gt = f32(w.gt);
     }
     return p;
@@ -137,9 +132,9 @@ static sq_status check_scan(const sq_scan_cfg* cfg, const sq_rows* q, const sq_r
     if (*empty) return SQ_OK;
     if (!cfg->d_seq_start && cfg->n_seq != 1) { set_error("d_seq_start is NULL with %d sequences", cfg->n_seq); return SQ_ERR_ARG; }
     if (cfg->n_tokens == 0) return SQ_OK;    // only empty sequences: the row arrays are not read
-    SQ_TRY(check_rows(q, "q", cfg->n_heads_k, cfg->d_k, cfg->dtype, true));
-    SQ_TRY(check_rows(k, "k", cfg->n_heads_k, cfg->d_k, cfg->dtype, true));
-    SQ_TRY(check_rows(v, "v", cfg->n_heads, cfg->d_v, cfg->dtype, false));
+    SQ_TRY(check_rows(q, "q", cfg->n_heads_k, cfg->d_k, cfg->dtype));
+    SQ_TRY(check_rows(k, "k", cfg->n_heads_k, cfg->d_k, cfg->dtype));
+    SQ_TRY(check_rows(v, "v", cfg->n_heads, cfg->d_v, cfg->dtype));
     SQ_TRY(check_f32(d_gate, "gate", cfg->form == SQ_FORM_KDA ? 16 : 4));
     SQ_TRY(check_f32(d_beta, "beta", 4));
     return SQ_OK;
@@ -151,7 +146,7 @@ extern "C" sq_status sq_delta_scan(const sq_scan_cfg* cfg, const sq_rows* q, con
     bool empty = false;
     SQ_TRY(check_scan(cfg, q, k, v, d_gate, d_beta, &empty));
     if (empty) return SQ_OK;
-    if (cfg->n_tokens > 0) SQ_TRY(check_rows(y, "y", cfg->n_heads, cfg->d_v, cfg->dtype, false));
+    if (cfg->n_tokens > 0) SQ_TRY(check_rows(y, "y", cfg->n_heads, cfg->d_v, cfg->dtype));
     const ScanWork w = scan_work(*cfg, false);
     SQ_TRY(check_work(d_work, work_bytes, w.total));
     ScanParams p = scan_params(*cfg, w, d_work, false);
@@ -173,10 +168,10 @@ extern "C" sq_status sq_delta_scan_bwd(const sq_scan_cfg* cfg, const sq_rows* q,
     SQ_TRY(check_scan(cfg, q, k, v, d_gate, d_beta, &empty));
     if (empty) return SQ_OK;
     if (cfg->n_tokens > 0) {
-        SQ_TRY(check_rows(dy, "dy", cfg->n_heads, cfg->d_v, cfg->dtype, true));
-        SQ_TRY(check_rows(dq, "dq", cfg->n_heads_k, cfg->d_k, cfg->dtype, false));
-        SQ_TRY(check_rows(dk, "dk", cfg->n_heads_k, cfg->d_k, cfg->dtype, false));
-        SQ_TRY(check_rows(dv, "dv", cfg->n_heads, cfg->d_v, cfg->dtype, false));
+        SQ_TRY(check_rows(dy, "dy", cfg->n_heads, cfg->d_v, cfg->dtype));
+        SQ_TRY(check_rows(dq, "dq", cfg->n_heads_k, cfg->d_k, cfg->dtype));
+        SQ_TRY(check_rows(dk, "dk", cfg->n_heads_k, cfg->d_k, cfg->dtype));
+        SQ_TRY(check_rows(dv, "dv", cfg->n_heads, cfg->d_v, cfg->dtype));
         SQ_TRY(check_f32(d_dgate, "dgate", 4));
         SQ_TRY(check_f32(d_dbeta, "dbeta", 4));
     }

@@ -28,17 +28,16 @@ struct ScanParams {
     const float* s0;                 // [n_seq][H][dk][dv] or NULL
     float* s1;                       // or NULL
     // workspace
-    uint16_t* mat_th;                // [slot][H] That = (I + A diag(beta))^-1
-    uint16_t* mat_p;                 // [slot][H] P (forward)
+    uint16_t* mat_f;                 // [slot][H][2] diag(beta) That, That = (I + A diag(beta))^-1, and P; backward: [slot][H] That
     float* mat_gb;                   // [slot][H][2][32] products of the gates up to and after each token (GDN)
     // backward
-    uint16_t* mat_tt;                // [slot][H] T^T, T = (I + diag(beta) A)^-1
-    uint16_t* mat_pt;                // [slot][H] P^T
+    uint16_t* mat_r;                 // [slot][H][2] T^T, T = (I + diag(beta) A)^-1, and P^T
     float* mat_ap;                   // [slot][H][2][32][32] A and P in float32 (GDN)
-    float* e;                        // [n_tokens][H][dv]
-    float* du;                       // [n_tokens][H][dv]
-    float* st;                       // [slot][H][dk][dv] state before each chunk
-    float* gt;                       // [slot][H][dk][dv] gradient of the state after each chunk
+    // in blocks of 16 value columns
+    float* e;                        // [slot][H][dv / 16][32][16]
+    float* du;                       // [slot][H][dv / 16][32][16]
+    float* st;                       // [slot][H][dv / 16][dk][16] state before each chunk
+    float* gt;                       // [slot][H][dv / 16][dk][16] gradient of the state after each chunk
     ScanRows dy, dq, dkk, dvv;
     const float* ds1;
     float* ds0;

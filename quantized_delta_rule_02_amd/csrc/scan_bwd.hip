@@ -152,12 +152,13 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
         const Window ws(p.st + id * DK * dv, (uint32_t)(DK * dv) * 4), wg(p.gt + id * DK * dv, (uint32_t)(DK * dv) * 4);
         Raw<SQ_DTYPE_F32, 4> sn[ND][2], gn[ND][2];   // the next 32 value columns of S and G
         auto fetch_states = [&](int v0) {
-            const int at = opaque(d0 * dv + 8 * g) + v0;
+            // blocks of 16 value columns: [dv / 16][DK][16]
+            const int at = opaque((d0 + (g >> 1) * DK) * 16 + 8 * (g & 1)) + v0 * DK;
 #pragma unroll
             for (int nd = 0; nd < ND; ++nd)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    uint32_t off = (at + 16 * nd * dv + 4 * i) * 4;
+                    uint32_t off = (at + 16 * nd * 16 + 4 * i) * 4;
                     if (VB < 32 && 8 * g >= VB) off = 0xfffffff0u;
                     sn[nd][i].load(ws, off);
                     gn[nd][i].load(wg, off);
@@ -218,9 +219,9 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
         for (int j = 0; j < JOBS; ++j) bj[j] = zero;
         float corner[ND] = {}, dbeta[UPT] = {};
         const int oct = tid % OCT, stok = tid / OCT;             // staging: eight value columns of tokens stok + u NTHR / OCT
-        const uint32_t ds = (uint32_t)p.dy.stride * ES, es = (uint32_t)H * dv * 4;
-        const Window wy(static_cast<const char*>(p.dy.p) + tok0 * ds, rem * ds), we(p.e + tok0 * H * dv, rem * es),
-            wu(p.du + tok0 * H * dv, rem * es), wb(p.beta + tok0 * H, (uint32_t)rem * H * 4);
+        const uint32_t ds = (uint32_t)p.dy.stride * ES;
+        const Window wy(static_cast<const char*>(p.dy.p) + tok0 * ds, rem * ds), we(p.e + id * dv * kChunk, dv * kChunk * 4),
+            wu(p.du + id * dv * kChunk, dv * kChunk * 4), wb(p.beta + tok0 * H, (uint32_t)rem * H * 4);
         float sbeta[UPT];
 #pragma unroll
         for (int u = 0; u < UPT; ++u)
@@ -236,8 +237,10 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
                 for (int i = 0; i < RW; ++i) yr[u][i].load(wy, tok * ds + (c + 4 * i) * ES);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    er[u][i].load(we, tok * es + (c + 4 * i) * 4);
-                    ur[u][i].load(wu, tok * es + (c + 4 * i) * 4);
+                    // blocks of 16 value columns: [dv / 16][32][16], zero behind the sequence's end
+                    const uint32_t o = (((vb + 8 * oct) >> 4) * (kChunk * 16) + tok * 16 + 8 * (oct & 1) + 4 * i) * 4;
+                    er[u][i].load(we, o);
+                    ur[u][i].load(wu, o);
                 }
             }
             if (vb) lds_barrier();
@@ -296,10 +299,10 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
                     for (int t = 0; t < 2; ++t) {
                         const Frag<NPL> fy = lds_frag<NPL>(&s.dy[0][0][0], 32 * LDV, off + 16 * t * LDV);
 #pragma unroll
-                        for (int nd = 0; nd < ND; ++nd) mma(x1[nd][t], fy, f[nd]);
+                        for (int nd = 0; nd < ND; ++nd) mma<2>(x1[nd][t], fy, f[nd]);
                         const Frag<3> fw = lds_frag<3>(&s.w[0][0][0], 32 * LDV, off + 16 * t * LDV);
 #pragma unroll
-                        for (int nd = 0; nd < ND; ++nd) mma(x2[nd][t], fw, f[nd]);
+                        for (int nd = 0; nd < ND; ++nd) mma<2>(x2[nd][t], fw, f[nd]);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);   // keeps the registers of the two halves apart
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
                     for (int t = 0; t < 2; ++t) {
                         const Frag<3> fu = lds_frag<3>(&s.u[0][0][0], 32 * LDV, off + 16 * t * LDV);
 #pragma unroll
-                        for (int nd = 0; nd < ND; ++nd) mma(x3[nd][t], fu, f[nd]);
+                        for (int nd = 0; nd < ND; ++nd) mma<2>(x3[nd][t], fu, f[nd]);
                     }
                 }
 #pragma unroll
@@ -326,8 +329,8 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
                         const int tl = jb % 3, ti = tl > 0, tj = tl > 1;
                         const Frag<3> fu = lds_frag<3>(&s.u[0][0][0], 32 * LDV, off + 16 * tj * LDV);
                         const int oi = off + 16 * ti * LDV;
-                        if (jb < 3) mma(bj[j], lds_frag<3>(&s.w[0][0][0], 32 * LDV, oi), fu);
-                        else mma(bj[j], lds_frag<NPL>(&s.dy[0][0][0], 32 * LDV, oi), fu);
+                        if (jb < 3) mma<2>(bj[j], lds_frag<3>(&s.w[0][0][0], 32 * LDV, oi), fu);
+                        else mma<2>(bj[j], lds_frag<NPL>(&s.dy[0][0][0], 32 * LDV, oi), fu);
                     }
                 }
             }
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
                 auto put = [&](int which, const float* v) {
                     split4<3>(v, w);
 #pragma unroll
-                    for (int pl = 0; pl < 3; ++pl) *reinterpret_cast<u32x2*>(&s.m[which][pl][i][kpos(j0)]) = w[pl];
+                    for (int pl = 0; pl < 3; ++pl) *reinterpret_cast<u32x2*>(&s.m[which][pl][i][kpos32(j0)]) = w[pl];
                 };
                 put(0, m1);
                 put(1, mt);
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
                 for (int q = 0; q < 4; ++q) {
                     split4<3>(m[q], w);
 #pragma unroll
-                    for (int pl = 0; pl < 3; ++pl) *reinterpret_cast<u32x2*>(&s.m[KDA ? q : 0][pl][i][kpos(j0)]) = w[pl];
+                    for (int pl = 0; pl < 3; ++pl) *reinterpret_cast<u32x2*>(&s.m[KDA ? q : 0][pl][i][kpos32(j0)]) = w[pl];
                 }
             }
         }
@@ -459,9 +462,9 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
                         dq[nd][t][r] = fmaf(pre[t][r], x1[nd][t][r], dq[nd][t][r]);
                         dk[nd][t][r] += suf[t][r] * x3[nd][t][r] - pre[t][r] * x2[nd][t][r];
                     }
-                    mma(dq[nd][t], m1, kf[nd]);
-                    mma(dk[nd][t], mt, qf[nd]);
-                    mma(dk[nd][t], ms, kf[nd]);
+                    mma<2>(dq[nd][t], m1, kf[nd]);
+                    mma<2>(dk[nd][t], mt, qf[nd]);
+                    mma<2>(dk[nd][t], ms, kf[nd]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -500,7 +503,7 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt) {
                         f32x4 f = zero;
-                        mma(f, ef[ti], ones[tt]);
+                        mma<2>(f, ef[ti], ones[tt]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) out[tt] += pick(16 * ti + 4 * g + r >= 16 * tt + n, f[r] + row[r], col[r]);
                     }
@@ -611,12 +614,12 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
                     for (int t = 0; t < 2; ++t) {
                         f32x4 da = zero, db = zero, dc = zero;
                         if (LEV < 4 || t == 1) {
-                            mma(da, frag(0, t), fc);
-                            mma(db, frag(KDA ? 2 : 0, t), fc);
+                            mma<2>(da, frag(0, t), fc);
+                            mma<2>(db, frag(KDA ? 2 : 0, t), fc);
                         }
                         if (LEV < 4 || t == 0) {
-                            mma(dc, frag(1, t), fq);
-                            mma(dc, frag(KDA ? 3 : 0, t), fc);
+                            mma<2>(dc, frag(1, t), fq);
+                            mma<2>(dc, frag(KDA ? 3 : 0, t), fc);
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {

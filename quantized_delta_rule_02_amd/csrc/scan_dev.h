@@ -1,14 +1,14 @@
 // Device helpers of the gated delta scan: float32 products on the bfloat16 matrix units.
 //
-// A float32 value is exactly the sum of three bfloat16 values (8 significand bits each, by truncation), so a
-// product of two float32 matrices is six bfloat16 products (the three smallest of the nine, below 2^-21 of the
-// largest, are left out): about float32 accuracy at 2500 / 6 TFLOP/s, where the float32 matrix instructions
-// reach 157.  An operand that is a bfloat16 input already is one plane and needs three products.
+// A float32 value is the sum of three bfloat16 values (rounded to nearest, then what is left, twice), so a product of
+// two float32 matrices is six bfloat16 products (the three smallest of the nine, below 2^-25 of the largest, are left
+// out): about float32 accuracy at 2500 / 6 TFLOP/s, where the float32 matrix instructions reach 157.  An operand that is
+// a bfloat16 input already is one plane and needs three products.
 //
 // MFMA 16x16x32: A lane (i = l & 15, g = l >> 4) holds 8 elements of row i, B lane (n, g) the same 8 positions of
 // column n, D lane (n, g) rows 4g + r, r < 4.  Which k a position (g, e) stands for is free as long as A and B agree.
 // Here position (g, 4t + r) of a block of 32 is k = 16 t + 4 g + r: then two D tiles of a lane are, as they stand,
-// a B operand of the next product, and states and updates never leave their registers.
+// an operand of the next product, and states and updates never leave their registers.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -28,24 +28,35 @@ struct Frag {
     u32x4v p[N];
 };
 
-__device__ __forceinline__ uint32_t hi16_pair(float a, float b) {   // the upper halves of a (low) and b (high)
-    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+// Two float32 rounded to bfloat16 (a low), and what rounding left of each: x - bf16(x) is exact in float32, and one
+// instruction as the two-element dot product with (-1, 0) or (0, -1), half of what masking and subtracting takes.  The
+// constants come from registers: as an inline constant 0xbf800000 stands for another pair.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t round_pair(float a, float b) {
+    bf16x2 r;
+    r[0] = (__bf16)a;
+    r[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, r);
 }
-__device__ __forceinline__ float trunc_bf16(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+__device__ __forceinline__ void rest_pair(uint32_t pair, float& a, float& b) {
+    uint32_t lo = 0x0000bf80u, hi = 0xbf800000u;
+    __asm__("" : "+s"(lo));
+    __asm__("" : "+s"(hi));
+    const bf16x2 p = __builtin_bit_cast(bf16x2, pair);
+    a = __builtin_amdgcn_fdot2_f32_bf16(p, __builtin_bit_cast(bf16x2, lo), a, false);
+    b = __builtin_amdgcn_fdot2_f32_bf16(p, __builtin_bit_cast(bf16x2, hi), b, false);
+}
 
 template <int N>
 __device__ __forceinline__ Frag<N> split8(const float* x) {
     Frag<N> f;
-    float m[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m[j] = x[j];
+    for (int j = 0; j < 4; ++j) {
+        float a = x[2 * j], b = x[2 * j + 1];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f.p[n][j] = hi16_pair(m[2 * j], m[2 * j + 1]);
-        if (n + 1 < N) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m[j] -= trunc_bf16(m[j]);
+        for (int n = 0; n < N; ++n) {
+            f.p[n][j] = round_pair(a, b);
+            if (n + 1 < N) rest_pair(f.p[n][j], a, b);
         }
     }
     return f;
@@ -65,24 +76,22 @@ __device__ __forceinline__ int opaque(int x) {
 // Four elements: the dwords of plane n.
 template <int N>
 __device__ __forceinline__ void split4(const float* x, u32x2* out) {
-    float m[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m[j] = x[j];
+    for (int j = 0; j < 2; ++j) {
+        float a = x[2 * j], b = x[2 * j + 1];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        out[n][0] = hi16_pair(m[0], m[1]);
-        out[n][1] = hi16_pair(m[2], m[3]);
-        if (n + 1 < N) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m[j] -= trunc_bf16(m[j]);
+        for (int n = 0; n < N; ++n) {
+            out[n][j] = round_pair(a, b);
+            if (n + 1 < N) rest_pair(out[n][j], a, b);
         }
     }
 }
 
-template <int NA, int NB>
+// acc += a b, the terms of planes i and j with i + j <= ORD, the smallest first.
+template <int ORD, int NA, int NB>
 __device__ __forceinline__ void mma(f32x4& acc, const Frag<NA>& a, const Frag<NB>& b) {
 #pragma unroll
-    for (int s = 2; s >= 0; --s) {       // smallest terms first
+    for (int s = ORD; s >= 0; --s) {
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
             const int j = s - i;
@@ -93,8 +102,8 @@ __device__ __forceinline__ void mma(f32x4& acc, const Frag<NA>& a, const Frag<NB
     }
 }
 
-// Position of column c of a matrix row inside the row's storage: blocks of 32 in the order described above.
-__device__ __forceinline__ constexpr int kpos(int c) {
+// Position of column c of a matrix row inside the row's storage, in the order described above.
+__device__ __forceinline__ constexpr int kpos32(int c) {
     return (c & ~31) | ((c & 12) << 1) | ((c & 16) >> 2) | (c & 3);
 }
 
