@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 from ctypes import POINTER, byref, c_double, c_float, c_int32, c_size_t, c_uint64, c_void_p
-from contextlib import contextmanager
 
 import numpy as np
 
@@ -389,22 +388,35 @@ def sq_valu_probe(waves_per_simd, out, stream=None):
 
 # ---------------------------------------------------------------- scan and norms
 
+_DTYPES = {}                 # torch's element types to SQ_DTYPE_*
+
+
 def _dtype_code(dtype) -> int:
-    import torch
-    codes = {torch.float32: SQ_DTYPE_F32, torch.bfloat16: SQ_DTYPE_BF16, torch.float16: SQ_DTYPE_F16}
-    if dtype not in codes:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: SQ_DTYPE_F32, torch.bfloat16: SQ_DTYPE_BF16, torch.float16: SQ_DTYPE_F16})
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"element type {dtype}: float32, bfloat16 or float16")
-    return codes[dtype]
+    return code
 
 
-@contextmanager
-def _launch_on(device, stream):
-    """The device current, and the handle of `stream` on it (None: the device's current stream)."""
+def _call(fn, name, device, stream, *args):
+    """fn(*args, stream handle) with `device` current (None: the device's current stream)."""
     import torch
-    if getattr(stream, "device", device) != device:
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    elif getattr(stream, "device", device) != device:
         raise ValueError(f"stream on {stream.device}, tensors on {device}")
-    with torch.cuda.device(device):
-        yield _stream(stream)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != 0:
+        _check(status, name)
 
 
 def _workspace(workspace, nbytes, device, stream):
@@ -419,7 +431,7 @@ def _workspace(workspace, nbytes, device, stream):
         owner = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(owner):
             buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return c_void_p(buf.data_ptr()), nbytes, buf
+    return buf.data_ptr(), nbytes, buf
 
 
 def _on(t, device, name):
@@ -431,16 +443,19 @@ def _on(t, device, name):
 
 
 def _row_array(t, shape, dtype, device, name):
-    """sq_rows of a tensor [tokens, heads, d] whose heads lie side by side (any stride between tokens)."""
-    _on(t, device, name)
-    if t.dtype != dtype:
+    """sq_rows of a tensor [tokens, heads, d] (or [rows, d]) whose heads lie side by side (any stride between tokens)."""
+    if getattr(t, "device", None) != device:
+        _on(t, device, name)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    T, H, d = shape
-    if t.numel() and ((d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
+    st = t.stride()
+    T, d = shape[0], shape[-1]
+    H = shape[1] if len(shape) == 3 else 1
+    if ((d > 1 and st[-1] != 1) or (H > 1 and st[1] != d)) and t.numel():
         raise ValueError(f"{name}: the elements and heads of a token must be contiguous")
-    return _lib.SqRows(c_void_p(t.data_ptr()), t.stride(0) if T > 1 else H * d)
+    return _lib.SqRows(t.data_ptr(), st[0] if T > 1 else H * d)
 
 
 def _plain(t, shape, device, name):
@@ -448,10 +463,15 @@ def _plain(t, shape, device, name):
     import torch
     if t is None:
         return None
-    _on(t, device, name)
-    if tuple(t.shape) != tuple(shape):
+    if getattr(t, "device", None) != device:
+        _on(t, device, name)
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return _dev(t, torch.float32, 0, name)
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _scan_cfg(form, q, v, seq_start):
@@ -500,10 +520,9 @@ def sq_delta_scan(form, q, k, v, gate, beta, y, seq_start=None, s0=None, s1=None
     args = [rows(q, Hk, dk, "q"), rows(k, Hk, dk, "k"), rows(v, H, dv, "v"),
             _plain(gate, (T, H, dk) if form == SQ_FORM_KDA else (T, H), dev, "gate"), _plain(beta, (T, H), dev, "beta"),
             _plain(s0, st, dev, "s0"), rows(y, H, dv, "y"), _plain(s1, st, dev, "s1")]
-    with _launch_on(dev, stream) as handle:
-        work, nbytes, keep = _workspace(workspace, _scan_bytes(cfg, 0), dev, stream)
-        _check(_lib.load().sq_delta_scan(byref(cfg), *args, work, nbytes, handle), "sq_delta_scan")
-        del keep
+    work, nbytes, keep = _workspace(workspace, _scan_bytes(cfg, 0), dev, stream)
+    _call(_lib.load().sq_delta_scan, "sq_delta_scan", dev, stream, byref(cfg), *args, work, nbytes)
+    del keep
 
 
 def sq_delta_scan_bwd(form, q, k, v, gate, beta, dy, dq, dk, dv, dgate, dbeta, seq_start=None, s0=None, ds1=None,
@@ -517,10 +536,9 @@ def sq_delta_scan_bwd(form, q, k, v, gate, beta, dy, dq, dk, dv, dgate, dbeta, s
             _plain(beta, (T, H), dev, "beta"), _plain(s0, st, dev, "s0"), rows(dy, H, nv, "dy"), _plain(ds1, st, dev, "ds1"),
             rows(dq, Hk, nk, "dq"), rows(dk, Hk, nk, "dk"), rows(dv, H, nv, "dv"), _plain(dgate, gs, dev, "dgate"),
             _plain(dbeta, (T, H), dev, "dbeta"), _plain(ds0, st, dev, "ds0")]
-    with _launch_on(dev, stream) as handle:
-        work, nbytes, keep = _workspace(workspace, _scan_bytes(cfg, 1), dev, stream)
-        _check(_lib.load().sq_delta_scan_bwd(byref(cfg), *args, work, nbytes, handle), "sq_delta_scan_bwd")
-        del keep
+    work, nbytes, keep = _workspace(workspace, _scan_bytes(cfg, 1), dev, stream)
+    _call(_lib.load().sq_delta_scan_bwd, "sq_delta_scan_bwd", dev, stream, byref(cfg), *args, work, nbytes)
+    del keep
 
 
 class _NormCall:
@@ -530,25 +548,21 @@ class _NormCall:
         import torch
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-        if first.dim() not in (2, 3):
+        self.shape, self.device = first.shape, first.device
+        n = len(self.shape)
+        if n != 2 and n != 3:
             raise ValueError(f"{name} must be [rows, d] or [tokens, heads, d]")
-        self.shape, self.device = tuple(first.shape), first.device
-        self.outer, self.d = first.shape[0], first.shape[-1]
-        self.inner = first.shape[1] if first.dim() == 3 else 1
+        self.outer, self.d = self.shape[0], self.shape[-1]
+        self.inner = self.shape[1] if n == 3 else 1
 
     def rows(self, t, dtype, name):
-        if t is None:
-            return None
-        if tuple(t.shape) != self.shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.shape}")
-        t = t if t.dim() == 3 else t.unsqueeze(1)
-        return byref(_row_array(t, (self.outer, self.inner, self.d), dtype, self.device, name))
+        return None if t is None else byref(_row_array(t, self.shape, dtype, self.device, name))
 
     def vec(self, t, name):
-        return _plain(t, (self.d,), self.device, name)
+        return None if t is None else _plain(t, (self.d,), self.device, name)
 
     def cfg(self, dtype, dtype_out, kind, act, eps, res_scale, out_scale):
-        return byref(_lib.SqNormCfg(_dtype_code(dtype), _dtype_code(dtype_out), int(kind), int(act), self.outer,
+        return byref(_lib.SqNormCfg(_dtype_code(dtype), _dtype_code(dtype_out), kind, act, self.outer,
                                     self.inner, self.d, eps, res_scale, out_scale))
 
     def work(self, workspace, stream, wanted):
@@ -570,8 +584,7 @@ def sq_norm_in(x, n, weight=None, r=None, h=None, chan_scale=None, res_scale=1.0
     c = _NormCall(x, "x")
     args = [c.rows(x, x.dtype, "x"), c.rows(r, x.dtype, "r"), c.vec(weight, "weight"), c.vec(chan_scale, "chan_scale"),
             c.rows(h, x.dtype, "h"), c.rows(n, n.dtype, "n")]
-    with _launch_on(c.device, stream) as handle:
-        _check(_lib.load().sq_norm_in(c.cfg(x.dtype, n.dtype, kind, 0, eps, res_scale, out_scale), *args, handle), "sq_norm_in")
+    _call(_lib.load().sq_norm_in, "sq_norm_in", c.device, stream, c.cfg(x.dtype, n.dtype, kind, 0, eps, res_scale, out_scale), *args)
 
 
 def sq_norm_in_bwd(h, dn, dx, weight=None, r=None, dh=None, dr=None, chan_scale=None, res_scale=1.0, dweight=None,
@@ -581,11 +594,9 @@ def sq_norm_in_bwd(h, dn, dx, weight=None, r=None, dh=None, dr=None, chan_scale=
     args = [c.rows(h, h.dtype, "h"), c.rows(dn, dn.dtype, "dn"), c.rows(dh, h.dtype, "dh"), c.rows(r, h.dtype, "r"),
             c.vec(weight, "weight"), c.vec(chan_scale, "chan_scale"), c.rows(dx, h.dtype, "dx"), c.rows(dr, h.dtype, "dr"),
             c.vec(dweight, "dweight"), c.vec(dchan_scale, "dchan_scale")]
-    with _launch_on(c.device, stream) as handle:
-        work, nbytes, keep = c.work(workspace, stream, dweight is not None or dchan_scale is not None)
-        _check(_lib.load().sq_norm_in_bwd(c.cfg(h.dtype, dn.dtype, kind, 0, eps, res_scale, out_scale), *args, work, nbytes,
-                                          handle), "sq_norm_in_bwd")
-        del keep
+    work, nbytes, keep = c.work(workspace, stream, dweight is not None or dchan_scale is not None)
+    _call(_lib.load().sq_norm_in_bwd, "sq_norm_in_bwd", c.device, stream, c.cfg(h.dtype, dn.dtype, kind, 0, eps, res_scale, out_scale), *args, work, nbytes)
+    del keep
 
 
 def sq_norm_out(y, o, weight=None, z=None, act=SQ_ACT_SILU, x=None, chan_scale=None, res_scale=1.0, eps=1e-6,
@@ -594,8 +605,7 @@ def sq_norm_out(y, o, weight=None, z=None, act=SQ_ACT_SILU, x=None, chan_scale=N
     c = _NormCall(y, "y")
     args = [c.rows(y, y.dtype, "y"), c.rows(z, o.dtype, "z"), c.rows(x, o.dtype, "x"), c.vec(weight, "weight"),
             c.vec(chan_scale, "chan_scale"), c.rows(o, o.dtype, "o")]
-    with _launch_on(c.device, stream) as handle:
-        _check(_lib.load().sq_norm_out(c.cfg(y.dtype, o.dtype, kind, act, eps, res_scale, 1.0), *args, handle), "sq_norm_out")
+    _call(_lib.load().sq_norm_out, "sq_norm_out", c.device, stream, c.cfg(y.dtype, o.dtype, kind, act, eps, res_scale, 1.0), *args)
 
 
 def sq_norm_out_bwd(y, do, dy, weight=None, z=None, dz=None, act=SQ_ACT_SILU, chan_scale=None, res_scale=1.0,
@@ -605,8 +615,6 @@ def sq_norm_out_bwd(y, do, dy, weight=None, z=None, dz=None, act=SQ_ACT_SILU, ch
     args = [c.rows(y, y.dtype, "y"), c.rows(z, do.dtype, "z"), c.rows(do, do.dtype, "do"), c.vec(weight, "weight"),
             c.vec(chan_scale, "chan_scale"), c.rows(dy, y.dtype, "dy"), c.rows(dz, do.dtype, "dz"),
             c.vec(dweight, "dweight"), c.vec(dchan_scale, "dchan_scale")]
-    with _launch_on(c.device, stream) as handle:
-        work, nbytes, keep = c.work(workspace, stream, dweight is not None or dchan_scale is not None)
-        _check(_lib.load().sq_norm_out_bwd(c.cfg(y.dtype, do.dtype, kind, act, eps, res_scale, 1.0), *args, work, nbytes,
-                                           handle), "sq_norm_out_bwd")
-        del keep
+    work, nbytes, keep = c.work(workspace, stream, dweight is not None or dchan_scale is not None)
+    _call(_lib.load().sq_norm_out_bwd, "sq_norm_out_bwd", c.device, stream, c.cfg(y.dtype, do.dtype, kind, act, eps, res_scale, 1.0), *args, work, nbytes)
+    del keep

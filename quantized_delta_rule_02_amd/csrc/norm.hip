@@ -42,14 +42,20 @@ __device__ __forceinline__ Sum2 row_sum(Sum2 v, float* lds) {
     return v;
 }
 
+// exp(-z) from the hardware's 2^x: the rounding of z log2(e) is put back as a factor, so that its error does not grow with |z|.
+__device__ __forceinline__ float exp_neg(float z) {
+    constexpr float l2e = 1.44269504089f, ln2 = 0.69314718056f;
+    const float a = -z * l2e, lo = fmaf(-z, l2e, -a), e = __builtin_amdgcn_exp2f(a);
+    return fabsf(a) < 200.f ? fmaf(e, lo * ln2, e) : e;        // beyond: 0, infinity or NaN as they are
+}
 __device__ __forceinline__ void act_of(int act, float z, float& g, float& dg) {
+    const float s = __builtin_amdgcn_rcpf(1.f + exp_neg(z));
     if (act == SQ_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-z));
         g = z * s;
-        dg = s * (1.f + z * (1.f - s));
+        dg = s * fmaf(z, 1.f - s, 1.f);
     } else {                                   // SQ_ACT_SIGMOID
-        g = 1.f / (1.f + expf(-z));
-        dg = g * (1.f - g);
+        g = s;
+        dg = s * (1.f - s);
     }
 }
 
@@ -58,136 +64,219 @@ __device__ __forceinline__ int64_t row_at(const NormRows& a, uint32_t outer, uin
     return (int64_t)outer * a.stride + (int64_t)(inner * (uint32_t)d);
 }
 
-template <int OP, int V, int TPR, int K>
-__global__ void __launch_bounds__(kNormThreads) k_norm(const NormParams p) {
+// Elements as loaded: what follows a load waits for it, so all loads of a row come before the first conversion.
+template <int V>
+struct RawV {
+    u32x4v a, b;
+    __device__ __forceinline__ void load(const NormRows& r, int dt, int64_t i) {
+        if constexpr (V == 8) {
+            if (dt == SQ_DTYPE_F32) {
+                const u32x4v* s = reinterpret_cast<const u32x4v*>(static_cast<const float*>(r.p) + i);
+                a = s[0];
+                b = s[1];
+            } else {
+                a = *reinterpret_cast<const u32x4v*>(static_cast<const uint16_t*>(r.p) + i);
+            }
+        } else {
+            a[0] = dt == SQ_DTYPE_F32 ? static_cast<const uint32_t*>(r.p)[i] : static_cast<const uint16_t*>(r.p)[i];
+        }
+    }
+    __device__ __forceinline__ void get(int dt, float* x) const {
+        if constexpr (V == 8) {
+            if (dt == SQ_DTYPE_F32) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) { x[j] = __uint_as_float(a[j]); x[4 + j] = __uint_as_float(b[j]); }
+            } else if (dt == SQ_DTYPE_BF16) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) { x[2 * j] = bf16_lo(a[j]); x[2 * j + 1] = bf16_hi(a[j]); }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) { x[2 * j] = f16_val(a[j] & 0xffffu); x[2 * j + 1] = f16_val(a[j] >> 16); }
+            }
+        } else {
+            x[0] = dt == SQ_DTYPE_F32 ? __uint_as_float(a[0]) : dt == SQ_DTYPE_BF16 ? bf16_lo(a[0]) : f16_val(a[0]);
+        }
+    }
+};
+
+// U rows at a time: their loads are in flight together.
+// EXTRA (gradients of the first norm): dh or r is there.
+template <int OP, int V, int TPR, int K, int U, bool EXTRA>
+__global__ void __launch_bounds__(kNormThreads, V == 8 && K == 1 ? 4 : 1) k_norm(const NormParams p) {
     constexpr int RPB = kNormThreads / TPR;
     constexpr bool kBwd = OP == kNormInBwd || OP == kNormOutBwd;
+    constexpr bool kIn = OP == kNormIn || OP == kNormInBwd;
+    constexpr bool kAll = K <= 2;              // few enough registers to load every array at once
     __shared__ float s_red[8];
     __shared__ float s_col[kBwd && RPB > 1 ? kNormThreads * V * K : 1];
     const int lane = (int)threadIdx.x % TPR, sub = (int)threadIdx.x / TPR;
     const int d = p.d;
+    // first: the row the norm is of, its addend or gate, the incoming gradient; second: what only the result needs
+    const NormRows& ra = OP == kNormIn ? p.x : OP == kNormInBwd ? p.h : p.y;
+    const NormRows& rt = OP == kNormIn ? p.r : p.z;
+    const NormRows& rg = OP == kNormInBwd ? p.dn : p.d_o;
+    const NormRows& re = OP == kNormInBwd ? p.dh : p.x;
+    const bool has_t = OP == kNormIn ? p.has_r : kIn ? false : p.has_z;
+    const bool has_e = OP == kNormInBwd ? EXTRA && p.has_dh : OP == kNormOut ? p.has_x : false;
+    const bool has_r = EXTRA && p.has_r;
+    const int dt_t = OP == kNormIn ? p.dtype : p.dtype_out, dt_e = OP == kNormInBwd ? p.dtype : p.dtype_out;
+    RawV<V> xa[U][K], xt[U][K], xg[kBwd ? U : 1][K], xe[U][K], xr[OP == kNormInBwd ? U : 1][K];
     int col[K];
     bool in[K];
-    float w[K][V], c[K][V], sw[K][V], sc[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         col[k] = (k * TPR + lane) * V;
         in[k] = col[k] < d;
+    }
+    uint32_t outer[U], inner[U];
+    bool live[U];
+    auto load_second = [&](int u, int k) {
+        if (has_e) xe[u][k].load(re, dt_e, row_at(re, outer[u], inner[u], d) + col[k]);
+        if constexpr (OP == kNormInBwd) {
+            if (has_r) xr[u][k].load(p.r, p.dtype, row_at(p.r, outer[u], inner[u], d) + col[k]);
+        }
+    };
+    auto load_rows = [&](int64_t row0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * RPB + sub;
+            live[u] = row < p.n_rows;
+            outer[u] = (uint32_t)row / (uint32_t)p.n_inner;
+            inner[u] = (uint32_t)row % (uint32_t)p.n_inner;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!(live[u] && in[k])) continue;
+                xa[u][k].load(ra, p.dtype, row_at(ra, outer[u], inner[u], d) + col[k]);
+                if (has_t) xt[u][k].load(rt, dt_t, row_at(rt, outer[u], inner[u], d) + col[k]);
+                if constexpr (kBwd) xg[kBwd ? u : 0][k].load(rg, p.dtype_out, row_at(rg, outer[u], inner[u], d) + col[k]);
+                if constexpr (kAll) load_second(u, k);
+            }
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB * U;
+    int64_t row0 = (int64_t)blockIdx.x * RPB * U;
+    if (row0 < p.n_rows) load_rows(row0);
+    float w[K][V], c[K][V], sw[K][V], sc[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             w[k][j] = (p.weight && in[k]) ? p.weight[col[k] + j] : 1.f;
             c[k][j] = (p.chan_scale && in[k]) ? p.chan_scale[col[k] + j] * p.res_scale : p.res_scale;
             sw[k][j] = sc[k][j] = 0.f;
         }
-    }
     // every thread of a workgroup makes the same number of rounds: the row sums hold barriers
-    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.n_rows; row0 += (int64_t)gridDim.x * RPB) {
-        const int64_t row = row0 + sub;
-        const bool live = row < p.n_rows;
-        const uint32_t outer = (uint32_t)row / (uint32_t)p.n_inner, inner = (uint32_t)row % (uint32_t)p.n_inner;
-        float a[K][V], g[K][V], t[K][V];
-        Sum2 s{0.f, 0.f};
+    for (; row0 < p.n_rows; row0 += step) {
+        float a[U][K][V], g[U][K][V], t[U][K][V], e[U][K][V], q[U][K][V];   // t: act(z), q: its derivative (or r)
+        Sum2 s[U];
+        uint32_t o_[U], i_[U];
+        bool lv[U];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const bool on = live && in[k];
+        for (int u = 0; u < U; ++u) {
+            s[u] = Sum2{0.f, 0.f};
+            o_[u] = outer[u];
+            i_[u] = inner[u];
+            lv[u] = live[u];
 #pragma unroll
-            for (int j = 0; j < V; ++j) a[k][j] = g[k][j] = t[k][j] = 0.f;
-            if (!on) continue;
-            if constexpr (OP == kNormIn) {
-                loadv<V>(p.x.p, p.dtype, row_at(p.x, outer, inner, d) + col[k], a[k]);
-                if (p.has_r) {
-                    loadv<V>(p.r.p, p.dtype, row_at(p.r, outer, inner, d) + col[k], t[k]);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) a[k][j] = fmaf(c[k][j], t[k][j], a[k][j]);
-                }
-            } else if constexpr (OP == kNormInBwd) {
-                loadv<V>(p.h.p, p.dtype, row_at(p.h, outer, inner, d) + col[k], a[k]);
-                loadv<V>(p.dn.p, p.dtype_out, row_at(p.dn, outer, inner, d) + col[k], g[k]);
-            } else {
-                loadv<V>(p.y.p, p.dtype, row_at(p.y, outer, inner, d) + col[k], a[k]);
-                if (p.has_z) loadv<V>(p.z.p, p.dtype_out, row_at(p.z, outer, inner, d) + col[k], t[k]);
-                if constexpr (OP == kNormOutBwd)
-                    loadv<V>(p.d_o.p, p.dtype_out, row_at(p.d_o, outer, inner, d) + col[k], g[k]);
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) s.a = fmaf(a[k][j], a[k][j], s.a);
-            if constexpr (OP == kNormInBwd) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) s.b = fmaf(g[k][j] * w[k][j], a[k][j], s.b);
-            }
-            if constexpr (OP == kNormOutBwd) {
+            for (int k = 0; k < K; ++k) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    float act = 1.f, dact = 0.f;
-                    if (p.has_z) act_of(p.act, t[k][j], act, dact);
-                    s.b = fmaf(g[k][j] * c[k][j] * w[k][j] * act, a[k][j], s.b);
+                    a[u][k][j] = g[u][k][j] = e[u][k][j] = q[u][k][j] = 0.f;
+                    t[u][k][j] = kIn ? 0.f : 1.f;
+                }
+                if (!(lv[u] && in[k])) continue;
+                xa[u][k].get(p.dtype, a[u][k]);
+                if (has_t) {
+                    xt[u][k].get(dt_t, t[u][k]);
+                    if constexpr (!kIn) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const float z = t[u][k][j];
+                            act_of(p.act, z, t[u][k][j], q[u][k][j]);
+                        }
+                    }
+                }
+                if constexpr (kBwd) xg[kBwd ? u : 0][k].get(p.dtype_out, g[u][k]);
+                if constexpr (kAll) {
+                    if (has_e) xe[u][k].get(dt_e, e[u][k]);
+                    if constexpr (OP == kNormInBwd) {
+                        if (has_r) xr[OP == kNormInBwd ? u : 0][k].get(p.dtype, q[u][k]);
+                    }
                 }
             }
         }
-        s = row_sum<TPR>(s, s_red);
-        const float inv = 1.f / sqrtf(fmaf(s.a, p.inv_div, p.eps));
-        [[maybe_unused]] float back = 0.f;
-        if constexpr (OP == kNormInBwd) back = s.b * p.out_scale * inv * inv * p.inv_div;
-        if constexpr (OP == kNormOutBwd) back = s.b * inv * inv * p.inv_div;
+        if constexpr (kAll) {
+            if (row0 + step < p.n_rows) load_rows(row0 + step);
+        }
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (!(live && in[k])) continue;
-            float o[V];
-            if constexpr (OP == kNormIn) {
-                if (p.write_h) storev<V>(p.h.p, p.dtype, row_at(p.h, outer, inner, d) + col[k], a[k]);
-                const float f = inv * p.out_scale;
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = a[k][j] * f * w[k][j];
-                storev<V>(p.n.p, p.dtype_out, row_at(p.n, outer, inner, d) + col[k], o);
-            } else if constexpr (OP == kNormInBwd) {
-                float e[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) e[j] = 0.f;
-                if (p.has_dh) loadv<V>(p.dh.p, p.dtype, row_at(p.dh, outer, inner, d) + col[k], e);
+            for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float gf = g[k][j] * p.out_scale;
-                    o[j] = fmaf(inv, gf * w[k][j] - a[k][j] * back, e[j]);
-                    sw[k][j] = fmaf(gf * inv, a[k][j], sw[k][j]);
+                    if constexpr (OP == kNormIn) a[u][k][j] = fmaf(c[k][j], t[u][k][j], a[u][k][j]);
+                    s[u].a = fmaf(a[u][k][j], a[u][k][j], s[u].a);
+                    if constexpr (OP == kNormInBwd) s[u].b = fmaf(g[u][k][j] * w[k][j], a[u][k][j], s[u].b);
+                    if constexpr (OP == kNormOutBwd) s[u].b = fmaf(g[u][k][j] * c[k][j] * w[k][j] * t[u][k][j], a[u][k][j], s[u].b);
                 }
-                if (p.has_r) {                 // only dchan_scale needs r
-                    loadv<V>(p.r.p, p.dtype, row_at(p.r, outer, inner, d) + col[k], t[k]);
+        }
 #pragma unroll
-                    for (int j = 0; j < V; ++j) sc[k][j] = fmaf(o[j] * p.res_scale, t[k][j], sc[k][j]);
+        for (int u = 0; u < U; ++u) s[u] = row_sum<TPR>(s[u], s_red);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float inv = 1.f / sqrtf(fmaf(s[u].a, p.inv_div, p.eps));
+            [[maybe_unused]] float back = 0.f;
+            if constexpr (OP == kNormInBwd) back = s[u].b * p.out_scale * inv * inv * p.inv_div;
+            if constexpr (OP == kNormOutBwd) back = s[u].b * inv * inv * p.inv_div;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!(lv[u] && in[k])) continue;
+                if constexpr (!kAll) {
+                    load_second(u, k);
+                    if (has_e) xe[u][k].get(dt_e, e[u][k]);
+                    if constexpr (OP == kNormInBwd) {
+                        if (has_r) xr[OP == kNormInBwd ? u : 0][k].get(p.dtype, q[u][k]);
+                    }
                 }
-                if (p.write_dr) {
+                auto put = [&](const NormRows& r, int dt, const float* v) { storev<V>(r.p, dt, row_at(r, o_[u], i_[u], d) + col[k], v); };
+                float o[V], e2[V];
+                if constexpr (OP == kNormIn) {
+                    if (p.write_h) put(p.h, p.dtype, a[u][k]);
+                    const float f = inv * p.out_scale;
 #pragma unroll
-                    for (int j = 0; j < V; ++j) e[j] = o[j] * c[k][j];
-                    storev<V>(p.dr.p, p.dtype, row_at(p.dr, outer, inner, d) + col[k], e);
+                    for (int j = 0; j < V; ++j) o[j] = a[u][k][j] * f * w[k][j];
+                    put(p.n, p.dtype_out, o);
+                } else if constexpr (OP == kNormInBwd) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float gf = g[u][k][j] * p.out_scale;
+                        o[j] = fmaf(inv, gf * w[k][j] - a[u][k][j] * back, e[u][k][j]);
+                        sw[k][j] = fmaf(gf * inv, a[u][k][j], sw[k][j]);
+                        if constexpr (EXTRA) sc[k][j] = fmaf(o[j] * p.res_scale, q[u][k][j], sc[k][j]);   // q: r, or 0 where nobody asks
+                        e2[j] = o[j] * c[k][j];
+                    }
+                    if (p.write_dr) put(p.dr, p.dtype, e2);
+                    put(p.dx, p.dtype, o);
+                } else if constexpr (OP == kNormOut) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) o[j] = fmaf(a[u][k][j] * inv * w[k][j] * t[u][k][j], c[k][j], e[u][k][j]);
+                    put(p.o, p.dtype_out, o);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float yh = a[u][k][j] * inv, gc = g[u][k][j] * c[k][j];
+                        o[j] = inv * (gc * w[k][j] * t[u][k][j] - a[u][k][j] * back);
+                        e2[j] = gc * w[k][j] * yh * q[u][k][j];
+                        sw[k][j] = fmaf(gc * t[u][k][j], yh, sw[k][j]);
+                        sc[k][j] = fmaf(g[u][k][j] * p.res_scale * t[u][k][j], w[k][j] * yh, sc[k][j]);
+                    }
+                    if (p.write_dz) put(p.dz, p.dtype_out, e2);
+                    put(p.dy, p.dtype, o);
                 }
-                storev<V>(p.dx.p, p.dtype, row_at(p.dx, outer, inner, d) + col[k], o);
-            } else if constexpr (OP == kNormOut) {
-                float e[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) e[j] = 0.f;
-                if (p.has_x) loadv<V>(p.x.p, p.dtype_out, row_at(p.x, outer, inner, d) + col[k], e);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float act = 1.f, dact = 0.f;
-                    if (p.has_z) act_of(p.act, t[k][j], act, dact);
-                    o[j] = fmaf(a[k][j] * inv * w[k][j] * act, c[k][j], e[j]);
-                }
-                storev<V>(p.o.p, p.dtype_out, row_at(p.o, outer, inner, d) + col[k], o);
-            } else {
-                float e[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float act = 1.f, dact = 0.f;
-                    if (p.has_z) act_of(p.act, t[k][j], act, dact);
-                    const float yh = a[k][j] * inv, gc = g[k][j] * c[k][j];
-                    o[j] = inv * (gc * w[k][j] * act - a[k][j] * back);
-                    e[j] = gc * w[k][j] * yh * dact;
-                    sw[k][j] = fmaf(gc * act, yh, sw[k][j]);
-                    sc[k][j] = fmaf(g[k][j] * p.res_scale * act, w[k][j] * yh, sc[k][j]);
-                }
-                if (p.write_dz) storev<V>(p.dz.p, p.dtype_out, row_at(p.dz, outer, inner, d) + col[k], e);
-                storev<V>(p.dy.p, p.dtype, row_at(p.dy, outer, inner, d) + col[k], o);
             }
+        }
+        if constexpr (!kAll) {
+            if (row0 + step < p.n_rows) load_rows(row0 + step);
         }
     }
     if constexpr (kBwd) {
@@ -222,31 +311,38 @@ __global__ void __launch_bounds__(kNormThreads) k_norm(const NormParams p) {
     }
 }
 
-// Adds the partial rows: 16 columns x 16 row groups per workgroup, the groups in LDS, in a fixed order.
-__global__ void __launch_bounds__(kNormThreads) k_norm_sum(const NormParams p) {
-    __shared__ float s[16][17];
+// Adds the partial rows: 16 columns x 64 row groups per workgroup, the groups in LDS, in a fixed order (with 16 groups a sum
+// of 1024 rows of 128 columns took 20 us).
+constexpr int kSumGroups = 64;
+__global__ void __launch_bounds__(16 * kSumGroups) k_norm_sum(const NormParams p) {
+    __shared__ float s[kSumGroups][17];
     const int ci = (int)threadIdx.x & 15, g = (int)threadIdx.x >> 4;
     const int which = (int)blockIdx.y, col = (int)blockIdx.x * 16 + ci;
     float* out = which ? p.dchan_scale : p.dweight;
     if (!out) return;
     const float* in = p.part + (size_t)which * p.n_blocks * p.d;
     float t = 0.f;
-    if (col < p.d)
-        for (int b = g; b < p.n_blocks; b += 16) t += in[(size_t)b * p.d + col];
+    if (col < p.d) {
+#pragma unroll 4
+        for (int b = g; b < p.n_blocks; b += kSumGroups) t += in[(size_t)b * p.d + col];
+    }
     s[g][ci] = t;
     __syncthreads();
-    if (g == 0 && col < p.d) {
-        for (int r = 1; r < 16; ++r) t += s[r][ci];
-        out[col] = t;
+    if (g < 4) {
+        for (int r = g + 4; r < kSumGroups; r += 4) t += s[r][ci];
+        s[g][ci] = t;
     }
+    __syncthreads();
+    if (g == 0 && col < p.d) out[col] = s[0][ci] + s[1][ci] + s[2][ci] + s[3][ci];
 }
 
 template <int OP, int V, int TPR, int K>
 static hipError_t launch_t(const NormParams& p0, hipStream_t s) {
     constexpr int RPB = kNormThreads / TPR;
+    constexpr int U = V == 8 && K == 1 && TPR < 256 && OP == kNormIn ? 2 : 1;
     constexpr bool kBwd = OP == kNormInBwd || OP == kNormOutBwd;
     NormParams p = p0;
-    int64_t blocks = (p.n_rows + RPB - 1) / RPB;
+    int64_t blocks = (p.n_rows + RPB * U - 1) / (RPB * U);
     if (kBwd) {
         const int64_t cap = norm_bwd_blocks(p.n_rows, p.d);
         if (blocks > cap) blocks = cap;
@@ -254,10 +350,15 @@ static hipError_t launch_t(const NormParams& p0, hipStream_t s) {
         blocks = 8192;                         // the weights are loaded once per workgroup and kept over its rows
     }
     p.n_blocks = (int32_t)blocks;
-    if (blocks > 0) k_norm<OP, V, TPR, K><<<dim3((unsigned)blocks), dim3(kNormThreads), 0, s>>>(p);
+    const dim3 grid((unsigned)blocks), blk(kNormThreads);
+    if (blocks > 0) {
+        constexpr bool kChoice = OP == kNormInBwd;
+        if (kChoice && !p.has_dh && !p.has_r) k_norm<OP, V, TPR, K, U, !kChoice><<<grid, blk, 0, s>>>(p);
+        else k_norm<OP, V, TPR, K, U, true><<<grid, blk, 0, s>>>(p);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !kBwd || !(p.dweight || p.dchan_scale)) return e;
-    k_norm_sum<<<dim3((unsigned)((p.d + 15) / 16), 2), dim3(kNormThreads), 0, s>>>(p);
+    k_norm_sum<<<dim3((unsigned)((p.d + 15) / 16), 2), dim3(16 * kSumGroups), 0, s>>>(p);
     return hipGetLastError();
 }
 
