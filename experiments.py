@@ -16,6 +16,12 @@
       The two-stream arrangement against a stand-in for the model's per-layer compute (a bf16
       GEMM on the main stream): fit + pack of layer l on the second stream overlaps the GEMM of
       layer l + 1 (hyper.ai summary, 方法, the second-stream arrangement).
+  python experiments.py block [--workload gdn-decode-32h-128] [--prompt 512] [--steps 64]
+      A gated-delta block around the packed state, as a model runs it: the q and k projections to unit
+      norm (sq_norm_in), ragged prompts brought into the states (sq_delta_scan), the states packed
+      (sq_pack), decode steps (sq_state_step) and the gated norm of each readout (sq_norm_out).  Reports
+      the drift of the block's output against the same decode on float32 states, next to the time of the
+      prompt by the scan and token by token (sq_fp32_step).
 
 Inputs are seeded synthetic tensors of the workloads' shapes (workloads/); nothing is read from
 disk.
@@ -277,6 +283,73 @@ def overlap(args):
                       "results": res}), flush=True)
 
 
+def block(args):
+    import numpy as np
+    from workloads import configs
+    wl = configs.BY_NAME[args.workload]
+    B = min(wl.batch, args.batch)
+    wb = Workbench(wl, batch=B)
+    torch, sq, dev = wb.torch, wb.sq, wb.dev
+    H, dk, dv, per = wb.H, wb.dk, wb.dv, wb.B * wb.H
+    if wb.L != 1:
+        raise SystemExit("the block experiment takes a workload of one layer")
+    bf = torch.bfloat16
+    lens = np.random.default_rng(5).integers(args.prompt // 2, args.prompt + 1, size=B)
+    T = int(lens.sum())
+    start = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=dev)
+    wb.tg.manual_seed(77)
+    rn = lambda *s: torch.randn(*s, device=dev, generator=wb.tg)  # noqa: E731
+    qk, v, beta = rn(T, 2, H, dk).to(bf), rn(T, H, dv).to(bf), torch.sigmoid(rn(T, H))
+    unit = wb.gate.view(B, H, -1)[0]
+    gate = (unit if wb.form == sq.SQ_FORM_KDA else unit[:, 0])[None].expand(T, *((H, dk) if wb.form == sq.SQ_FORM_KDA else (H,))).contiguous()
+    q, k, y = (torch.empty(T, H, d, dtype=bf, device=dev) for d in (dk, dk, dv))
+    S = torch.empty(B, H, dk, dv, device=dev)
+    work = torch.empty(sq.sq_delta_scan_bytes(wb.form, bf, H, H, dk, dv, B, T), dtype=torch.uint8, device=dev)
+
+    def prompt():
+        sq.sq_norm_in(qk[:, 0], q, kind=sq.SQ_NORM_L2)
+        sq.sq_norm_in(qk[:, 1], k, kind=sq.SQ_NORM_L2)
+        sq.sq_delta_scan(wb.form, q, k, v, gate, beta, y, seq_start=start, s1=S, workspace=work)
+
+    def timed(fn, reps):
+        fn()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(reps):
+            fn()
+        e1.record()
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) / reps
+
+    scan_ms = timed(prompt, 5)
+    # the same prompts one token of every request at a time (lengths rounded to the mean)
+    S2, tok = torch.zeros_like(S), int(round(T / B))
+    q1, k1, v1, b1 = wb.inputs(0)
+    step_ms = timed(lambda: [sq.sq_fp32_step(wb.form, H, dk, dv, B, 0, 1, B, wb.ident, S2, q1, k1, v1, wb.gate, b1, wb.y)
+                             for _ in range(tok)], 1)
+    pool, mem = wb.pool(wb.plan(), S)
+    w = 1.0 + 0.1 * rn(dv)
+    yp, yf = torch.empty(per * dv, device=dev), torch.empty(per * dv, device=dev)
+    o = [torch.empty(B, H, dv, dtype=bf, device=dev) for _ in range(2)]
+    drift = []
+    qd, kd = torch.empty(B, H, dk, device=dev), torch.empty(B, H, dk, device=dev)
+    for _ in range(args.steps):
+        raw, vd, bd, z = rn(B, 2, H, dk).to(bf), rn(per * dv), torch.sigmoid(rn(per)), rn(B, H, dv).to(bf)
+        sq.sq_norm_in(raw[:, 0], qd, kind=sq.SQ_NORM_L2)
+        sq.sq_norm_in(raw[:, 1], kd, kind=sq.SQ_NORM_L2)
+        sq.sq_state_step(pool, 0, 1, B, wb.ident, qd, kd, vd, wb.gate, bd, yp)
+        sq.sq_fp32_step(wb.form, H, dk, dv, B, 0, 1, B, wb.ident, S, qd, kd, vd, wb.gate, bd, yf)
+        for out, src in zip(o, (yp, yf)):
+            sq.sq_norm_out(src.view(B, H, dv), out, weight=w, z=z)
+        drift.append(_rel(o[0].float(), o[1].float()))
+    print(json.dumps({"experiment": "block", "workload": wl.name, "requests": B, "prompt_tokens": T, "steps": args.steps,
+                      "prompt_scan_ms": scan_ms, "prompt_token_by_token_ms": step_ms,
+                      "metric": "relative L2 of the block's gated output, packed against float32 states after the same prompt",
+                      "output_rel_mean": float(np.mean(drift)), "output_rel_first": drift[0], "output_rel_last": drift[-1]}),
+          flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     sub = ap.add_subparsers(dest="cmd", required=True)
@@ -286,12 +359,17 @@ def main():
     b = sub.add_parser("lifetime")
     b.add_argument("--steps", type=int, default=256)
     b.add_argument("--batch", type=int, default=8)
+    d = sub.add_parser("block")
+    d.add_argument("--workload", default="gdn-decode-32h-128")
+    d.add_argument("--prompt", type=int, default=512)
+    d.add_argument("--batch", type=int, default=32)
+    d.add_argument("--steps", type=int, default=64)
     c = sub.add_parser("overlap")
     c.add_argument("--gemm-k", type=int, default=5120)
     c.add_argument("--gemm-n", type=int, default=24576)
     c.add_argument("--reps", type=int, default=10)
     args = ap.parse_args()
-    {"ablation": ablation, "lifetime": lifetime, "overlap": overlap}[args.cmd](args)
+    {"ablation": ablation, "lifetime": lifetime, "overlap": overlap, "block": block}[args.cmd](args)
 
 
 if __name__ == "__main__":

@@ -335,3 +335,14 @@ def test_prompt_then_packed_decode(dev):
     near(o, yd / (yd.square().mean(-1, keepdim=True) + 1e-6).sqrt() * torch.nn.functional.silu(gate.double().cpu()), "gated norm")
     pool.close()
     plan.close()
+
+
+@pytest.mark.parametrize("workload", ("gdn-decode-32h-64", "kda-decode-32h-64"))
+def test_block_experiment_runs(workload, dev, capsys):
+    import argparse
+    import json
+
+    import experiments
+    experiments.block(argparse.Namespace(workload=workload, prompt=40, batch=3, steps=2))
+    got = json.loads(capsys.readouterr().out.strip().splitlines()[-1])
+    assert got["experiment"] == "block" and got["requests"] == 3 and np.isfinite(got["output_rel_mean"])
