@@ -14,8 +14,14 @@
 // The last sum is taken over exactly those terms, not as a difference of running sums over all of them: each term is
 // proportional to alpha_t, so that the quotient by alpha_t keeps its relative accuracy for small gates.
 //
-// One workgroup per (chunk, q/k head), a wave per 32 key rows; the value heads that share q and k follow one another and
+// One workgroup per (chunk, q/k head), a wave per 16 key rows; the value heads that share q and k follow one another and
 // their dq and dk add up in registers, in a fixed order.
+//
+// Reads 128 KiB of states and gradients per chunk and head (128 x 128), 1.06 GB at 8190 tokens and 32 heads: 174 us at the rate
+// of a copy; the launch takes 490 us there (one gate per head), 266 us at 3001 tokens with gates per key row.  Its vector
+// instructions alone are 141 us, its products 66; the rest is waiting for the states with two waves a SIMD.  A wave per 32 key
+// rows is as fast (480 us) with one gate per head and slower with a gate per key row (307 us), where its registers spill; 16 waves
+// a CU (128 registers, spilling) take 589 and 367 us; all of a workgroup's states in flight at once (spilling) 677 and 322.
 #include <hip/hip_runtime.h>
 
 #include "scan_dev.h"
@@ -86,7 +92,7 @@ __device__ __forceinline__ void prefix_before(float (&v)[2][4], int g) {
 
 template <int DK, int DT, bool KDA>
 struct GradLds {
-    static constexpr int NPL = planes_of(DT), NW = DK >= 64 ? DK / 32 : 1;
+    static constexpr int NPL = planes_of(DT), NW = DK / 16;
     static constexpr int VB = DK, VBP = VB < 32 ? 32 : VB, LDV = VBP + 8;    // value columns staged at a time
     union {
         struct { uint16_t dy[NPL][32][LDV], u[3][32][LDV], w[3][32][LDV]; };
@@ -113,7 +119,7 @@ __device__ __forceinline__ float transpose_sum16(float (&v)[16], int n) {
 }
 
 template <int DK, int DT, bool KDA>
-__global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const ScanParams p) {
+__global__ void __launch_bounds__(DK * 4, 2) k_grad(const ScanParams p) {
     using Lds = GradLds<DK, DT, KDA>;
     constexpr int NPL = Lds::NPL, NW = Lds::NW, ND = DK / 16 / NW, NTHR = NW * 64, ES = DT == SQ_DTYPE_F32 ? 4 : 2;
     constexpr int VB = Lds::VB, VBP = Lds::VBP, LDV = Lds::LDV, OCT = VB / 8, UPT = 32 * OCT / NTHR, JOBS = (6 + NW - 1) / NW;
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
                 for (int r = 0; r < 4; ++r) out[16 * ti + 4 * g + r][16 * tj + n] = bj[j][r];
             }
         }
-        constexpr int MPT = 256 / NTHR;              // units (row, four columns) per thread
+        constexpr int MPT = NTHR < 256 ? 256 / NTHR : 1;         // units (row, four columns) per thread
         if constexpr (!KDA) {
             // sums over the key rows of the terms with the chunk's first state and last gradient
             float sums[16];
@@ -382,6 +388,7 @@ __global__ void __launch_bounds__((DK >= 64 ? 2 * DK : 64), 2) k_grad(const Scan
         // the small matrices as A operands, over the staged rows
 #pragma unroll 1
         for (int u = 0; u < MPT; ++u) {
+            if (NTHR > 256 && tid >= 256) break;
             const int i = (tid + u * NTHR) >> 3, j0 = 4 * ((tid + u * NTHR) & 7);
             if constexpr (!KDA) {
                 const float* ap = p.mat_ap + id * 2048 + i * 32 + j0;
@@ -675,7 +682,7 @@ template <int DK, int DT, bool KDA>
 static hipError_t grad_t(const ScanParams& p, hipStream_t s) {
     const int64_t blocks = p.n_slots * p.n_heads_k;
     if (blocks > 0x7fffffff || p.dv % DK != 0) return hipErrorInvalidValue;
-    k_grad<DK, DT, KDA><<<dim3((unsigned)blocks), dim3(DK >= 64 ? 2 * DK : 64), 0, s>>>(p);
+    k_grad<DK, DT, KDA><<<dim3((unsigned)blocks), dim3(DK * 4), 0, s>>>(p);
     return hipGetLastError();
 }
 
