@@ -119,7 +119,7 @@ __device__ __forceinline__ float transpose_sum16(float (&v)[16], int n) {
 }
 
 template <int DK, int DT, bool KDA>
-__global__ void __launch_bounds__(DK * 4, 2) k_grad(const ScanParams p) {
+__global__ void __launch_bounds__(DK * 4, DK < 64 ? 1 : 2) k_grad(const ScanParams p) {
     using Lds = GradLds<DK, DT, KDA>;
     constexpr int NPL = Lds::NPL, NW = Lds::NW, ND = DK / 16 / NW, NTHR = NW * 64, ES = DT == SQ_DTYPE_F32 ? 4 : 2;
     constexpr int VB = Lds::VB, VBP = Lds::VBP, LDV = Lds::LDV, OCT = VB / 8, UPT = 32 * OCT / NTHR, JOBS = (6 + NW - 1) / NW;

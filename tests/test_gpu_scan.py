@@ -102,6 +102,44 @@ def test_backward(c, dev):
             near(g[n], r[n], n)
 
 
+@pytest.mark.parametrize("dt", (BF16, F16, F32), ids=("bfloat16", "float16", "float32"))
+@pytest.mark.parametrize("form", (0, 1), ids=("gdn", "kda"))
+def test_many_states(form, dt, dev):
+    """More workgroups than CUs: eight computing waves to a workgroup instead of four (both directions)."""
+    H, Hk, dk, dv, lens = 32, 16, 128, 128, [33, 1, 0, 4, 2]
+    x = scan_inputs(form, H, Hk, dk, dv, lens, 71, dt)
+    y, s1 = forward(form, x, lens, dev)
+    yr, sr = scan_ref(x, lens)
+    near(y, yr, "y")
+    near(s1, sr, "s1")
+    g, r = backward(form, x, lens, dev), scan_grad_ref(x, lens)
+    for n in GRADS:
+        near(g[n], r[n], n)
+
+
+@pytest.mark.parametrize("form", (0, 1), ids=("gdn", "kda"))
+def test_many_wide_states(form, dev):
+    H, dk, dv, lens = 32, 128, 256, [5, 33, 1]
+    x = scan_inputs(form, H, H, dk, dv, lens, 72, BF16)
+    y, s1 = forward(form, x, lens, dev)
+    yr, sr = scan_ref(x, lens)
+    near(y, yr, "y")
+    near(s1, sr, "s1")
+
+
+def test_offsets_that_break_the_rules_stay_inside(dev):
+    """Offsets below zero, beyond the arrays or decreasing: results are unspecified, the rows around the arrays stay."""
+    H, dk, dv, N = 2, 64, 64, 40
+    for at in ([-7, 50, 20], [30, 10, 400], [0, 2 ** 31 - 1, 5], [-2 ** 31, 0, 40]):
+        pad = torch.full((N + 16, H * dv), 7.0, device=dev)
+        y = pad[8:8 + N].view(N, H, dv)
+        z = lambda *s: torch.zeros(*s, device=dev)  # noqa: E731
+        sq.sq_delta_scan(0, z(N, H, dk), z(N, H, dk), z(N, H, dv), torch.ones(N, H, device=dev), z(N, H), y,
+                         seq_start=torch.tensor(at, dtype=torch.int32, device=dev), s1=z(2, H, dk, dv))
+        torch.cuda.synchronize()
+        assert (pad[:8] == 7).all() and (pad[8 + N:] == 7).all(), at
+
+
 @pytest.mark.parametrize("form", (0, 1), ids=("gdn", "kda"))
 def test_equal_keys_and_extreme_beta(form, dev):
     """One key for all tokens, no decay, beta 1 or 0: (I + A)^-1 has rows that sum large terms; beta = 0 divides nowhere."""
