@@ -71,6 +71,12 @@ sq_status check_scan_cfg(const sq_scan_cfg* c) {
     return SQ_OK;
 }
 
+// Threads of the launch over all states: 8 computing and 4 staging waves per 128 value columns, 4 and 4 per 64, 1 and 1 per 16.
+int64_t scan_launch_threads(const sq_scan_cfg& c, bool backward) {
+    const int64_t per_col = c.d_k >= 128 ? 768 / 128 : c.d_k >= 64 ? 512 / 64 : 128 / 16;
+    return int64_t(c.n_seq) * c.n_heads * c.d_v * per_col * (backward ? 2 : 1);
+}
+
 // A row array of `heads` x d elements of type dt per token (accessed up to 16 bytes at a time).
 sq_status check_rows(const sq_rows* a, const char* name, int64_t heads, int64_t d, int32_t dt) {
     if (!a || !a->d_ptr) { set_error("%s is NULL", name); return SQ_ERR_ARG; }
@@ -88,6 +94,8 @@ sq_status check_f32(const float* a, const char* name, uintptr_t to) {
     if (!aligned(a, to)) { set_error("%s must be aligned to %u bytes", name, unsigned(to)); return SQ_ERR_ARG; }
     return SQ_OK;
 }
+
+sq_status check_states(const float* a, const char* name) { return a ? check_f32(a, name, 4) : SQ_OK; }
 
 sq_status check_work(const void* work, size_t bytes, size_t need) {
     if (bytes < need) { set_error("workspace of %zu bytes, the call needs %zu", bytes, need); return SQ_ERR_SHAPE; }
@@ -125,11 +133,15 @@ extern "C" sq_status sq_delta_scan_bytes(const sq_scan_cfg* cfg, int32_t backwar
 }
 
 // What both directions share; *empty: there is no sequence and nothing to do.
-static sq_status check_scan(const sq_scan_cfg* cfg, const sq_rows* q, const sq_rows* k, const sq_rows* v,
+static sq_status check_scan(const sq_scan_cfg* cfg, bool backward, const sq_rows* q, const sq_rows* k, const sq_rows* v,
                             const float* d_gate, const float* d_beta, bool* empty) {
     SQ_TRY(check_scan_cfg(cfg));
     *empty = cfg->n_seq == 0;
     if (*empty) return SQ_OK;
+    if (scan_launch_threads(*cfg, backward) > int64_t(0xffffffffu)) {    // what one launch can have
+        set_error("%d sequences of %d heads: too many states in one call", cfg->n_seq, cfg->n_heads);
+        return SQ_ERR_ARG;
+    }
     if (!cfg->d_seq_start && cfg->n_seq != 1) { set_error("d_seq_start is NULL with %d sequences", cfg->n_seq); return SQ_ERR_ARG; }
     if (cfg->n_tokens == 0) return SQ_OK;    // only empty sequences: the row arrays are not read
     SQ_TRY(check_rows(q, "q", cfg->n_heads_k, cfg->d_k, cfg->dtype));
@@ -144,11 +156,13 @@ extern "C" sq_status sq_delta_scan(const sq_scan_cfg* cfg, const sq_rows* q, con
                                    const float* d_gate, const float* d_beta, const float* d_s0, const sq_rows* y,
                                    float* d_s1, void* d_work, size_t work_bytes, void* stream) {
     bool empty = false;
-    SQ_TRY(check_scan(cfg, q, k, v, d_gate, d_beta, &empty));
+    SQ_TRY(check_scan(cfg, false, q, k, v, d_gate, d_beta, &empty));
     if (empty) return SQ_OK;
     if (cfg->n_tokens > 0) SQ_TRY(check_rows(y, "y", cfg->n_heads, cfg->d_v, cfg->dtype));
     const ScanWork w = scan_work(*cfg, false);
     SQ_TRY(check_work(d_work, work_bytes, w.total));
+    SQ_TRY(check_states(d_s0, "s0"));
+    SQ_TRY(check_states(d_s1, "s1"));
     ScanParams p = scan_params(*cfg, w, d_work, false);
     p.q = rows_of(q); p.k = rows_of(k); p.v = rows_of(v); p.y = rows_of(y);
     p.gate = d_gate; p.beta = d_beta; p.s0 = d_s0; p.s1 = d_s1;
@@ -165,7 +179,7 @@ extern "C" sq_status sq_delta_scan_bwd(const sq_scan_cfg* cfg, const sq_rows* q,
                                        float* d_dgate, float* d_dbeta, float* d_ds0, void* d_work, size_t work_bytes,
                                        void* stream) {
     bool empty = false;
-    SQ_TRY(check_scan(cfg, q, k, v, d_gate, d_beta, &empty));
+    SQ_TRY(check_scan(cfg, true, q, k, v, d_gate, d_beta, &empty));
     if (empty) return SQ_OK;
     if (cfg->n_tokens > 0) {
         SQ_TRY(check_rows(dy, "dy", cfg->n_heads, cfg->d_v, cfg->dtype));
@@ -177,6 +191,9 @@ extern "C" sq_status sq_delta_scan_bwd(const sq_scan_cfg* cfg, const sq_rows* q,
     }
     const ScanWork w = scan_work(*cfg, true);
     SQ_TRY(check_work(d_work, work_bytes, w.total));
+    SQ_TRY(check_states(d_s0, "s0"));
+    SQ_TRY(check_states(d_ds1, "ds1"));
+    SQ_TRY(check_states(d_ds0, "ds0"));
     ScanParams p = scan_params(*cfg, w, d_work, true);
     p.q = rows_of(q); p.k = rows_of(k); p.v = rows_of(v); p.dy = rows_of(dy);
     p.dq = rows_of(dq); p.dkk = rows_of(dk); p.dvv = rows_of(dv);

@@ -9,8 +9,8 @@
 //   e = That (V - (gamma K) S);  u = beta e;  y = (gamma Q) S + P u;  S <- gamma_C S + ((gamma_C / gamma) K)^T u
 //
 // k_prep: That and P of every chunk and head, one wave each, all chunks at once.
-// k_scan: the recurrence over a sequence's chunks.  A wave owns 32 value columns of one state (the columns do not
-// interact), in 16 registers per 32 x 32 tile; see scan_dev.h for why no register has to move between products.
+// k_scan: the recurrence over a sequence's chunks.  A wave owns 16 value columns of one state (the columns do not
+// interact), in 4 registers per 16 x 16 tile; see scan_dev.h for why no register has to move between products.
 #include <hip/hip_runtime.h>
 
 #include "scan_dev.h"
@@ -267,8 +267,8 @@ struct ScanLds {
     static constexpr bool REV = MODE == kScanRev, OUT = MODE == kScanOut;
     static constexpr bool VL = DT != SQ_DTYPE_F32;       // v through LDS (there is no room for it in float32)
     static constexpr int NP = KDA ? 3 : planes_of(DT);   // planes of the operands (gates make them float32)
-    // A result that is rounded to 16 bits at once (y) needs no third planes: two leave out 2^-17 of a product where the
-    // rounding takes 2^-9 or 2^-12.  The states and what they are made of always take three.
+    // A result that is rounded to 16 bits at once (y) needs no third planes: two leave out up to 2^-16 of an operand where
+    // the rounding takes 2^-8 or 2^-11 of the result.  The states and what they are made of always take three.
     static constexpr int YP = DT == SQ_DTYPE_F32 ? 3 : 2, NQ = NP < YP ? NP : YP;
     static constexpr int LDK = (DK < 32 ? 32 : DK) + 8, LDT = 40, NMAT = MODE == kScanKeep ? 1 : 2;
     // The chunk's matrices go through LDS where the operands are one plane.  With three, LDS is what a step waits for most,

@@ -1,7 +1,7 @@
 // Device helpers of the gated delta scan: float32 products on the bfloat16 matrix units.
 //
 // A float32 value is the sum of three bfloat16 values (rounded to nearest, then what is left, twice), so a product of
-// two float32 matrices is six bfloat16 products (the three smallest of the nine, below 2^-25 of the largest, are left
+// two float32 matrices is six bfloat16 products (the three smallest of the nine, up to 2^-24 of the largest, are left
 // out): about float32 accuracy at 2500 / 6 TFLOP/s, where the float32 matrix instructions reach 157.  An operand that is
 // a bfloat16 input already is one plane and needs three products.
 //

@@ -1,5 +1,5 @@
-// Loads and stores of the activation types (float32, bfloat16, float16) as float32 registers, shared
-// by the scan and norm kernels.  The type is a run-time value that is the same for a whole launch.
+// The activation types (float32, bfloat16, float16) as float32 registers, shared by the scan and norm
+// kernels.  The type is a run-time value that is the same for a whole launch.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -10,8 +10,6 @@ namespace sq {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4v __attribute__((ext_vector_type(4)));
-
-inline int dtype_bytes(int dt) { return dt == SQ_DTYPE_F32 ? 4 : 2; }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -37,34 +35,12 @@ __device__ __forceinline__ uint32_t f16_bits(float x) {
     return b;
 }
 
-__device__ __forceinline__ float load1(const void* p, int dt, int64_t i) {
-    if (dt == SQ_DTYPE_F32) return static_cast<const float*>(p)[i];
-    const uint32_t h = static_cast<const uint16_t*>(p)[i];
-    return dt == SQ_DTYPE_BF16 ? bf16_lo(h) : f16_val(h);
-}
 __device__ __forceinline__ void store1(void* p, int dt, int64_t i, float x) {
     if (dt == SQ_DTYPE_F32) static_cast<float*>(p)[i] = x;
     else static_cast<uint16_t*>(p)[i] = (uint16_t)(dt == SQ_DTYPE_BF16 ? bf16_bits(x) : f16_bits(x));
 }
 
-// Eight consecutive elements, 16-byte aligned (32 bytes for float32 in two accesses).
-__device__ __forceinline__ void load8(const void* p, int dt, int64_t i, float* x) {
-    if (dt == SQ_DTYPE_F32) {
-        const f32x4* s = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
-        const f32x4 a = s[0], b = s[1];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) { x[j] = a[j]; x[4 + j] = b[j]; }
-        return;
-    }
-    const u32x4v w = *reinterpret_cast<const u32x4v*>(static_cast<const uint16_t*>(p) + i);
-    if (dt == SQ_DTYPE_BF16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) { x[2 * j] = bf16_lo(w[j]); x[2 * j + 1] = bf16_hi(w[j]); }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) { x[2 * j] = f16_val(w[j] & 0xffffu); x[2 * j + 1] = f16_val(w[j] >> 16); }
-    }
-}
+// Eight consecutive elements, 16-byte aligned (float32 in two accesses).
 __device__ __forceinline__ void store8(void* p, int dt, int64_t i, const float* x) {
     if (dt == SQ_DTYPE_F32) {
         f32x4 a, b;
@@ -86,11 +62,6 @@ __device__ __forceinline__ void store8(void* p, int dt, int64_t i, const float* 
     *reinterpret_cast<u32x4v*>(static_cast<uint16_t*>(p) + i) = w;
 }
 
-template <int V>
-__device__ __forceinline__ void loadv(const void* p, int dt, int64_t i, float* x) {
-    if constexpr (V == 8) load8(p, dt, i, x);
-    else x[0] = load1(p, dt, i);
-}
 template <int V>
 __device__ __forceinline__ void storev(void* p, int dt, int64_t i, const float* x) {
     if constexpr (V == 8) store8(p, dt, i, x);

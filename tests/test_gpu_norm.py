@@ -168,6 +168,23 @@ def test_rows_of_zero_and_extreme_gates(dev):
     near(o[0, :64], 100 * hat(y[0].double(), 0, 1e-6)[:64], "open gate")
 
 
+def test_rows_beyond_32_bits(dev):
+    """Arrays of more than 2^32 elements: their last rows equal a call for those rows alone."""
+    R, d, n = 600003, 8192, 5
+    x = torch.empty(R, d, dtype=BF16, device=dev)
+    x[-n:] = rows((n, d), BF16, dev, 1)
+    x[:-n] = 1.0
+    assert x.numel() > 1 << 32
+    o, o2 = torch.empty_like(x), torch.empty(n, d, dtype=BF16, device=dev)
+    sq.sq_norm_in(x, o)
+    sq.sq_norm_in(x[-n:], o2)
+    assert torch.equal(o[-n:], o2)
+    dx, dx2, dw = torch.empty_like(x), torch.empty_like(o2), torch.empty(d, device=dev)
+    sq.sq_norm_in_bwd(x, o, dx, dweight=dw)
+    sq.sq_norm_in_bwd(x[-n:], o2, dx2)
+    assert torch.equal(dx[-n:], dx2) and torch.isfinite(dw).all()
+
+
 def test_no_rows(dev):
     e = torch.empty(0, 64, device=dev)
     dw = torch.full((64,), 5.0, device=dev)

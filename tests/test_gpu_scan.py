@@ -5,6 +5,9 @@ out the terms below 2 * 2^-7 * 2^-15 = 2^-21 of |a||b|; float32 accumulation add
 through at most five such products within a chunk (state, That, P, update; one more for gradients), and the states hand
 errors on, damped by the gates: 5 * 2^-21 = 2.4e-6 of the operands' size, with a factor 4 for terms that cancel:
 1e-5 of an output's largest value.  An output in t adds half a step: torch.finfo(t).eps / 2 of its value.
+The last products of a 16-bit y take two parts, which leave out at most 2^-16 of an operand, of either sign: over the
+16 terms and more of a sum 2^-16 / sqrt(3) of its typical size, some 9e-6 of it, and an output's largest value is three
+and more times its typical one, so the same 1e-5 of the largest value holds them.
 """
 import numpy as np
 import pytest
@@ -300,6 +303,69 @@ def test_runs_are_bitwise_equal_and_streams_are_kept(dev):
     torch.cuda.synchronize()
     for u, w in zip(a, (y, s1, *g.values())):
         assert torch.equal(u, w)
+
+
+def test_two_calls_at_once(dev):
+    """A forward and a backward call on two streams, each with its own workspace, and calls on a third in between."""
+    form, H, dk, dv, lens = 0, 16, 128, 128, [500, 33, 700]
+    x = scan_inputs(form, H, 8, dk, dv, lens, 78, BF16)
+    d = {n: t.to(dev) for n, t in x.items()}
+    at = starts(lens, dev)
+    ya, sa = forward(form, x, lens, dev)
+    ga = backward(form, x, lens, dev)
+    y, s1 = torch.zeros_like(d["v"]), torch.zeros_like(d["s0"])
+    y2, s2 = torch.zeros_like(y), torch.zeros_like(s1)
+    g = {"d" + n: torch.zeros_like(d[n]) for n in ("q", "k", "v", "gate", "beta", "s0")}
+    a, b, c = (torch.cuda.Stream() for _ in range(3))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        sq.sq_delta_scan_bwd(form, d["q"], d["k"], d["v"], d["gate"], d["beta"], d["dy"], g["dq"], g["dk"], g["dv"], g["dgate"],
+                             g["dbeta"], seq_start=at, s0=d["s0"], ds1=d["ds1"], ds0=g["ds0"], stream=a)
+        sq.sq_delta_scan(form, d["q"], d["k"], d["v"], d["gate"], d["beta"], y, seq_start=at, s0=d["s0"], s1=s1, stream=b)
+        sq.sq_delta_scan(form, d["q"], d["k"], d["v"], d["gate"], d["beta"], y2, seq_start=at, s0=d["s0"], s1=s2, stream=c)
+    torch.cuda.synchronize()
+    for u, w in zip((ya, sa, ya, sa, *ga.values()), (y, s1, y2, s2, *g.values())):
+        assert torch.equal(u, w)
+
+
+def test_arrays_beyond_32_bits(dev):
+    """One sequence whose gates pass 4 GiB and whose q rows lie 64 KiB apart: its last piece (a whole number of chunks in)
+    equals a call for that piece from the state before it, bit for bit."""
+    form, H, Hk, dk, dv, T, cut = 1, 32, 2, 128, 128, 280001, 279936
+    r = lambda *s: torch.randn(*s, device=dev)  # noqa: E731
+    wide = torch.zeros(T, 1 << 15, dtype=BF16, device=dev)
+    q, k = wide[:, 512:512 + Hk * dk].unflatten(1, (Hk, dk)), (r(T, Hk, dk) * dk ** -0.5).to(BF16)
+    q.copy_(r(T, Hk, dk))
+    v, y = r(T, H, dv).to(BF16), torch.empty(T, H, dv, dtype=BF16, device=dev)
+    gate, beta = torch.rand(T, H, dk, device=dev).mul_(0.1).add_(0.9), torch.rand(T, H, device=dev)
+    assert gate.numel() * 4 > 1 << 32 and wide.numel() * 2 > 1 << 32
+    s1, sc, s2 = (torch.empty(1, H, dk, dv, device=dev) for _ in range(3))
+    sq.sq_delta_scan(form, q, k, v, gate, beta, y, s1=s1)
+    say("whole sequence queued")
+    y2 = torch.empty_like(y[cut:])
+    sq.sq_delta_scan(form, q[:cut], k[:cut], v[:cut], gate[:cut], beta[:cut], torch.empty_like(y[:cut]), s1=sc)
+    sq.sq_delta_scan(form, q[cut:], k[cut:], v[cut:], gate[cut:], beta[cut:], y2, s0=sc, s1=s2)
+    assert torch.isfinite(y).all() and torch.equal(y[cut:], y2) and torch.equal(s1, s2)
+
+
+def test_gradients_with_states_beyond_32_bits(dev):
+    """States and their gradients of more than 2^31 elements each in the workspace: the last piece's gradients equal a
+    call for that piece from the state before it."""
+    form, H, Hk, dk, dv, T, cut = 0, 32, 8, 128, 128, 140001, 139936
+    assert (cut // 32) * H * dk * dv > 1 << 31 and cut % 32 == 0
+    r = lambda *s: torch.randn(*s, device=dev)  # noqa: E731
+    q, k, v, dy = r(T, Hk, dk).to(BF16), (r(T, Hk, dk) * dk ** -0.5).to(BF16), r(T, H, dv).to(BF16), r(T, H, dv).to(BF16)
+    gate, beta = torch.rand(T, H, device=dev).mul_(0.1).add_(0.9), torch.rand(T, H, device=dev)
+    sc = torch.empty(1, H, dk, dv, device=dev)
+    sq.sq_delta_scan(form, q[:cut], k[:cut], v[:cut], gate[:cut], beta[:cut], torch.empty_like(v[:cut]), s1=sc)
+    out = lambda s: [torch.empty_like(t[s]) for t in (q, k, v, gate, beta)]  # noqa: E731
+    whole, last = out(slice(0, T)), out(slice(cut, T))
+    sq.sq_delta_scan_bwd(form, q, k, v, gate, beta, dy, *whole)
+    say("whole sequence queued")
+    sq.sq_delta_scan_bwd(form, q[cut:], k[cut:], v[cut:], gate[cut:], beta[cut:], dy[cut:], *last, s0=sc)
+    for a, b, n in zip(whole, last, GRADS):
+        assert torch.isfinite(a).all(), n
+        near(a[cut:], b.double().cpu(), n, 2 * TOL + (0.0 if a.dtype == F32 else torch.finfo(a.dtype).eps / 2))    # both round
 
 
 def test_captured_and_replayed(dev):

@@ -36,7 +36,8 @@ def scan(cfg, backward=False, nbytes=1 << 40, work=BASE, **kw):
 BAD_CFG = [(dict(form=2), ARG), (dict(dtype=3), ARG), (dict(dtype=-1), ARG), (dict(n_heads=0), ARG), (dict(n_heads_k=3), ARG),
            (dict(n_heads_k=0), ARG), (dict(n_heads=4097, n_heads_k=4097), ARG), (dict(d_k=96), UNSUPPORTED),
            (dict(d_k=64, d_v=128), UNSUPPORTED), (dict(n_seq=-1), ARG), (dict(n_tokens=-1), ARG), (dict(n_tokens=1 << 31), ARG),
-           (dict(n_heads=4096, n_heads_k=4096, n_seq=1 << 20), ARG), (dict(d_seq_start=None), ARG)]
+           (dict(n_heads=4096, n_heads_k=4096, n_seq=1 << 20), ARG), (dict(d_seq_start=None), ARG),
+           (dict(n_heads=64, n_heads_k=64, n_seq=90000, n_tokens=0), ARG)]
 
 
 @pytest.mark.parametrize("kw,st", BAD_CFG, ids=[str(b[0]) for b in BAD_CFG])
@@ -62,6 +63,9 @@ def test_scan_arrays():
         assert scan(c, **{n: R(ptr=BASE + 8, stride=256)}) == ARG       # read 16 bytes at a time
         assert scan(c, **{n: R(stride=260)}) == ARG
     assert scan(c, True, dy=R(stride=516)) == ARG
+    for bwd, names in ((False, ("s0", "s1")), (True, ("s0", "ds1", "ds0"))):
+        for n in names:
+            assert scan(c, bwd, **{n: BASE + 2}) == ARG
     assert scan(scan_cfg(form=1), gate=BASE + 4) == ARG
 
 
