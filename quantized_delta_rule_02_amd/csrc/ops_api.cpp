@@ -77,6 +77,10 @@ int64_t scan_launch_threads(const sq_scan_cfg& c, bool backward) {
     return int64_t(c.n_seq) * c.n_heads * c.d_v * per_col * (backward ? 2 : 1);
 }
 
+// Sequences of at most kShortLen tokens go token by token where the mean is no longer than that (the lengths are the device's).
+constexpr int kShortLen = 8;
+bool takes_short(const sq_scan_cfg& c) { return c.d_k >= 64 && c.n_tokens <= int64_t(kShortLen) * c.n_seq; }
+
 // A row array of `heads` x d elements of type dt per token (accessed up to 16 bytes at a time).
 sq_status check_rows(const sq_rows* a, const char* name, int64_t heads, int64_t d, int32_t dt) {
     if (!a || !a->d_ptr) { set_error("%s is NULL", name); return SQ_ERR_ARG; }
@@ -108,6 +112,7 @@ ScanRows rows_of(const sq_rows* a) { return a ? ScanRows{a->d_ptr, a->stride} : 
 ScanParams scan_params(const sq_scan_cfg& c, const ScanWork& w, void* work, bool backward) {
     ScanParams p{};
     p.form = c.form; p.dtype = c.dtype; p.n_heads = c.n_heads; p.n_heads_k = c.n_heads_k; p.dk = c.d_k; p.dv = c.d_v;
+    p.short_len = -1;
     p.n_seq = c.n_seq; p.n_tokens = c.n_tokens; p.n_slots = scan_slots(c.n_tokens, c.n_seq); p.seq_start = c.d_seq_start;
     char* base = static_cast<char*>(work);
     auto u16 = [base](size_t o) { return reinterpret_cast<uint16_t*>(base + o); };
@@ -167,7 +172,14 @@ extern "C" sq_status sq_delta_scan(const sq_scan_cfg* cfg, const sq_rows* q, con
     p.q = rows_of(q); p.k = rows_of(k); p.v = rows_of(v); p.y = rows_of(y);
     p.gate = d_gate; p.beta = d_beta; p.s0 = d_s0; p.s1 = d_s1;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e = cfg->n_tokens > 0 ? launch_scan_prep(p, false, s) : hipSuccess;
+    hipError_t e = hipSuccess;
+    if (takes_short(*cfg)) {
+        p.short_len = kShortLen;
+        e = launch_scan_short(p, s);
+        if (e != hipSuccess) return fail_hip(e, "short scan launch");
+        if (cfg->n_tokens <= kShortLen) return SQ_OK;            // no sequence can be longer
+    }
+    if (cfg->n_tokens > 0) e = launch_scan_prep(p, false, s);
     if (e != hipSuccess) return fail_hip(e, "scan preparation launch");
     e = launch_scan(p, false, s);
     return e == hipSuccess ? SQ_OK : fail_hip(e, "scan launch");

@@ -333,6 +333,7 @@ struct Scan {
     __device__ __forceinline__ void stage(int tid);
     __device__ __forceinline__ void compute(int wave, int l);
     __device__ __forceinline__ void run() {
+        if (len <= p.short_len) return;              // the whole workgroup
         const int tid = (int)threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         if constexpr (DK < 32) {                     // the unused half of a block of 32 key rows stays zero
             for (int i = tid; i < 2 * NP * 32 * LDK; i += (NC + NS) * 64) {

@@ -125,7 +125,7 @@ __device__ __forceinline__ int64_t first_slot(const Seq& q, int b) { return (q.s
 // either way, and the quotient stays one of normal numbers, also for a gate of zero.  The states take the gates as they are.
 constexpr float kGateMin = 1e-30f;
 
-// The chunk of a slot: its first token and how many it has (0: no chunk uses the slot).  A binary search for the sequence
+// The chunk of a slot: its first token and how many it has (0: no chunk uses the slot, or not the chunked scan's).  A binary search for the sequence
 // whose first slot is the last one not above the slot.
 struct ChunkAt {
     int64_t tok0;
@@ -141,7 +141,7 @@ __device__ __forceinline__ ChunkAt chunk_of_slot(const ScanParams& p, int64_t sl
     const Seq q = sequence(p, lo);
     const int64_t c0 = (slot - first_slot(q, lo)) * kChunk;
     const int start = __builtin_amdgcn_readfirstlane((int)(q.start + c0));
-    int64_t rem = c0 < 0 ? 0 : q.len - c0;
+    int64_t rem = c0 < 0 || q.len <= p.short_len ? 0 : q.len - c0;
     rem = rem < 0 ? 0 : rem > kChunk ? kChunk : rem;
     return ChunkAt{start, __builtin_amdgcn_readfirstlane((int)rem)};
 }

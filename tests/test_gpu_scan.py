@@ -130,6 +130,68 @@ def test_many_wide_states(form, dev):
     near(s1, sr, "s1")
 
 
+SHORT = [(0, BF16, 4, 2, 128, 128), (0, F16, 2, 2, 128, 256), (0, F32, 3, 1, 64, 64), (0, F32, 2, 1, 128, 128),
+         (1, BF16, 4, 4, 128, 128), (1, F16, 3, 1, 64, 64), (1, F32, 2, 2, 128, 256), (0, BF16, 2, 1, 16, 16), (1, F32, 2, 2, 16, 16)]
+
+
+@pytest.mark.parametrize("gate", ("usual", "strong"))
+@pytest.mark.parametrize("c", SHORT, ids=[f"{'kda' if c[0] else 'gdn'}-{str(c[1])[6:]}-{c[2]}h{c[3]}-{c[4]}x{c[5]}" for c in SHORT])
+def test_short_sequences(c, gate, dev):
+    """Few tokens a sequence, all lengths up to 10 and one of 40 among them: the sequences of up to 8 go token by token."""
+    form, dt, H, Hk, dk, dv = c
+    lens = [1, 0, 8, 2, 9, 3, 40, 4, 1, 5, 10, 6, 0, 7, 1, 1, 8, 2]
+    assert sum(lens) <= 8 * len(lens)
+    x = scan_inputs(form, H, Hk, dk, dv, lens, 61, dt, gate)
+    for s0 in (True, False):
+        y, s1 = forward(form, x, lens, dev, s0)
+        yr, sr = scan_ref(x, lens, s0)
+        near(y, yr, "y")
+        near(s1, sr, "s1")
+    for few in ([3], [0, 8], [1] * 5):               # no sequence can be longer: nothing else runs
+        x = scan_inputs(form, H, Hk, dk, dv, few, 62, dt, gate)
+        y, s1 = forward(form, x, few, dev)
+        yr, sr = scan_ref(x, few)
+        near(y, yr, "y")
+        near(s1, sr, "s1")
+
+
+def test_short_sequences_in_wider_arrays_in_place_and_captured(dev):
+    """Parts of wider arrays with NaN around them, tokens of no sequence, the states replaced in place; the captured call
+    replayed gives what the eager calls give."""
+    form, H, Hk, dk, dv, lens, lead, tail = 1, 4, 2, 128, 128, [1, 5, 12, 0, 8], 2, 3
+    x = scan_inputs(form, H, Hk, dk, dv, lens, 63, BF16)
+    T = sum(lens)
+    assert lead + T + tail <= 8 * len(lens)
+    nan = lambda *s, dt=BF16: torch.full(s, float("nan"), dtype=dt, device=dev)  # noqa: E731
+    N, wide = lead + T + tail, nan(lead + T + tail, 2 * Hk * dk + H * dv + 8)
+    q, k = (wide[:, i * Hk * dk:(i + 1) * Hk * dk].unflatten(1, (Hk, dk)) for i in (0, 1))
+    v = wide[:, 2 * Hk * dk:2 * Hk * dk + H * dv].unflatten(1, (H, dv))
+    gate, beta = nan(N, H, dk, dt=F32), nan(N, H, dt=F32)
+    for a, n in ((q, "q"), (k, "k"), (v, "v"), (gate, "gate"), (beta, "beta")):
+        a[lead:lead + T] = x[n].to(dev)
+    out = torch.full((N, H * dv + 8), 7.0, dtype=BF16, device=dev)
+    y, st, at = out[:, :H * dv].unflatten(1, (H, dv)), x["s0"].to(dev), starts(lens, dev, lead)
+    work = torch.empty(sq.sq_delta_scan_bytes(form, BF16, H, Hk, dk, dv, len(lens), N), dtype=torch.uint8, device=dev)
+    call = lambda: sq.sq_delta_scan(form, q, k, v, gate, beta, y, seq_start=at, s0=st, s1=st, workspace=work)  # noqa: E731
+    call()
+    yr, sr = scan_ref(x, lens)
+    near(y[lead:lead + T], yr, "y")
+    near(st, sr, "s1")
+    assert (out[:lead] == 7).all() and (out[lead + T:] == 7).all() and (out[:, H * dv:] == 7).all()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        before = st.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone(), st.clone()
+        st.copy_(before)
+        call()
+        assert torch.equal(got[1], st) and torch.equal(got[0][lead:lead + T], y[lead:lead + T])
+
+
 def test_offsets_that_break_the_rules_stay_inside(dev):
     """Offsets below zero, beyond the arrays or decreasing: results are unspecified, the rows around the arrays stay."""
     H, dk, dv, N = 2, 64, 64, 40
