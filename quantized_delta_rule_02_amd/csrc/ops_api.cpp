@@ -113,6 +113,7 @@ ScanParams scan_params(const sq_scan_cfg& c, const ScanWork& w, void* work, bool
     ScanParams p{};
     p.form = c.form; p.dtype = c.dtype; p.n_heads = c.n_heads; p.n_heads_k = c.n_heads_k; p.dk = c.d_k; p.dv = c.d_v;
     p.short_len = -1;
+    p.n_long = c.n_seq;
     p.n_seq = c.n_seq; p.n_tokens = c.n_tokens; p.n_slots = scan_slots(c.n_tokens, c.n_seq); p.seq_start = c.d_seq_start;
     char* base = static_cast<char*>(work);
     auto u16 = [base](size_t o) { return reinterpret_cast<uint16_t*>(base + o); };
@@ -178,6 +179,8 @@ extern "C" sq_status sq_delta_scan(const sq_scan_cfg* cfg, const sq_rows* q, con
         e = launch_scan_short(p, s);
         if (e != hipSuccess) return fail_hip(e, "short scan launch");
         if (cfg->n_tokens <= kShortLen) return SQ_OK;            // no sequence can be longer
+        const int64_t n_long = cfg->n_tokens / (kShortLen + 1);
+        if (n_long < p.n_long) p.n_long = int32_t(n_long);
     }
     if (cfg->n_tokens > 0) e = launch_scan_prep(p, false, s);
     if (e != hipSuccess) return fail_hip(e, "scan preparation launch");

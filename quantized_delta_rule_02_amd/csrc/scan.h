@@ -22,6 +22,7 @@ struct ScanParams {
     int32_t form, dtype, n_heads, n_heads_k, dk, dv, n_seq;
     int64_t n_tokens, n_slots;
     int64_t short_len;               // sequences of at most this length are not the chunked scan's (-1: all are)
+    int32_t n_long;                  // at most so many are the chunked scan's
     const int32_t* seq_start;        // [n_seq + 1], or NULL: one sequence of n_tokens
     ScanRows q, k, v, y;
     const float* gate;               // [n_tokens][H] or [n_tokens][H][dk]

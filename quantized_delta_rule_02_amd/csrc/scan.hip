@@ -316,10 +316,12 @@ struct Scan {
 
     __device__ __forceinline__ Scan(const ScanParams& p_, Lds& s_, unsigned block) : p(p_), s(s_) {
         H = p.n_heads;
-        const int bh = (int)(block % (unsigned)(H * p.n_seq));
-        sg = (int)(block / (unsigned)(H * p.n_seq));
+        const int bh = (int)(block % (unsigned)(H * p.n_long));
+        sg = (int)(block / (unsigned)(H * p.n_long));
         b = bh / H;
         h = bh % H;
+        if (p.short_len >= 0) b = __builtin_amdgcn_readfirstlane(long_sequence(p, b));
+        if (b < 0) return;                           // see run()
         const Seq sv = sequence(p, b);
         start = __builtin_amdgcn_readfirstlane((int)sv.start);
         len = __builtin_amdgcn_readfirstlane((int)sv.len);
@@ -333,7 +335,7 @@ struct Scan {
     __device__ __forceinline__ void stage(int tid);
     __device__ __forceinline__ void compute(int wave, int l);
     __device__ __forceinline__ void run() {
-        if (len <= p.short_len) return;              // the whole workgroup
+        if (b < 0) return;                           // no such sequence: the whole workgroup leaves
         const int tid = (int)threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         if constexpr (DK < 32) {                     // the unused half of a block of 32 key rows stays zero
             for (int i = tid; i < 2 * NP * 32 * LDK; i += (NC + NS) * 64) {
@@ -840,7 +842,7 @@ static hipError_t prep_t(const ScanParams& p, bool backward, hipStream_t s) {
 template <int DK, int DT, bool KDA, int NC>
 static hipError_t scan_nc(const ScanParams& p, bool backward, hipStream_t s) {
     if (p.dv % (16 * NC) != 0) return hipErrorInvalidValue;
-    const int64_t blocks = (int64_t)p.n_seq * p.n_heads * (p.dv / (16 * NC)) * (backward ? 2 : 1);
+    const int64_t blocks = (int64_t)p.n_long * p.n_heads * (p.dv / (16 * NC)) * (backward ? 2 : 1);
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks), blk(scan_threads(DK, NC));
     if (backward) k_scan_both<DK, DT, KDA, NC><<<grid, blk, 0, s>>>(p, (unsigned)(blocks / 2));
@@ -854,7 +856,7 @@ static hipError_t scan_t(const ScanParams& p, bool backward, hipStream_t s) {
     // below that, four put the columns on twice as many CUs (a prompt of 777 tokens: 61 us, with eight 73; seven prompts of
     // 12301 tokens, 448 workgroups of four: 288 us, with eight 268).
     if constexpr (DK == 128) {
-        if ((int64_t)p.n_seq * p.n_heads * (p.dv / 64) * (backward ? 2 : 1) > 256) return scan_nc<DK, DT, KDA, 8>(p, backward, s);
+        if ((int64_t)p.n_long * p.n_heads * (p.dv / 64) * (backward ? 2 : 1) > 256) return scan_nc<DK, DT, KDA, 8>(p, backward, s);
     }
     return scan_nc<DK, DT, KDA, DK < 32 ? 1 : 4>(p, backward, s);
 }

@@ -125,18 +125,36 @@ __device__ __forceinline__ int64_t first_slot(const Seq& q, int b) { return (q.s
 // either way, and the quotient stays one of normal numbers, also for a gate of zero.  The states take the gates as they are.
 constexpr float kGateMin = 1e-30f;
 
-// The chunk of a slot: its first token and how many it has (0: no chunk uses the slot, or not the chunked scan's).  A binary search for the sequence
-// whose first slot is the last one not above the slot.
+// The i-th sequence longer than short_len, or -1.  A whole wave looks at 64 sequences at a time.
+__device__ __forceinline__ int long_sequence(const ScanParams& p, int i) {
+    for (int b0 = 0; b0 < p.n_seq; b0 += 64) {
+        const int b = b0 + ((int)threadIdx.x & 63);
+        uint64_t m = __ballot(b < p.n_seq && sequence(p, b < p.n_seq ? b : 0).len > p.short_len);
+        const int c = __popcll(m);
+        if (i < c) {
+            while (i-- > 0) m &= m - 1;
+            return b0 + __builtin_ctzll(m);
+        }
+        i -= c;
+    }
+    return -1;
+}
+
+// The chunk of a slot: its first token and how many it has (0: no chunk uses the slot, or not the chunked scan's).  Of the
+// sequences whose first slot is not above the slot it is the last one's: a search by 64 lanes at a time (one round for 64
+// sequences, two for 4096), since a round is a load's latency.
 struct ChunkAt {
     int64_t tok0;
     int rem;
 };
 __device__ __forceinline__ ChunkAt chunk_of_slot(const ScanParams& p, int64_t slot) {
-    int lo = 0, hi = p.n_seq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first_slot(sequence(p, mid), mid) <= slot) lo = mid;
-        else hi = mid - 1;
+    int lo = 0, n = p.n_seq;                         // it is one of the n from lo
+    while (n > 1) {
+        const int step = (n + 63) / 64, at = ((int)threadIdx.x & 63) * step;
+        const bool below = at < n && first_slot(sequence(p, lo + at), lo + at) <= slot;
+        const int last = 63 - __builtin_clzll(__ballot(below) | 1);
+        lo += last * step;
+        n = n - last * step < step ? n - last * step : step;
     }
     const Seq q = sequence(p, lo);
     const int64_t c0 = (slot - first_slot(q, lo)) * kChunk;

@@ -14,8 +14,6 @@
 
 namespace sq {
 
-typedef float f32x4w __attribute__((ext_vector_type(4), aligned(4)));   // states are aligned to their elements only
-
 template <int DK, int DT, bool KDA>
 __global__ void __launch_bounds__(256, DT == SQ_DTYPE_F32 || KDA ? 2 : 4) k_short(const ScanParams p) {
     constexpr int R = DK / 8, ES = DT == SQ_DTYPE_F32 ? 4 : 2, W = 16 / ES;      // key rows of a lane; elements per 16 bytes
@@ -28,11 +26,14 @@ __global__ void __launch_bounds__(256, DT == SQ_DTYPE_F32 || KDA ? 2 : 4) k_shor
     const Seq sv = sequence(p, b);
     if (sv.len > p.short_len) return;                // the chunked scan's
     const int len = __builtin_amdgcn_readfirstlane((int)sv.len);
+    const int64_t start = __builtin_amdgcn_readfirstlane((int)sv.start);
 
-    const int64_t at = (st * DK + kl * R) * dv + col;
+    // all addresses are one wave's base, a lane's 32-bit offset and a row's: none takes registers of its own
+    const uint32_t at = (uint32_t)(kl * R * dv + col) * 4, bytes = (uint32_t)(DK * dv) * 4;
+    const Window w0(p.s0 + st * DK * dv, p.s0 ? bytes : 0);      // no first states: zeros
     f32x4 S[R];
 #pragma unroll
-    for (int j = 0; j < R; ++j) S[j] = p.s0 ? f32x4(*reinterpret_cast<const f32x4w*>(p.s0 + at + (int64_t)j * dv)) : f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < R; ++j) S[j] = __builtin_bit_cast(f32x4, (u32x4v)__builtin_amdgcn_raw_buffer_load_b128(w0.r, at, j * dv * 4, 0));
 
     using Words = std::conditional_t<ES == 4, u32x4v, u32x2>;       // four elements
     struct Token {                                   // as loaded
@@ -42,18 +43,20 @@ __global__ void __launch_bounds__(256, DT == SQ_DTYPE_F32 || KDA ? 2 : 4) k_shor
     };
     auto load = [&](int64_t t) {
         Token x;
-        const char* kp = static_cast<const char*>(p.k.p) + (t * p.k.stride + hk * DK + kl * R) * ES;
-        const char* qp = static_cast<const char*>(p.q.p) + (t * p.q.stride + hk * DK + kl * R) * ES;
+        const Window wk(static_cast<const char*>(p.k.p) + (t * p.k.stride + hk * DK) * ES, DK * ES);
+        const Window wq(static_cast<const char*>(p.q.p) + (t * p.q.stride + hk * DK) * ES, DK * ES);
+        const Window wv(static_cast<const char*>(p.v.p) + (t * p.v.stride + h * dv) * ES, dv * ES);
 #pragma unroll
         for (int i = 0; i < R / W; ++i) {
-            x.k[i] = reinterpret_cast<const u32x4v*>(kp)[i];
-            x.q[i] = reinterpret_cast<const u32x4v*>(qp)[i];
+            x.k[i] = __builtin_amdgcn_raw_buffer_load_b128(wk.r, kl * R * ES + 16 * i, 0, 0);
+            x.q[i] = __builtin_amdgcn_raw_buffer_load_b128(wq.r, kl * R * ES + 16 * i, 0, 0);
         }
-        x.v = *reinterpret_cast<const Words*>(static_cast<const char*>(p.v.p) + (t * p.v.stride + h * dv + col) * ES);
+        if constexpr (ES == 4) x.v = __builtin_amdgcn_raw_buffer_load_b128(wv.r, col * ES, 0, 0);
+        else x.v = __builtin_amdgcn_raw_buffer_load_b64(wv.r, col * ES, 0, 0);
         if constexpr (KDA) {
-            const u32x4v* ap = reinterpret_cast<const u32x4v*>(p.gate + (t * H + h) * DK + kl * R);
+            const Window wa(p.gate + (t * H + h) * DK, DK * 4);
 #pragma unroll
-            for (int i = 0; i < R / 4; ++i) x.a[i] = ap[i];
+            for (int i = 0; i < R / 4; ++i) x.a[i] = __builtin_amdgcn_raw_buffer_load_b128(wa.r, kl * R * 4 + 16 * i, 0, 0);
         } else {
             x.gate = p.gate[t * H + h];
         }
@@ -65,10 +68,10 @@ __global__ void __launch_bounds__(256, DT == SQ_DTYPE_F32 || KDA ? 2 : 4) k_shor
         else return val1<DT>((j & 1) ? w[j / 2] >> 16 : w[j / 2] & 0xffffu);
     };
     Token next;
-    if (len > 0) next = load(sv.start);
+    if (len > 0) next = load(start);
     for (int t = 0; t < len; ++t) {
         const Token x = next;
-        if (t + 1 < len) next = load(sv.start + t + 1);
+        if (t + 1 < len) next = load(start + t + 1);
         f32x4 sk{0.f, 0.f, 0.f, 0.f}, sq{0.f, 0.f, 0.f, 0.f};
         float qk = 0.f;
 #pragma unroll
@@ -95,21 +98,22 @@ __global__ void __launch_bounds__(256, DT == SQ_DTYPE_F32 || KDA ? 2 : 4) k_shor
         for (int j = 0; j < R; ++j) S[j] += value(x.k[j / W], j % W) * u;
         if (kl == 0) {
             const f32x4 y = sq + qk * u;
-            char* yp = static_cast<char*>(p.y.p) + ((sv.start + t) * p.y.stride + h * dv + col) * ES;
+            const Window wy(static_cast<const char*>(p.y.p) + ((start + t) * p.y.stride + h * dv) * ES, dv * ES);
             if constexpr (DT == SQ_DTYPE_F32) {
-                *reinterpret_cast<f32x4*>(yp) = y;
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, y), wy.r, col * ES, 0, 0);
             } else {
                 u32x2 w;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     w[i] = DT == SQ_DTYPE_BF16 ? round_pair(y[2 * i], y[2 * i + 1]) : f16_bits(y[2 * i]) | f16_bits(y[2 * i + 1]) << 16;
-                *reinterpret_cast<u32x2*>(yp) = w;
+                __builtin_amdgcn_raw_buffer_store_b64(w, wy.r, col * ES, 0, 0);
             }
         }
     }
     if (p.s1) {
+        const Window w1(p.s1 + st * DK * dv, bytes);
 #pragma unroll
-        for (int j = 0; j < R; ++j) *reinterpret_cast<f32x4w*>(p.s1 + at + (int64_t)j * dv) = S[j];
+        for (int j = 0; j < R; ++j) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, S[j]), w1.r, at, j * dv * 4, 0);
     }
 }
 
