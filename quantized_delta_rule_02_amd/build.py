@@ -16,7 +16,7 @@ OUT = os.path.join(HERE, "libstepq.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 ARCH = os.environ.get("STEPQ_ARCH", "gfx950")
 
-SOURCES = ["api.cpp", "ops_api.cpp", "planner.cpp", "kernels.hip", "probe.hip", "norm.hip", "scan.hip", "scan_short.hip", "scan_bwd.hip"]
+SOURCES = ["api.cpp", "ops_api.cpp", "planner.cpp", "kernels.hip", "probe.hip", "norm.hip", "scan.hip", "scan_prep.hip", "scan_bwd.hip"]
 
 
 def _hipcc() -> str:
@@ -37,7 +37,7 @@ def build(verbose: bool = False) -> str:
     device = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
     step = ["-munsafe-fp-atomics", "-mno-amdgpu-ieee", "-fno-honor-nans"]
     # the norms and the scan let NaN and infinities through
-    ieee = {"norm.hip", "scan.hip", "scan_short.hip", "scan_bwd.hip"}
+    ieee = {"norm.hip", "scan.hip", "scan_prep.hip", "scan_bwd.hip"}
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD_DIR, src.replace(".", "_") + ".o")

@@ -176,14 +176,15 @@ extern "C" sq_status sq_delta_scan(const sq_scan_cfg* cfg, const sq_rows* q, con
     hipError_t e = hipSuccess;
     if (takes_short(*cfg)) {
         p.short_len = kShortLen;
-        e = launch_scan_short(p, s);
-        if (e != hipSuccess) return fail_hip(e, "short scan launch");
-        if (cfg->n_tokens <= kShortLen) return SQ_OK;            // no sequence can be longer
-        const int64_t n_long = cfg->n_tokens / (kShortLen + 1);
+        const int64_t n_long = cfg->n_tokens / (kShortLen + 1);          // no more sequences can be longer
         if (n_long < p.n_long) p.n_long = int32_t(n_long);
+        e = launch_scan_short(p, n_long > 0, s);
+        if (e != hipSuccess) return fail_hip(e, "short scan launch");
+        if (n_long == 0) return SQ_OK;
+    } else {
+        if (cfg->n_tokens > 0) e = launch_scan_prep(p, false, s);
+        if (e != hipSuccess) return fail_hip(e, "scan preparation launch");
     }
-    if (cfg->n_tokens > 0) e = launch_scan_prep(p, false, s);
-    if (e != hipSuccess) return fail_hip(e, "scan preparation launch");
     e = launch_scan(p, false, s);
     return e == hipSuccess ? SQ_OK : fail_hip(e, "scan launch");
 }

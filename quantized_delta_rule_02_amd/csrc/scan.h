@@ -1,4 +1,4 @@
-// Launchers of the gated delta scan (scan.hip, scan_short.hip, scan_bwd.hip), called by the C ABI (ops_api.cpp).
+// Launchers of the gated delta scan (scan_prep.hip, scan.hip, scan_bwd.hip), called by the C ABI (ops_api.cpp).
 //
 // Workspace of a call, per chunk slot and head (chunks of 32 tokens, counted from each sequence's start):
 // chunk c of sequence b has the slot (start_b >> 5) + b + c.  Slots of different chunks differ, because
@@ -54,7 +54,8 @@ inline int64_t scan_slots(int64_t n_tokens, int n_seq) { return (n_tokens / kChu
 hipError_t launch_scan_prep(const ScanParams& p, bool backward, hipStream_t s);
 hipError_t launch_scan(const ScanParams& p, bool backward, hipStream_t s);
 hipError_t launch_scan_grad(const ScanParams& p, hipStream_t s);
-// The sequences of at most short_len tokens, token by token (d_k of 64 and more; outputs and final states).
-hipError_t launch_scan_short(const ScanParams& p, hipStream_t s);
+// The sequences of at most short_len tokens, token by token (d_k of 64 and more; outputs and final states), and with prep, in
+// the same launch, the preparation of the others.
+hipError_t launch_scan_short(const ScanParams& p, bool prep, hipStream_t s);
 
 }  // namespace sq

@@ -8,7 +8,7 @@
 //   A_tj = k_t . Gamma_tj k_j (j < t),  P_tj = q_t . Gamma_tj k_j (j <= t),  That = (I + A diag(beta))^-1
 //   e = That (V - (gamma K) S);  u = beta e;  y = (gamma Q) S + P u;  S <- gamma_C S + ((gamma_C / gamma) K)^T u
 //
-// k_prep: That and P of every chunk and head, one wave each, all chunks at once.
+// k_prep (scan_prep.hip): That and P of every chunk and head, one wave each, all chunks at once.
 // k_scan: the recurrence over a sequence's chunks.  A wave owns 16 value columns of one state (the columns do not
 // interact), in 4 registers per 16 x 16 tile; see scan_dev.h for why no register has to move between products.
 #include <hip/hip_runtime.h>
@@ -16,242 +16,6 @@
 #include "scan_dev.h"
 
 namespace sq {
-
-// ---------------------------------------------------------------- prep
-
-constexpr int kPrepWaves = 4;
-constexpr int kPrepLd = 36;          // 16-byte aligned rows, 4 banks apart
-
-// One wave per chunk and head.  Its LDS is one 32 x 32 matrix (two for the backward pass), used in turn for I + N, for
-// its inverse and for P, so that four and more waves fit on a SIMD: with all of them side by side (18 KiB a wave, two
-// waves) the launch took 118 us where it now takes 61 (12301 tokens, 32 heads, bfloat16).
-template <int DK, int DT, bool KDA, bool BWD>
-__global__ void __launch_bounds__(kPrepWaves * 64) k_prep(const ScanParams p) {
-    constexpr int NKB = (DK + 31) / 32, NPL = planes_of(DT), NM = BWD ? 2 : 1, ES = DT == SQ_DTYPE_F32 ? 4 : 2;
-    __shared__ __align__(16) float s_m[kPrepWaves][NM][32][kPrepLd];
-    __shared__ float s_gt[KDA ? 1 : kPrepWaves][2][5][32];
-    __shared__ float s_b[kPrepWaves][32];
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), l = (int)threadIdx.x & 63, n = l & 15, g = l >> 4;
-    const int64_t id = (int64_t)blockIdx.x * kPrepWaves + wave;
-    if (id >= p.n_slots * p.n_heads) return;         // no workgroup barrier below: each wave works alone
-    const int h = (int)(id % p.n_heads);
-    const ChunkAt ck = chunk_of_slot(p, id / p.n_heads);
-    if (ck.rem <= 0) return;                         // a slot that no chunk uses
-    const int rem = ck.rem, H = p.n_heads, hk = h / (H / p.n_heads_k);
-    const int64_t tok0 = ck.tok0;
-    constexpr float gmin = BWD ? kGateMin : 0.f;
-
-    float(&M)[NM][32][kPrepLd] = s_m[wave];
-    if (l < 32) s_b[wave][l] = l < rem ? p.beta[(tok0 + l) * H + h] : 0.f;
-    if constexpr (!KDA) {
-        const int t = l & 31;
-        const float a = t < rem ? p.gate[(tok0 + t) * H + h] : 1.f;
-        GateLevels<float> lv(fmaxf(a, gmin));
-#pragma unroll
-        for (int lev = 0; lev < 5; ++lev) {
-            if (l < 32) {
-                s_gt[wave][0][lev][t] = lv.pre;
-                s_gt[wave][1][lev][t] = lv.suf;
-            }
-            lv.grow((t >> lev) & 1, __shfl_xor(lv.full, 1 << lev));
-        }
-        // the gates' products up to each token and after it, for the scan (which takes the gates as they are)
-        if constexpr (BWD) {
-            lv = GateLevels<float>(a);
-#pragma unroll
-            for (int lev = 0; lev < 5; ++lev) lv.grow((t >> lev) & 1, __shfl_xor(lv.full, 1 << lev));
-        }
-        if (l < 32) {
-            p.mat_gb[id * 64 + t] = lv.pre;
-            p.mat_gb[id * 64 + 32 + t] = lv.suf;
-        }
-    }
-
-    f32x4 aA[3], aP[3];                              // tiles (0,0), (1,0), (1,1)
-#pragma unroll
-    for (int t = 0; t < 3; ++t) aA[t] = aP[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    [[maybe_unused]] float diag[2] = {0.f, 0.f};
-    const uint32_t ks = (uint32_t)p.k.stride * ES, qs = (uint32_t)p.q.stride * ES, gs = (uint32_t)H * DK * 4;
-    const Window wk(static_cast<const char*>(p.k.p) + tok0 * ks, rem * ks), wq(static_cast<const char*>(p.q.p) + tok0 * qs, rem * qs);
-    const Window wg(reinterpret_cast<const char*>(p.gate) + tok0 * gs, KDA ? rem * gs : 0);
-    constexpr int RW = DT == SQ_DTYPE_F32 ? 2 : 1;   // 16-byte loads of 8 elements
-    struct Rows { Raw<DT, 8 / RW> k[2][RW], q[2][RW]; Raw<SQ_DTYPE_F32, 4> a[2][KDA ? 2 : 1]; };
-    auto fetch = [&](int kb) {                       // key rows 32 kb + 8 g .. + 7 of tokens 16 t + n
-        Rows r;
-        const int ch = 32 * kb + 8 * g;
-        auto at = [&](uint32_t off) { return DK < 32 && ch >= DK ? 0xfffffff0u : off; };   // beyond the rows: zeros
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-            for (int i = 0; i < RW; ++i) {
-                r.k[t][i].load(wk, at((16 * t + n) * ks + (hk * DK + ch + 4 * i) * ES));
-                r.q[t][i].load(wq, at((16 * t + n) * qs + (hk * DK + ch + 4 * i) * ES));
-            }
-            if constexpr (KDA) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) r.a[t][i].load(wg, at((16 * t + n) * gs + (h * DK + ch + 4 * i) * 4));
-            }
-        }
-        return r;
-    };
-    Rows next = fetch(0);
-#pragma unroll KDA ? 1 : NKB
-    for (int kb = 0; kb < NKB; ++kb) {
-        const Rows cur = next;
-        if (kb + 1 < NKB) next = fetch(kb + 1);
-        float kx[2][8], qx[2][8];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                kx[t][j] = RW == 2 ? cur.k[t][RW - 1 ? j >> 2 : 0].at(j & 3) : cur.k[t][0].at(j);
-                qx[t][j] = RW == 2 ? cur.q[t][RW - 1 ? j >> 2 : 0].at(j & 3) : cur.q[t][0].at(j);
-            }
-        if constexpr (!KDA) {
-            Frag<NPL> kf[2], qf[2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) { kf[t] = split8<NPL>(kx[t]); qf[t] = split8<NPL>(qx[t]); }
-            mma<2>(aA[0], kf[0], kf[0]); mma<2>(aP[0], qf[0], kf[0]);
-            mma<2>(aA[1], kf[1], kf[0]); mma<2>(aP[1], qf[1], kf[0]);
-            mma<2>(aA[2], kf[1], kf[1]); mma<2>(aP[2], qf[1], kf[1]);
-        } else {
-            // Pairs (i, j), j < i, by the highest bit in which i and j differ: with blocks of 2^lev tokens, i lies in an odd
-            // block and j in the even one before it, and Gamma_ij is (gates of i's block up to i) x (gates of j's block
-            // after j), both at most 1.  Five levels cover the triangle.  At a level a token is a row or a column, never
-            // both: one scaled and split k serves as either operand.
-            GateLevels<float> lv[2][8];
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    diag[t] = fmaf(qx[t][j], kx[t][j], diag[t]);
-                    const bool on = 16 * t + n < rem && (DK >= 32 || 32 * kb + 8 * g < DK);
-                    lv[t][j] = GateLevels<float>(on ? fmaxf(cur.a[t][KDA ? j >> 2 : 0].at(j & 3), gmin) : 1.f);
-                }
-#pragma unroll
-            for (int lev = 0; lev < 4; ++lev) {
-                const bool odd = (n >> lev) & 1;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    float ku[8], qu[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        ku[j] = kx[t][j] * pick(odd, lv[t][j].pre, lv[t][j].suf);
-                        qu[j] = qx[t][j] * lv[t][j].pre;
-                    }
-                    const Frag<3> fk = split8<3>(ku), fq = split8<3>(qu);
-                    f32x4 ta{0.f, 0.f, 0.f, 0.f}, tp{0.f, 0.f, 0.f, 0.f};
-                    mma<2>(ta, fk, fk);
-                    mma<2>(tp, fq, fk);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int i = 4 * g + r;
-                        const bool pair = ((i ^ n) >> lev) == 1 && i > n;
-                        aA[2 * t][r] += pair ? ta[r] : 0.f;
-                        aP[2 * t][r] += pair ? tp[r] : 0.f;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) lv[t][j].grow(odd, __shfl_xor(lv[t][j].full, 1 << lev));
-                }
-            }
-            float kr[8], qr[8], kc[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                kr[j] = kx[1][j] * lv[1][j].pre;
-                qr[j] = qx[1][j] * lv[1][j].pre;
-                kc[j] = kx[0][j] * lv[0][j].suf;
-            }
-            const Frag<3> fk = split8<3>(kr), fq = split8<3>(qr), fc = split8<3>(kc);
-            mma<2>(aA[1], fk, fc);
-            mma<2>(aP[1], fq, fc);
-        }
-    }
-    wave_sync();
-    float* ap = nullptr;
-    if constexpr (BWD && !KDA) ap = p.mat_ap + id * 2 * 32 * 32;
-    if constexpr (KDA) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            diag[t] += __shfl_xor(diag[t], 16);      // lane n: q_i . k_i of token 16 t + n
-            diag[t] += __shfl_xor(diag[t], 32);
-        }
-    }
-#pragma unroll
-    for (int tl = 0; tl < 3; ++tl) {
-        const int ti = tl > 0, tj = tl > 1;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * ti + 4 * g + r, j = 16 * tj + n;
-            float a = aA[tl][r], pv = aP[tl][r];
-            if constexpr (!KDA) {
-                const int lev = j < i ? 31 - __builtin_clz(i ^ j) : 0;
-                const float gm = s_gt[wave][0][lev][i] * s_gt[wave][1][lev][j];
-                a *= gm;
-                pv *= i == j ? 1.f : gm;
-            } else if (ti == tj) {
-                pv = i == j ? diag[ti] : pv;
-            }
-            a = j < i ? a : 0.f;
-            pv = j <= i ? pv : 0.f;
-            aP[tl][r] = pv;
-            M[0][i][j] = a * s_b[wave][j];
-            if constexpr (BWD) M[NM - 1][i][j] = a * s_b[wave][i];
-            if constexpr (BWD && !KDA) {
-                ap[i * 32 + j] = a;
-                ap[1024 + i * 32 + j] = pv;
-            }
-        }
-    }
-    wave_sync();
-    // (I + N) X = I by rows: lane c holds column c; lanes 0-31 take A diag(beta), lanes 32-63 diag(beta) A
-    const int which = BWD ? l >> 5 : 0, cl = l & 31;
-    float x[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        float s0 = i == cl ? 1.f : 0.f, s1 = 0.f;
-#pragma unroll
-        for (int jj = 0; jj < (i + 3) / 4; ++jj) {
-            const f32x4 row = *reinterpret_cast<const f32x4*>(&M[which][i][4 * jj]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (4 * jj + j < i) {
-                    if (j & 1) s1 = fmaf(-row[j], x[4 * jj + j], s1);
-                    else s0 = fmaf(-row[j], x[4 * jj + j], s0);
-                }
-        }
-        x[i] = s0 + s1;
-    }
-    wave_sync();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) M[which][i][cl] = x[i];         // without BWD both halves write the same values
-    wave_sync();
-    auto put = [&](uint16_t* mat, const float (&m)[32][kPrepLd], bool transposed, float scale0, float scale1) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {                // rows 16 t + n
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = 16 * (e >> 2) + 4 * g + (e & 3);
-                v[e] = transposed ? m[c][16 * t + n] : m[16 * t + n][c] * pick(t, scale1, scale0);
-            }
-            const Frag<3> f = split8<3>(v);
-#pragma unroll
-            for (int pl = 0; pl < 3; ++pl)
-                *reinterpret_cast<u32x4v*>(mat + ((t * 3 + pl) * 64 + l) * 8) = f.p[pl];
-        }
-    };
-    put(p.mat_f + id * (BWD ? 1 : 2) * kMatShorts, M[0], false, BWD ? 1.f : s_b[wave][n], BWD ? 1.f : s_b[wave][16 + n]);
-    if constexpr (BWD) put(p.mat_r + id * 2 * kMatShorts, M[NM - 1], true, 1.f, 1.f);
-    wave_sync();
-#pragma unroll
-    for (int tl = 0; tl < 3; ++tl)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) M[0][16 * (tl > 0) + 4 * g + r][16 * (tl > 1) + n] = aP[tl][r];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) M[0][4 * g + r][16 + n] = 0.f;   // the tile above the diagonal
-    wave_sync();
-    put(BWD ? p.mat_r + (id * 2 + 1) * kMatShorts : p.mat_f + (id * 2 + 1) * kMatShorts, M[0], BWD, 1.f, 1.f);
-}
 
 // ---------------------------------------------------------------- scan
 
@@ -829,16 +593,6 @@ __global__ void __launch_bounds__(scan_threads(DK, NC)) k_scan_both(const ScanPa
 
 // ---------------------------------------------------------------- launchers
 
-template <int DK, int DT, bool KDA>
-static hipError_t prep_t(const ScanParams& p, bool backward, hipStream_t s) {
-    const int64_t blocks = (p.n_slots * p.n_heads + kPrepWaves - 1) / kPrepWaves;
-    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), blk(kPrepWaves * 64);
-    if (backward) k_prep<DK, DT, KDA, true><<<grid, blk, 0, s>>>(p);
-    else k_prep<DK, DT, KDA, false><<<grid, blk, 0, s>>>(p);
-    return hipGetLastError();
-}
-
 template <int DK, int DT, bool KDA, int NC>
 static hipError_t scan_nc(const ScanParams& p, bool backward, hipStream_t s) {
     if (p.dv % (16 * NC) != 0) return hipErrorInvalidValue;
@@ -861,7 +615,6 @@ static hipError_t scan_t(const ScanParams& p, bool backward, hipStream_t s) {
     return scan_nc<DK, DT, KDA, DK < 32 ? 1 : 4>(p, backward, s);
 }
 
-hipError_t launch_scan_prep(const ScanParams& p, bool backward, hipStream_t s) { SQ_SCAN_DISPATCH(prep_t, p, backward, s); }
 hipError_t launch_scan(const ScanParams& p, bool backward, hipStream_t s) { SQ_SCAN_DISPATCH(scan_t, p, backward, s); }
 
 }  // namespace sq
