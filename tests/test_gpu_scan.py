@@ -137,17 +137,17 @@ SHORT = [(0, BF16, 4, 2, 128, 128), (0, F16, 2, 2, 128, 256), (0, F32, 3, 1, 64,
 @pytest.mark.parametrize("gate", ("usual", "strong"))
 @pytest.mark.parametrize("c", SHORT, ids=[f"{'kda' if c[0] else 'gdn'}-{str(c[1])[6:]}-{c[2]}h{c[3]}-{c[4]}x{c[5]}" for c in SHORT])
 def test_short_sequences(c, gate, dev):
-    """Few tokens a sequence, all lengths up to 10 and one of 40 among them: the sequences of up to 8 go token by token."""
+    """Few tokens a sequence, and one of 17 and one of 40 among them: the sequences of up to 16 go token by token."""
     form, dt, H, Hk, dk, dv = c
-    lens = [1, 0, 8, 2, 9, 3, 40, 4, 1, 5, 10, 6, 0, 7, 1, 1, 8, 2]
-    assert sum(lens) <= 8 * len(lens)
+    lens = [1, 0, 8, 2, 9, 3, 40, 4, 1, 5, 10, 6, 0, 7, 16, 17, 1, 2]
+    assert sum(lens) <= 12 * len(lens)
     x = scan_inputs(form, H, Hk, dk, dv, lens, 61, dt, gate)
     for s0 in (True, False):
         y, s1 = forward(form, x, lens, dev, s0)
         yr, sr = scan_ref(x, lens, s0)
         near(y, yr, "y")
         near(s1, sr, "s1")
-    for few in ([3], [0, 8], [1] * 5):               # no sequence can be longer: nothing else runs
+    for few in ([3], [0, 16], [1] * 5):              # no sequence can be longer: nothing else runs
         x = scan_inputs(form, H, Hk, dk, dv, few, 62, dt, gate)
         y, s1 = forward(form, x, few, dev)
         yr, sr = scan_ref(x, few)
@@ -158,10 +158,10 @@ def test_short_sequences(c, gate, dev):
 def test_short_sequences_in_wider_arrays_in_place_and_captured(dev):
     """Parts of wider arrays with NaN around them, tokens of no sequence, the states replaced in place; the captured call
     replayed gives what the eager calls give."""
-    form, H, Hk, dk, dv, lens, lead, tail = 1, 4, 2, 128, 128, [1, 5, 12, 0, 8], 2, 3
+    form, H, Hk, dk, dv, lens, lead, tail = 1, 4, 2, 128, 128, [1, 5, 20, 0, 8], 2, 3
     x = scan_inputs(form, H, Hk, dk, dv, lens, 63, BF16)
     T = sum(lens)
-    assert lead + T + tail <= 8 * len(lens)
+    assert lead + T + tail <= 12 * len(lens)
     nan = lambda *s, dt=BF16: torch.full(s, float("nan"), dtype=dt, device=dev)  # noqa: E731
     N, wide = lead + T + tail, nan(lead + T + tail, 2 * Hk * dk + H * dv + 8)
     q, k = (wide[:, i * Hk * dk:(i + 1) * Hk * dk].unflatten(1, (Hk, dk)) for i in (0, 1))
@@ -192,9 +192,10 @@ def test_short_sequences_in_wider_arrays_in_place_and_captured(dev):
         assert torch.equal(got[1], st) and torch.equal(got[0][lead:lead + T], y[lead:lead + T])
 
 
-def test_offsets_that_break_the_rules_stay_inside(dev):
+@pytest.mark.parametrize("N", (40, 16), ids=("chunks", "tokens"))
+def test_offsets_that_break_the_rules_stay_inside(N, dev):
     """Offsets below zero, beyond the arrays or decreasing: results are unspecified, the rows around the arrays stay."""
-    H, dk, dv, N = 2, 64, 64, 40
+    H, dk, dv = 2, 64, 64
     for at in ([-7, 50, 20], [30, 10, 400], [0, 2 ** 31 - 1, 5], [-2 ** 31, 0, 40]):
         pad = torch.full((N + 16, H * dv), 7.0, device=dev)
         y = pad[8:8 + N].view(N, H, dv)
