@@ -293,7 +293,7 @@ sq_status sq_valu_probe(int32_t waves_per_simd, int32_t n_blocks, float* d_out, 
  * Row arrays (sq_rows): element (token, head, j) at d_ptr[token * stride + head * d + j], so that q, k and
  * v may be parts of one wider array.  q, k: n_heads_k heads (a divisor of n_heads) of d_k elements; head h
  * reads q and k of head h / (n_heads / n_heads_k).  v, y: n_heads heads of d_v elements.  All four have the
- * element type cfg->dtype; gates, beta, states and the arithmetic are float32 (products on the bfloat16
+ * element type cfg->dtype; gates, beta, states and the arithmetic are float32 (the chunks' products on the bfloat16
  * matrix units with every float32 operand split into three parts; into two, 2^-16, in the last products of a y
  * of 16 bits), each output rounded once.
  * d_gate: alpha in [0, 1], [n_tokens][n_heads] (GDN) or [n_tokens][n_heads][d_k] (KDA); d_beta
@@ -305,7 +305,8 @@ sq_status sq_valu_probe(int32_t waves_per_simd, int32_t n_blocks, float* d_out, 
  * Workspace: sq_delta_scan_bytes bytes of device memory, the caller's, free again when the call's work on
  * `stream` is done; calls that may overlap (two streams, or two captured graphs whose replays overlap)
  * need one each.  No call allocates or synchronizes, so all of them can be captured.
- * The result does not depend on what else runs (no atomics; sums in a fixed order). */
+ * The result does not depend on what else runs (no atomics; sums in a fixed order).  Sequences of at most 16 tokens of a call
+ * with 12 or fewer a sequence go token by token, all others in chunks of 32; the two agree to float32 rounding. */
 typedef struct sq_rows {
     void* d_ptr;
     int64_t stride;               /* elements from one token (row) to the next */
