@@ -467,6 +467,51 @@ def test_captured_and_replayed(dev):
             assert torch.equal(u, w)
 
 
+@pytest.mark.parametrize("n,dk,form", ((65, 64, 1), (150, 64, 0), (4200, 16, 0)))
+def test_many_sequences(n, dk, form, dev):
+    """More sequences than a wave has lanes, empty ones and longer ones among them."""
+    lens = [int(i) for i in np.random.default_rng(n).choice([0, 1, 2, 20, 35], size=n, p=[0.3, 0.4, 0.25, 0.03, 0.02])]
+    lens[-1], lens[n // 2] = 33, 40
+    x = scan_inputs(form, 1, 1, dk, dk, lens, 97, F32)
+    y, s1 = forward(form, x, lens, dev)
+    yr, sr = scan_ref(x, lens)
+    near(y, yr, "y")
+    near(s1, sr, "s1")
+    g, r = backward(form, x, lens, dev), scan_grad_ref(x, lens)
+    for i in GRADS:
+        near(g[i], r[i], i)
+
+
+@pytest.mark.parametrize("sizes", ([[1, 3, 0, 20, 2], [16, 17, 1, 0, 5], [0, 0, 39, 0, 0], [8] * 5], [[70, 30, 1], [0, 101, 0], [33, 32, 36]]),
+                         ids=("short", "long"))
+def test_captured_then_other_lengths(sizes, dev):
+    """The offsets live on the device: a captured call replayed with other lengths takes those."""
+    form, H, Hk, dk, dv = 0, 4, 2, 128, 128
+    N, n = max(map(sum, sizes)), len(sizes[0])
+    x = scan_inputs(form, H, Hk, dk, dv, [N], 95, BF16)
+    d = {i: t.to(dev) for i, t in x.items()}
+    s0 = 0.3 * torch.randn(n, H, dk, dv, device=dev)
+    y, s1, at = torch.zeros_like(d["v"]), torch.zeros_like(s0), starts(sizes[0], dev)
+    work = torch.empty(sq.sq_delta_scan_bytes(form, BF16, H, Hk, dk, dv, n, N), dtype=torch.uint8, device=dev)
+    call = lambda: sq.sq_delta_scan(form, d["q"], d["k"], d["v"], d["gate"], d["beta"], y, seq_start=at, s0=s0, s1=s1,  # noqa: E731
+                                    workspace=work)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lens in sizes[1:] + sizes[:1]:
+        at.copy_(starts(lens, dev))
+        y.zero_(), s1.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        T = sum(lens)
+        yr, sr = scan_ref({**{i: t[:T] for i, t in x.items()}, "s0": s0.cpu()}, lens)
+        near(y[:T], yr, "y")
+        near(s1, sr, "s1")
+        assert not y[T:].any()
+
+
 def test_prompt_then_packed_decode(dev):
     """The whole path: unit-norm rows, scan of a prompt, sq_pack, decode steps, sq_unpack, scan again, gated norm."""
     H, dk, dv, T = 2, 64, 64, 75
