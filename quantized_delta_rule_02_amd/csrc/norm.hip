@@ -43,10 +43,12 @@ __device__ __forceinline__ Sum2 row_sum(Sum2 v, float* lds) {
 }
 
 // exp(-z) from the hardware's 2^x: the rounding of z log2(e) is put back as a factor, so that its error does not grow with |z|.
+// From a = 128 on 2^a is infinity, and infinity times a remainder of zero or below would be NaN; far below -126 it is zero,
+// and the remainder of an infinite a is NaN: there 2^a stays as it is.
 __device__ __forceinline__ float exp_neg(float z) {
     constexpr float l2e = 1.44269504089f, ln2 = 0.69314718056f;
     const float a = -z * l2e, lo = fmaf(-z, l2e, -a), e = __builtin_amdgcn_exp2f(a);
-    return fabsf(a) < 200.f ? fmaf(e, lo * ln2, e) : e;        // beyond: 0, infinity or NaN as they are
+    return a < 128.f && a > -200.f ? fmaf(e, lo * ln2, e) : e;
 }
 __device__ __forceinline__ void act_of(int act, float z, float& g, float& dg) {
     const float s = __builtin_amdgcn_rcpf(1.f + exp_neg(z));

@@ -238,3 +238,54 @@ def test_gradients_against_differences(dev):
         ana = (g.double() * (hi[i].double() - lo[i].double())).sum().item() / (2 * step)
         # float32 outputs: 2^-24 of each of 576 terms of the losses; the third derivative: step^2 of the gradient's size
         assert abs(num - ana) <= 2e-6 * do.norm().item() * y.norm().item() / step * 0.1 + 4 * step ** 2 * g.norm().item()
+
+
+def gate_values(t):
+    """Every value of a 16-bit type in [-300, 300]; for float32 a grid of steps of 2^-7, and of 2^-10 where exp(-z) leaves
+    float32's range (z from -140 to -86)."""
+    if t == F32:
+        z = torch.cat([torch.arange(-300, 300, 2.0 ** -7), torch.arange(-140, -86, 2.0 ** -10) + 1e-4])
+    else:
+        z = torch.arange(-(1 << 15), 1 << 15, dtype=torch.int32).to(torch.int16).view(t)
+        z = z[z.float().abs() <= 300]
+    z = z[:z.numel() // 128 * 128].clone()
+    z[:2] = torch.tensor([-90.5, -138.0])
+    return z.view(-1, 128)
+
+
+def gates(z, act):
+    """The gate and its derivative, in 64 bits."""
+    s, r = torch.sigmoid(z), torch.sigmoid(-z)
+    return (z * s, s * (1 + z * r)) if act == 0 else (s, s * r)
+
+
+@pytest.mark.parametrize("do", (F32, BF16, F16), ids=("float32", "bfloat16", "float16"))
+@pytest.mark.parametrize("act", (0, 1), ids=("silu", "sigmoid"))
+def test_gates_of_all_sizes(act, do, dev):
+    """Finite gates give finite results, near the formula's.  A sigmoid below float32's normal numbers may count as zero: 2^-126
+    of what it scales, |z| 2^-126 for z sigmoid(z).  Below 2^-126 bfloat16 has steps of 2^-133 (7 fraction bits) and float32 of
+    2^-149: rounding to them takes half a step, 2^-134 at most, however small the value (float16's 2^-25 is in `near`)."""
+    z = gate_values(do).to(dev)
+    y, d_o = rows(z.shape, F32, dev, 1), rows(z.shape, do, dev, 2)
+    w, c = 1 + 0.1 * rows((128,), F32, dev, 3), 1 + 0.1 * rows((128,), F32, dev, 4)
+    o, dy, dz = torch.empty_like(z), torch.empty_like(y), torch.empty_like(z)
+    dw, dc = torch.empty(128, device=dev), torch.empty(128, device=dev)
+    kw = dict(weight=w, z=z, act=act, chan_scale=c, eps=1e-6)
+    sq.sq_norm_out(y, o, **kw)
+    sq.sq_norm_out_bwd(y, d_o, dy, dz=dz, dweight=dw, dchan_scale=dc, **kw)
+    z64, y64 = z.double(), y.double()
+    g, dg = gates(z64, act)
+    low = 2.0 ** -126 / TOL * (1 + z64.abs())
+    yh, cw, gr = hat(y64, 0, 1e-6), c.double() * w.double(), d_o.double()
+    half = 2.0 ** -134 / TOL
+    near(o, cw * yh * g, "o", (cw * yh).abs() * (g.abs() + low) + half)
+    inv = yh.norm(dim=-1, keepdim=True) / y64.norm(dim=-1, keepdim=True)
+    dhat = gr * cw * g
+    part = inv * (gr * cw).abs() * (g.abs() + low)
+    near(dy, inv * (dhat - yh * (dhat * yh).mean(-1, keepdim=True)), "dy",
+         part + part.norm(dim=-1, keepdim=True) * y64.abs() / y64.norm(dim=-1, keepdim=True))
+    s = torch.sigmoid(z64)
+    near(dz, gr * cw * yh * dg, "dz", (gr * cw * yh).abs() * ((s * (1 + z64.abs() * (1 - s)) if act == 0 else s) + low) + half)
+    terms = (gr * yh).abs() * (g.abs() + low)
+    near(dw, (gr * c.double() * yh * g).sum(0), "dweight", (terms * c.double()).sum(0))
+    near(dc, (gr * w.double() * yh * g).sum(0), "dchan_scale", (terms * w.double()).sum(0))
