@@ -50,14 +50,17 @@ __device__ __forceinline__ float exp_neg(float z) {
     const float a = -z * l2e, lo = fmaf(-z, l2e, -a), e = __builtin_amdgcn_exp2f(a);
     return a < 128.f && a > -200.f ? fmaf(e, lo * ln2, e) : e;
 }
+// The reciprocal is the hardware's, off by at most one unit in the last place of float32 (2^-23 of the gate): an output in
+// float32 carries some five roundings of that size, one in 16 bits is rounded by 2^-11 or more.
 __device__ __forceinline__ void act_of(int act, float z, float& g, float& dg) {
-    const float s = __builtin_amdgcn_rcpf(1.f + exp_neg(z));
+    const float e = exp_neg(z), s = __builtin_amdgcn_rcpf(1.f + e);
     if (act == SQ_ACT_SILU) {
         g = z * s;
         dg = s * fmaf(z, 1.f - s, 1.f);
     } else {                                   // SQ_ACT_SIGMOID
+        // 1 - s = sigmoid(-z): the difference loses all its digits as s nears 1, e s loses none there
         g = s;
-        dg = s * (1.f - s);
+        dg = s * (z > 0.f ? e * s : 1.f - s);
     }
 }
 

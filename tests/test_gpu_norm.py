@@ -289,3 +289,18 @@ def test_gates_of_all_sizes(act, do, dev):
     terms = (gr * yh).abs() * (g.abs() + low)
     near(dw, (gr * c.double() * yh * g).sum(0), "dweight", (terms * c.double()).sum(0))
     near(dc, (gr * w.double() * yh * g).sum(0), "dchan_scale", (terms * w.double()).sum(0))
+
+
+@pytest.mark.parametrize("do", (F32, BF16, F16), ids=("float32", "bfloat16", "float16"))
+def test_sigmoid_gradient_of_open_gates(do, dev):
+    """The derivative s (1 - s) itself, not s, sizes the error of dz, however near s is to 1.  Roundings: 1 of 1 + e, 2 of the
+    reciprocal (its error is one unit), 2 of e, 1 of e s or 1 - s (which doubles what s carries: at most 4 of s <= 1/2), 1 of the
+    product, 5 of the other factors and some 8 of the row's norm, each 2^-24: below 24 * 2^-24 = 1.5e-6, TOL is 1e-5."""
+    z = gate_values(do).to(dev)
+    z = z[(z.float().abs() < 80).all(-1)]
+    y, d_o = rows(z.shape, F32, dev, 5), rows(z.shape, do, dev, 6)
+    dy, dz = torch.empty_like(y), torch.empty_like(z)
+    sq.sq_norm_out_bwd(y, d_o, dy, z=z, dz=dz, act=sq.SQ_ACT_SIGMOID)
+    scale = d_o.double() * hat(y.double(), 0, 1e-6)
+    assert z.max() > 50
+    near(dz, scale * torch.sigmoid(z.double()) * torch.sigmoid(-z.double()), "dz")
