@@ -153,14 +153,15 @@ __global__ void __launch_bounds__(kPrepWaves * 64, !SHORT ? 1 : DT == SQ_DTYPE_F
     if (ck.rem <= 0) return;                         // a slot that no chunk uses
     const int rem = ck.rem, H = p.n_heads, hk = h / (H / p.n_heads_k);
     const int64_t tok0 = ck.tok0;
-    constexpr float gmin = BWD ? kGateMin : 0.f;
+    // Forward, a gate counts as it is (NaN stays NaN); the matrices of the backward pass are those of gates of at least kGateMin.
+    auto counted = [](float a) { return BWD ? fmaxf(a, kGateMin) : a; };
 
     float(&M)[NM][32][kPrepLd] = s_m[wave];
     if (l < 32) s_b[wave][l] = l < rem ? p.beta[(tok0 + l) * H + h] : 0.f;
     if constexpr (!KDA) {
         const int t = l & 31;
         const float a = t < rem ? p.gate[(tok0 + t) * H + h] : 1.f;
-        GateLevels<float> lv(fmaxf(a, gmin));
+        GateLevels<float> lv(counted(a));
 #pragma unroll
         for (int lev = 0; lev < 5; ++lev) {
             if (l < 32) {
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kPrepWaves * 64, !SHORT ? 1 : DT == SQ_DTYPE_F
                 for (int j = 0; j < 8; ++j) {
                     diag[t] = fmaf(qx[t][j], kx[t][j], diag[t]);
                     const bool on = 16 * t + n < rem && (DK >= 32 || 32 * kb + 8 * g < DK);
-                    lv[t][j] = GateLevels<float>(on ? fmaxf(cur.a[t][KDA ? j >> 2 : 0].at(j & 3), gmin) : 1.f);
+                    lv[t][j] = GateLevels<float>(on ? counted(cur.a[t][KDA ? j >> 2 : 0].at(j & 3)) : 1.f);
                 }
 #pragma unroll
             for (int lev = 0; lev < 4; ++lev) {

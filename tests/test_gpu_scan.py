@@ -558,3 +558,25 @@ def test_block_experiment_runs(workload, dev, capsys):
     experiments.block(argparse.Namespace(workload=workload, prompt=40, batch=3, steps=2))
     got = json.loads(capsys.readouterr().out.strip().splitlines()[-1])
     assert got["experiment"] == "block" and got["requests"] == 3 and np.isfinite(got["output_rel_mean"])
+
+
+@pytest.mark.parametrize("lens", ([40, 70], [9, 3, 1]), ids=("chunks", "tokens"))
+@pytest.mark.parametrize("form", (0, 1), ids=("gdn", "kda"))
+def test_a_nan_gate_is_not_a_reset(form, lens, dev):
+    """One gate of NaN: its head's outputs from there to the sequence's end, its last state and the gradients that hold it are
+    NaN; the other heads' and sequences' are what they are without it."""
+    H, dk, dv, h = 3, 64, 64, 1
+    x = scan_inputs(form, H, H, dk, dv, lens, 83, BF16)
+    at = lens[0] - 5
+    bad = dict(x, gate=x["gate"].clone())
+    bad["gate"][(at, h, 7) if form else (at, h)] = float("nan")
+    y, s1 = forward(form, bad, lens, dev)
+    assert torch.isnan(y[at:lens[0], h]).all() and torch.isnan(s1[0, h]).all()
+    g = backward(form, bad, lens, dev)
+    assert torch.isnan(g["dq"][at:lens[0], h]).all() and torch.isnan(g["ds0"][0, h]).any()
+    ok, rest = forward(form, x, lens, dev), backward(form, x, lens, dev)
+    others = [i for i in range(H) if i != h]
+    for a, b in ((y, ok[0]), *((g[n], rest[n]) for n in GRADS if n != "ds0")):
+        assert torch.equal(a[:, others], b[:, others]) and torch.equal(a[lens[0]:], b[lens[0]:])
+    for a, b in ((s1, ok[1]), (g["ds0"], rest["ds0"])):
+        assert torch.equal(a[0, others], b[0, others]) and torch.equal(a[1:], b[1:])
