@@ -294,8 +294,7 @@ sq_status sq_valu_probe(int32_t waves_per_simd, int32_t n_blocks, float* d_out, 
  * v may be parts of one wider array.  q, k: n_heads_k heads (a divisor of n_heads) of d_k elements; head h
  * reads q and k of head h / (n_heads / n_heads_k).  v, y: n_heads heads of d_v elements.  All four have the
  * element type cfg->dtype; gates, beta, states and the arithmetic are float32 (the chunks' products on the bfloat16
- * matrix units with every float32 operand split into three parts; into two, 2^-16, in the last products of a y
- * of 16 bits), each output rounded once.
+ * matrix units with every float32 operand split into three parts), each output rounded once.
  * d_gate: alpha in [0, 1], [n_tokens][n_heads] (GDN) or [n_tokens][n_heads][d_k] (KDA); d_beta
  * [n_tokens][n_heads].  (The gradients of q, k and gate count gates below 1e-30 as 1e-30.)
  * Alignment: row arrays 16 bytes, with stride * element size a multiple of 16; d_gate (KDA) 16 bytes;

@@ -31,9 +31,8 @@ struct ScanLds {
     static constexpr bool REV = MODE == kScanRev, OUT = MODE == kScanOut;
     static constexpr bool VL = DT != SQ_DTYPE_F32;       // v through LDS (there is no room for it in float32)
     static constexpr int NP = KDA ? 3 : planes_of(DT);   // planes of the operands (gates make them float32)
-    // A result that is rounded to 16 bits at once (y) needs no third planes: two leave out up to 2^-16 of an operand where
-    // the rounding takes 2^-8 or 2^-11 of the result.  The states and what they are made of always take three.
-    static constexpr int YP = DT == SQ_DTYPE_F32 ? 3 : 2, NQ = NP < YP ? NP : YP;
+    // A y of 16 bits takes three planes too: what two leave out, 2^-16 of an operand, is above the rounding of a y that is small
+    // against its terms.
     static constexpr int LDK = (DK < 32 ? 32 : DK) + 8, LDT = 40, NMAT = MODE == kScanKeep ? 1 : 2;
     // The chunk's matrices go through LDS where the operands are one plane.  With three, LDS is what a step waits for most,
     // and the computing waves read them from memory, a step ahead (KDA prefill of 6150 tokens: 335 -> 315 us; a prefill of
@@ -41,7 +40,7 @@ struct ScanLds {
     static constexpr bool ML = NP < 3;
     struct First {
         uint16_t k[NP][32][LDK];                         // token-major: gamma K forward, (gamma_C / gamma) K in reverse
-        uint16_t q[OUT ? NQ : 1][OUT ? 32 : 1][LDK];
+        uint16_t q[OUT ? NP : 1][OUT ? 32 : 1][LDK];
         uint16_t m[ML ? NMAT : 1][ML ? kMatShorts : 8];  // That, P (forward); T^T, P^T (reverse)
         float pre[32], suf[32], beta[32];
     } first[2];
@@ -67,7 +66,7 @@ template <int DK, int DT, bool KDA, int MODE, int NC>
 struct Scan {
     using Lds = ScanLds<DK, DT, KDA, MODE, NC>;
     static constexpr bool REV = MODE == kScanRev, OUT = MODE == kScanOut, VL = Lds::VL;
-    static constexpr int NPL = planes_of(DT), NP = Lds::NP, YP = Lds::YP, NQ = Lds::NQ;
+    static constexpr int NPL = planes_of(DT), NP = Lds::NP;
     static constexpr int NT = DK / 16, NKB = (DK + 31) / 32, LDK = Lds::LDK, LDT = Lds::LDT, NMAT = Lds::NMAT;
     static constexpr bool ML = Lds::ML;
     static constexpr int NS = DK < 32 ? 1 : 4, NTHR = NS * 64, CH = 8 * DK / NTHR, ES = DT == SQ_DTYPE_F32 ? 4 : 2;
@@ -106,7 +105,7 @@ struct Scan {
                 const int j = i % (NP * 32 * LDK);
                 typename Lds::First& f = s.first[i / (NP * 32 * LDK)];
                 (&f.k[0][0][0])[j] = 0;
-                if (OUT && j < NQ * 32 * LDK) (&f.q[0][0][0])[j] = 0;
+                if (OUT) (&f.q[0][0][0])[j] = 0;
             }
             lds_barrier();
         }
@@ -257,20 +256,19 @@ __device__ __forceinline__ void Scan<DK, DT, KDA, MODE, NC>::stage(int tid) {
                 }
             }
             // token-major: forward gamma K (and gamma Q), reverse (gamma_C / gamma) K; key-major: the other way round
-            auto put_row = [&](auto& arr, auto planes, const float* x, int row) {   // CH adjacent key rows of a token
-                constexpr int N = decltype(planes)::value;
+            auto put_row = [&](auto& arr, const float* x, int row) {   // CH adjacent key rows of a token
                 if constexpr (CH == 4) {
-                    u32x2 w[N];
-                    split4<N>(x, w);
+                    u32x2 w[NP];
+                    split4<NP>(x, w);
 #pragma unroll
-                    for (int pl = 0; pl < N; ++pl) *reinterpret_cast<u32x2*>(&arr[pl][row][pc]) = w[pl];
+                    for (int pl = 0; pl < NP; ++pl) *reinterpret_cast<u32x2*>(&arr[pl][row][pc]) = w[pl];
                 } else {
                     float a = x[0], b2 = x[1];
 #pragma unroll
-                    for (int pl = 0; pl < N; ++pl) {
+                    for (int pl = 0; pl < NP; ++pl) {
                         const uint32_t w = round_pair(a, b2);
                         *reinterpret_cast<uint32_t*>(&arr[pl][row][pc]) = w;
-                        if (pl + 1 < N) rest_pair(w, a, b2);
+                        if (pl + 1 < NP) rest_pair(w, a, b2);
                     }
                 }
             };
@@ -285,8 +283,8 @@ __device__ __forceinline__ void Scan<DK, DT, KDA, MODE, NC>::stage(int tid) {
                     kt[i][j] = kv * (KDA ? pick(REV, pre[j][i], suf[j][i]) : 1.f);
                     if constexpr (MODE != kScanKeep) bq[i] = qt[i][j] = qx[j].at(i) * (KDA ? pre[j][i] : 1.f);
                 }
-                put_row(f.k, std::integral_constant<int, NP>{}, a, 4 * tq + j);
-                if constexpr (OUT) put_row(f.q, std::integral_constant<int, NQ>{}, bq, 4 * tq + j);
+                put_row(f.k, a, 4 * tq + j);
+                if constexpr (OUT) put_row(f.q, bq, 4 * tq + j);
             }
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -391,17 +389,14 @@ __device__ __forceinline__ void Scan<DK, DT, KDA, MODE, NC>::compute(int wave, i
 
     // The chunk's matrices, That and P (reverse: T^T and P^T): rows 16 t + n as A operands, or as B operands of the transposed
     // product; from LDS when they are used, or from memory a step before.
-    constexpr int MP = REV ? 3 : YP;
-    Frag<3> m0[2];
-    Frag<MP> m1[2];
-    auto load_mat = [&](auto& m, const uint16_t* from) {
-        constexpr int N = sizeof(m[0].p) / 16;
+    Frag<3> m0[2], m1[2];
+    auto load_mat = [&](Frag<3>(&m)[2], const uint16_t* from) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < N; ++i) m[t].p[i] = *reinterpret_cast<const u32x4v*>(from + (uint32_t)((t * 3 + i) * 512 + 8 * l));
+            for (int i = 0; i < 3; ++i) m[t].p[i] = *reinterpret_cast<const u32x4v*>(from + (uint32_t)((t * 3 + i) * 512 + 8 * l));
     };
-    auto next_mat = [&](auto& m, int which, int step) {
+    auto next_mat = [&](Frag<3>(&m)[2], int which, int step) {
         if constexpr (!ML) {
             if (step < nc) load_mat(m, (REV ? p.mat_r : p.mat_f) + (id(chunk(step)) * NMAT + which) * kMatShorts);
         }
@@ -444,7 +439,7 @@ __device__ __forceinline__ void Scan<DK, DT, KDA, MODE, NC>::compute(int wave, i
             for (int t = 0; t < 2; ++t) {
                 const int off = (16 * t + n) * LDK + 32 * kb + 8 * g;
                 mma<2>(z[t], lds_frag<NP>(&f.k[0][0][0], 32 * LDK, off), sf);
-                if constexpr (OUT) mma<YP - 1>(yq[t], sf, lds_frag<NQ>(&f.q[0][0][0], 32 * LDK, off));
+                if constexpr (OUT) mma<2>(yq[t], sf, lds_frag<NP>(&f.q[0][0][0], 32 * LDK, off));
             }
             if constexpr (!OUT) {
                 // the backward pass reads the states at the chunk borders: transposed by a product with the unit matrix
@@ -496,13 +491,13 @@ __device__ __forceinline__ void Scan<DK, DT, KDA, MODE, NC>::compute(int wave, i
             }
             if constexpr (OUT) {
                 if constexpr (ML) load_mat(m1, &f.m[ML ? 1 : 0][0]);
-                const Frag<YP> uf = split8<YP>(w);
+                const Frag<3> uf = split8<3>(w);
                 const uint32_t ys = (uint32_t)p.y.stride * ES;
                 const Window wy(static_cast<const char*>(p.y.p) + tok0 * ys, (uint32_t)rem * ys);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if constexpr (!KDA) yq[t] *= f.pre[16 * t + n];
-                    mma<YP - 1>(yq[t], uf, m1[t]);
+                    mma<2>(yq[t], uf, m1[t]);
                     store4(row_type, wy, (16 * t + n) * ys + (h * dv + c0 + 4 * g) * ES, yq[t]);
                 }
                 next_mat(m1, 1, ci + 1);

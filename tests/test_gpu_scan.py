@@ -5,9 +5,6 @@ out the terms below 2 * 2^-7 * 2^-15 = 2^-21 of |a||b|; float32 accumulation add
 through at most five such products within a chunk (state, That, P, update; one more for gradients), and the states hand
 errors on, damped by the gates: 5 * 2^-21 = 2.4e-6 of the operands' size, with a factor 4 for terms that cancel:
 1e-5 of an output's largest value.  An output in t adds half a step: torch.finfo(t).eps / 2 of its value.
-The last products of a 16-bit y take two parts, which leave out at most 2^-16 of an operand, of either sign: over the
-16 terms and more of a sum 2^-16 / sqrt(3) of its typical size, some 9e-6 of it, and an output's largest value is three
-and more times its typical one, so the same 1e-5 of the largest value holds them.
 """
 import numpy as np
 import pytest
@@ -580,3 +577,44 @@ def test_a_nan_gate_is_not_a_reset(form, lens, dev):
         assert torch.equal(a[:, others], b[:, others]) and torch.equal(a[lens[0]:], b[lens[0]:])
     for a, b in ((s1, ok[1]), (g["ds0"], rest["ds0"])):
         assert torch.equal(a[0, others], b[0, others]) and torch.equal(a[1:], b[1:])
+
+
+@pytest.mark.parametrize("H", (2, 130), ids=("few", "many"))
+@pytest.mark.parametrize("dk", (64, 128))
+@pytest.mark.parametrize("dt", (BF16, F16, F32), ids=("bfloat16", "float16", "float32"))
+@pytest.mark.parametrize("form", (0, 1), ids=("gdn", "kda"))
+def test_outputs_small_against_their_terms(form, dt, dk, H, dev):
+    """y = 2^-14 as the difference of two terms of 32 and more that are the same but for a last part of 2^-20: in the state, in
+    the updates, in the gates' products of a chunk and (a gate per key row) in those from the state.  A float32 holds each term
+    exactly (21 bits), so do three parts of 8 bits, and every partial sum is a multiple of 2^-14 below 2^9; two parts lose y."""
+    T, n = 64, 4
+    hi, lo, one = 0.5 + 2.0 ** -10 + 2.0 ** -20, 0.5 + 2.0 ** -10, 64.0
+    z = lambda *s: torch.zeros(*s, dtype=torch.float64)  # noqa: E731
+    q, k, v, beta, s0 = z(n * T, H, dk), z(n * T, H, dk), torch.full((n * T, H, dk), one), z(n * T, H), z(n, H, dk, dk)
+    gate = torch.ones(n * T, H, dk if form else 1, dtype=torch.float64)
+    t, even, odd = torch.arange(T), torch.arange(0, T, 2), torch.arange(1, T, 2)
+    # 0: the state holds both terms
+    q[t, :, 2 * t % dk], q[t, :, (2 * t + 1) % dk] = 1.0, -1.0
+    s0[0, :, 0::2], s0[0, :, 1::2] = one * hi, one * lo
+    # 1: a token's update against the one before it
+    for b in (1, 2):
+        k[b * T + t, :, t] = 1.0
+        q[b * T + odd, :, even], q[b * T + odd, :, odd] = 1.0, -1.0
+    beta[T + even], beta[T + odd] = hi, lo
+    # 2: the update before, times a gate, against the token's own
+    beta[2 * T + even], beta[2 * T + odd] = 1.0, lo
+    gate[2 * T + odd] = hi
+    # 3: the state times a gate per key row (a gate per head: the state itself), the first token of each chunk
+    q[3 * T::32, :, 0::2], q[3 * T::32, :, 1::2] = 2.0 / dk, -2.0 / dk
+    if form:
+        gate[3 * T, :, 0::2] = hi
+        s0[3, :, 0::2], s0[3, :, 1::2] = one, one * lo
+    else:
+        s0[3, :, 0::2], s0[3, :, 1::2] = one * hi, one * lo
+    x = {"q": q.to(dt), "k": k.to(dt), "v": v.to(dt), "gate": (gate if form else gate[..., 0]).float(), "beta": beta.float(), "s0": s0.float()}
+    y, s1 = forward(form, x, [T] * n, dev)
+    yr, sr = scan_ref(x, [T] * n)
+    assert (yr[T + odd] == 2.0 ** -14).all() and (yr[2 * T + odd] == 2.0 ** -14).all() and (yr[:T] == 2.0 ** -14).all()
+    assert (yr[3 * T::32] == 2.0 ** -14).all() and not yr[T + even].any()
+    near(y, yr, "y")
+    near(s1, sr, "s1")
