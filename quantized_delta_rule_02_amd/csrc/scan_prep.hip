@@ -36,10 +36,17 @@ __device__ __forceinline__ void short_sequences(const ScanParams& p, unsigned bl
 
     // all addresses are one wave's base, a lane's 32-bit offset and a row's: none takes registers of its own
     const uint32_t at = (uint32_t)(kl * R * dv + col) * 4, bytes = (uint32_t)(DK * dv) * 4;
-    const Window w0(p.s0 + st * DK * dv, p.s0 ? bytes : 0);      // no first states: zeros
     f32x4 S[R];
+    if (p.s0) {
+        const Window w0(p.s0 + st * DK * dv, bytes);
 #pragma unroll
-    for (int j = 0; j < R; ++j) S[j] = __builtin_bit_cast(f32x4, (u32x4v)__builtin_amdgcn_raw_buffer_load_b128(w0.r, at, j * dv * 4, 0));
+        for (int j = 0; j < R; ++j) S[j] = __builtin_bit_cast(f32x4, (u32x4v)__builtin_amdgcn_raw_buffer_load_b128(w0.r, at, j * dv * 4, 0));
+    } else {
+        // not a window of no bytes: whether an offset is beyond it is decided by the lane's offset against its size less the
+        // row's, which would be below zero here
+#pragma unroll
+        for (int j = 0; j < R; ++j) S[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 
     using Words = std::conditional_t<ES == 4, u32x4v, u32x2>;       // four elements
     struct Token {                                   // as loaded
