@@ -77,9 +77,14 @@ int64_t scan_launch_threads(const sq_scan_cfg& c, bool backward) {
     return int64_t(c.n_seq) * c.n_heads * c.d_v * per_col * (backward ? 2 : 1);
 }
 
-// Sequences of at most 16 tokens go token by token where the mean is at most 12 (the lengths themselves are the device's).
-// 64 ragged sequences x 32 heads, bfloat16, one gate per head, both launches of each way: mean 4 tokens 65 us against 96
-// in chunks, 8: 76 / 99, 10: 82 / 99, 12: 95 / 99, 16: 102 / 100.  One token of 32 heads: 5 us against 14.
+// Sequences of at most 16 tokens go token by token where the mean is at most 12 (the lengths themselves are the device's) and
+// d_k is 64 or more.  Microseconds on the GPU, this way / in chunks, ragged sequences x 32 heads, at means of 1, 4, 8, 12, 16:
+//   one gate per head, bfloat16, 128 x 128:  64:  47/87 55/89 74/91 88/92 94/96     8:  7/20 15/20 19/20 29/21 30/21
+//   one gate per head, float32, 128 x 128:   64:  48/102 61/105 82/107 102/110 113/110    8:  7/23 15/22 20/24 30/24 32/24
+//   a gate per key row, bfloat16, 128 x 128: 64:  48/130 62/144 92/146 116/153 123/147    8:  7/34 14/34 21/34 34/35 39/35
+//   a gate per key row, float32, 128 x 256:  64:  109/213 123/230 174/231 208/242 221/236 8:  13/47 22/47 28/47 41/48 38/48
+// 256 sequences and 64 x 64 states are alike, and so is one token of 32 heads: 5 against 13 to 29.  It loses where a few
+// sequences with one gate per head have means of 9 to 12 (the chain of one sequence's tokens, 29 against 21).
 constexpr int kShortLen = 16, kShortMean = 12;
 bool takes_short(const sq_scan_cfg& c) { return c.d_k >= 64 && c.n_tokens <= int64_t(kShortMean) * c.n_seq; }
 
