@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 8 && K == 1 ? 4 : 1) k_norm
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    if constexpr (OP == kNormIn) a[u][k][j] = fmaf(c[k][j], t[u][k][j], a[u][k][j]);
+                    if constexpr (OP == kNormIn) a[u][k][j] = has_t ? fmaf(c[k][j], t[u][k][j], a[u][k][j]) : a[u][k][j];
                     s[u].a = fmaf(a[u][k][j], a[u][k][j], s[u].a);
                     if constexpr (OP == kNormInBwd) s[u].b = fmaf(g[u][k][j] * w[k][j], a[u][k][j], s[u].b);
                     if constexpr (OP == kNormOutBwd) s[u].b = fmaf(g[u][k][j] * c[k][j] * w[k][j] * t[u][k][j], a[u][k][j], s[u].b);

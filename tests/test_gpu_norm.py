@@ -304,3 +304,15 @@ def test_sigmoid_gradient_of_open_gates(do, dev):
     scale = d_o.double() * hat(y.double(), 0, 1e-6)
     assert z.max() > 50
     near(dz, scale * torch.sigmoid(z.double()) * torch.sigmoid(-z.double()), "dz")
+
+
+@pytest.mark.parametrize("d", (128, 37))
+def test_without_a_residual_its_scale_counts_for_nothing(d, dev):
+    """No r: h = x, whatever chan_scale holds."""
+    x, n, want = rows((9, d), BF16, dev, 1), torch.empty(9, d, device=dev), torch.empty(9, d, device=dev)
+    h = torch.empty_like(x)
+    c = torch.ones(d, device=dev)
+    c[::3], c[1::3] = float("inf"), float("nan")
+    sq.sq_norm_in(x, want)
+    sq.sq_norm_in(x, n, h=h, chan_scale=c)
+    assert torch.equal(n, want) and torch.equal(h, x)
