@@ -304,8 +304,13 @@ sq_status sq_valu_probe(int32_t waves_per_simd, int32_t n_blocks, float* d_out, 
  * Workspace: sq_delta_scan_bytes bytes of device memory, the caller's, free again when the call's work on
  * `stream` is done; calls that may overlap (two streams, or two captured graphs whose replays overlap)
  * need one each.  No call allocates or synchronizes, so all of them can be captured.
- * The result does not depend on what else runs (no atomics; sums in a fixed order).  Sequences of at most 16 tokens of a call
- * with 12 or fewer a sequence go token by token, all others in chunks of 32; the two agree to float32 rounding. */
+ * The result does not depend on what else runs (no atomics; sums in a fixed order).  sq_delta_scan takes the sequences of at
+ * most 16 tokens of a call with 12 or fewer a sequence token by token if d_k is 64 or more; all others, and everything in
+ * sq_delta_scan_bwd, go in chunks of 32 tokens from a sequence's start.  The two ways agree to float32 rounding for finite
+ * values.  A result that the formula makes NaN or infinite (from an input or a state, or a value above 3.38e38 on the way)
+ * is not finite here either, but in chunks it may be NaN where the formula keeps an infinity, and the same head's results of
+ * the other tokens of its chunk, those before it among them, may be NaN too.  Chunks before it in sq_delta_scan, other heads
+ * and other sequences keep their results. */
 typedef struct sq_rows {
     void* d_ptr;
     int64_t stride;               /* elements from one token (row) to the next */

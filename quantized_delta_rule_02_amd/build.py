@@ -36,7 +36,8 @@ def build(verbose: bool = False) -> str:
     # v_max/v_min instead of being preceded by canonicalizing copies of their operands
     device = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
     step = ["-munsafe-fp-atomics", "-mno-amdgpu-ieee", "-fno-honor-nans"]
-    # the norms and the scan let NaN and infinities through
+    # the norms and the scan take NaN and infinities as inputs like others (the norms give what their formulas give, the scan
+    # what include/stepq.h says), so they are compiled without the assumption that there are none
     ieee = {"norm.hip", "scan.hip", "scan_prep.hip", "scan_bwd.hip"}
 
     def compile_one(src: str) -> str:

@@ -1,10 +1,12 @@
 """The gated delta scan and its gradients on the GPU against float64 references, token by token.
 
-Tolerance.  Products split every float32 operand exactly into three bfloat16 parts (8 bits each, truncated) and leave
-out the terms below 2 * 2^-7 * 2^-15 = 2^-21 of |a||b|; float32 accumulation adds some 2^-24 per term.  A result passes
-through at most five such products within a chunk (state, That, P, update; one more for gradients), and the states hand
-errors on, damped by the gates: 5 * 2^-21 = 2.4e-6 of the operands' size, with a factor 4 for terms that cancel:
-1e-5 of an output's largest value.  An output in t adds half a step: torch.finfo(t).eps / 2 of its value.
+Tolerance.  Products split every float32 operand exactly into three bfloat16 parts (8 bits each, rounded to nearest: what one
+leaves is at most 2^-8 of the value, what two leave 2^-16) and leave out two terms of at most 2^-8 * 2^-16 = 2^-24 of |a||b|;
+float32 accumulation adds some 2^-24 per term, over at most 24 products of matrix instructions a result.  TOL holds an output's
+largest error against its largest value: a result passes through at most five such products within a chunk (state, That, P,
+update; one more for gradients), 5 * 26 * 2^-24 = 7.7e-6 of the terms if all roundings agree.  L2 and L2_GRAD hold the relative error of a
+whole array, where roundings add up in quadrature: see test_every_part_counts.  An output in t adds half a step:
+torch.finfo(t).eps / 2 of its value.
 """
 import numpy as np
 import pytest
@@ -618,3 +620,49 @@ def test_outputs_small_against_their_terms(form, dt, dk, H, dev):
     assert (yr[3 * T::32] == 2.0 ** -14).all() and not yr[T + even].any()
     near(y, yr, "y")
     near(s1, sr, "s1")
+
+
+L2, L2_GRAD = 1e-6, 1.5e-6
+
+
+@pytest.mark.parametrize("c", CASES, ids=IDS)
+def test_every_part_counts(c, dev):
+    """The relative L2 error of the float32 outputs.  A rounding to float32 is off by 2^-24 / sqrt(3) = 3.4e-8 of a partial sum,
+    24 of them (six products of parts for each 32 of 128 key rows) in quadrature by 1.7e-7; the terms left out, 2^-24 at most, are
+    some 2^-27 in the mean square.  Outputs and states pass through five products (3.7e-7), gradients through twelve (5.9e-7); states hand errors on, damped by the gates;
+    terms that cancel, a factor of 2, and for gradients 2.5: 1e-6 and 1.5e-6.  One product of parts lost (say the first with the
+    third of two operands) makes 2.6e-6 to 4e-6 of y and the states, which 1e-5 of the largest value does not show."""
+    form, dt, H, Hk, dk, dv, lens, gate = c
+    x = scan_inputs(form, H, Hk, dk, dv, lens, 29, dt, gate)
+    y, s1 = forward(form, x, lens, dev)
+    yr, sr = scan_ref(x, lens)
+    g, r = backward(form, x, lens, dev), scan_grad_ref(x, lens)
+    off = {}
+    for n, a, b in [("y", y, yr), ("s1", s1, sr)] + [(n, g[n], r[n]) for n in GRADS]:
+        if a.dtype == F32:
+            off[n] = ((a.double().cpu() - b).norm() / b.norm()).item(), L2 if n in ("y", "s1") else L2_GRAD
+    say({n: f"{e:.2e}" for n, (e, _) in off.items()})
+    for n, (e, tol) in off.items():
+        assert e <= tol, (n, e)
+
+
+@pytest.mark.parametrize("value", (float("nan"), float("inf")), ids=("nan", "inf"))
+@pytest.mark.parametrize("what", ("q", "k", "v", "beta", "s0"))
+@pytest.mark.parametrize("lens", ([90, 40], [16, 3, 1]), ids=("chunks", "tokens"))
+@pytest.mark.parametrize("form", (0, 1), ids=("gdn", "kda"))
+def test_a_value_that_is_not_finite_stays_in_its_head(form, lens, what, value, dev):
+    """What it reaches is not finite; chunks before it, other heads and sequences keep their bits."""
+    H, dk, dv, h = 3, 64, 64, 1
+    x = scan_inputs(form, H, H, dk, dv, lens, 84, F32)
+    at = 0 if what == "s0" else lens[0] - 10
+    bad = dict(x, **{what: x[what].clone()})
+    bad[what][{"q": (at, h, 3), "k": (at, h, 3), "v": (at, h), "beta": (at, h), "s0": (0, h)}[what]] = value
+    y, s1 = forward(form, bad, lens, dev)
+    oy, os_ = forward(form, x, lens, dev)
+    end = at + 1 if what == "q" else lens[0]
+    assert not torch.isfinite(y[at:end, h]).any()
+    assert torch.isfinite(s1[0, h]).any() == (what == "q")
+    others, before = [i for i in range(H) if i != h], at // 32 * 32
+    assert torch.equal(y[:, others], oy[:, others]) and torch.equal(s1[:, others], os_[:, others])
+    assert torch.equal(y[lens[0]:], oy[lens[0]:]) and torch.equal(s1[1:], os_[1:])
+    assert torch.equal(y[:before], oy[:before])
