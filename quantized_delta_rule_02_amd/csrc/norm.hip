@@ -9,7 +9,8 @@
 // All four are bound by memory: every row is read once into registers (both sums of a backward pass
 // are taken from there) and written once.  A row of d elements belongs to TPR threads with K vectors of
 // V elements each, so that one workgroup of 256 threads holds 256 / TPR rows: head rows (d <= 512 with 16-byte
-// accesses) live in part of a wave and need no LDS, longer ones take the whole workgroup.
+// accesses) live in part of a wave and need no LDS, longer ones take the whole workgroup.  Rows above 2048 elements that cannot
+// be read 16 bytes at a time take 1024 threads, the widest of them a kernel that reads them twice (k_norm_wide).
 // dweight and dchan_scale are sums over all rows: each thread keeps its columns' sums in registers over the
 // workgroup's rows, the workgroup adds its row groups in LDS and writes one partial row, and a second
 // kernel adds the partial rows in a fixed order (no atomics, so results do not depend on the schedule).
@@ -19,6 +20,8 @@
 #include "vec.h"
 
 namespace sq {
+
+constexpr int norm_threads(int tpr) { return tpr > kNormThreads ? tpr : kNormThreads; }    // of a workgroup
 
 struct Sum2 { float a, b; };
 
@@ -36,8 +39,9 @@ __device__ __forceinline__ Sum2 row_sum(Sum2 v, float* lds) {
         __syncthreads();                       // the previous row's sums have been read
         if ((threadIdx.x & 63) == 0) { lds[2 * wave] = v.a; lds[2 * wave + 1] = v.b; }
         __syncthreads();
-        v.a = lds[0] + lds[2] + lds[4] + lds[6];
-        v.b = lds[1] + lds[3] + lds[5] + lds[7];
+        v = Sum2{0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) { v.a += lds[2 * w]; v.b += lds[2 * w + 1]; }
     }
     return v;
 }
@@ -107,13 +111,13 @@ struct RawV {
 // U rows at a time: their loads are in flight together.
 // EXTRA (gradients of the first norm): dh or r is there.
 template <int OP, int V, int TPR, int K, int U, bool EXTRA>
-__global__ void __launch_bounds__(kNormThreads, V == 8 && K == 1 ? 4 : 1) k_norm(const NormParams p) {
-    constexpr int RPB = kNormThreads / TPR;
+__global__ void __launch_bounds__(norm_threads(TPR), V == 8 && K == 1 ? 4 : 1) k_norm(const NormParams p) {
+    constexpr int NT = norm_threads(TPR), RPB = NT / TPR;
     constexpr bool kBwd = OP == kNormInBwd || OP == kNormOutBwd;
     constexpr bool kIn = OP == kNormIn || OP == kNormInBwd;
     constexpr bool kAll = K <= 2;              // few enough registers to load every array at once
-    __shared__ float s_red[8];
-    __shared__ float s_col[kBwd && RPB > 1 ? kNormThreads * V * K : 1];
+    __shared__ float s_red[2 * NT / 64];
+    __shared__ float s_col[kBwd && RPB > 1 ? NT * V * K : 1];
     const int lane = (int)threadIdx.x % TPR, sub = (int)threadIdx.x / TPR;
     const int d = p.d;
     // first: the row the norm is of, its addend or gate, the incoming gradient; second: what only the result needs
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 8 && K == 1 ? 4 : 1) k_norm
             }
             float* out = p.part + ((size_t)which * p.n_blocks + blockIdx.x) * d;
             if constexpr (RPB > 1) {
-                for (int i = (int)threadIdx.x; i < d; i += kNormThreads) {
+                for (int i = (int)threadIdx.x; i < d; i += NT) {
                     float t = 0.f;
                     for (int r = 0; r < RPB; ++r) t += s_col[r * (TPR * V * K) + i];
                     out[i] = t;
@@ -312,6 +316,132 @@ __global__ void __launch_bounds__(kNormThreads, V == 8 && K == 1 ? 4 : 1) k_norm
                         for (int j = 0; j < V; ++j) out[col[k] + j] = v[k][j];
                     }
             }
+        }
+    }
+}
+
+// Rows above 4096 elements that are read one at a time: 1024 threads take a row in groups of four elements each, once for its
+// sums and once more for its results (from the caches: a row is 64 KiB at most), so that no array of a row is held and only the
+// column sums stay in registers.
+constexpr int kWideThreads = 1024;
+template <int OP>
+__global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormParams p) {
+    constexpr int NT = kWideThreads, G = 4, NK = kNormMaxD / NT;
+    constexpr bool kBwd = OP == kNormInBwd || OP == kNormOutBwd;
+    constexpr bool kIn = OP == kNormIn || OP == kNormInBwd;
+    __shared__ float s_red[2 * NT / 64];
+    const int lane = (int)threadIdx.x, d = p.d;
+    const NormRows& ra = OP == kNormIn ? p.x : OP == kNormInBwd ? p.h : p.y;
+    const NormRows& rt = OP == kNormIn ? p.r : p.z;
+    const NormRows& rg = OP == kNormInBwd ? p.dn : p.d_o;
+    const NormRows& re = OP == kNormInBwd ? p.dh : p.x;
+    const bool has_t = OP == kNormIn ? p.has_r : kIn ? false : p.has_z;
+    const bool has_e = OP == kNormInBwd ? p.has_dh : OP == kNormOut ? p.has_x : false;
+    const int dt_t = OP == kNormIn ? p.dtype : p.dtype_out, dt_e = OP == kNormInBwd ? p.dtype : p.dtype_out;
+    float sw[kBwd ? NK : 1], sc[kBwd ? NK : 1];
+#pragma unroll
+    for (int k = 0; k < (kBwd ? NK : 1); ++k) sw[k] = sc[k] = 0.f;
+    for (int64_t row = blockIdx.x; row < p.n_rows; row += gridDim.x) {
+        const uint32_t outer = (uint32_t)row / (uint32_t)p.n_inner, inner = (uint32_t)row % (uint32_t)p.n_inner;
+        RawV<1> xa[G], xt[G], xg[G], xe[G], xr[G];
+        float w[G], c[G];
+        auto col = [&](int k, int u) { return (k + u) * NT + lane; };
+        auto load = [&](const NormRows& r, int dt, RawV<1>& x, int i) { x.load(r, dt, row_at(r, outer, inner, d) + i); };
+        auto fetch = [&](int k) {
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                const int i = col(k, u);
+                if (i >= d) continue;
+                load(ra, p.dtype, xa[u], i);
+                if (has_t) load(rt, dt_t, xt[u], i);
+                if constexpr (kBwd) load(rg, p.dtype_out, xg[u], i);
+                w[u] = p.weight ? p.weight[i] : 1.f;
+                c[u] = p.chan_scale ? p.chan_scale[i] * p.res_scale : p.res_scale;
+            }
+        };
+        // the row's element (norm_in: h), the gate and its derivative, the incoming gradient
+        auto element = [&](int u, float& a, float& t, float& q, float& g) {
+            xa[u].get(p.dtype, &a);
+            t = 1.f;
+            q = g = 0.f;
+            if (has_t) {
+                xt[u].get(dt_t, &t);
+                if constexpr (kIn) a = fmaf(c[u], t, a);
+                else act_of(p.act, t, t, q);
+            }
+            if constexpr (kBwd) xg[u].get(p.dtype_out, &g);
+        };
+        Sum2 s{0.f, 0.f};
+#pragma unroll 1
+        for (int k = 0; k * NT < d; k += G) {
+            fetch(k);
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                if (col(k, u) >= d) continue;
+                float a, t, q, g;
+                element(u, a, t, q, g);
+                s.a = fmaf(a, a, s.a);
+                if constexpr (OP == kNormInBwd) s.b = fmaf(g * w[u], a, s.b);
+                if constexpr (OP == kNormOutBwd) s.b = fmaf(g * c[u] * w[u] * t, a, s.b);
+            }
+        }
+        s = row_sum<NT>(s, s_red);
+        const float inv = 1.f / sqrtf(fmaf(s.a, p.inv_div, p.eps));
+        const float back = s.b * (OP == kNormInBwd ? p.out_scale : 1.f) * inv * inv * p.inv_div;
+#pragma unroll(kBwd ? NK / G : 1)
+        for (int k = 0; k < NK; k += G) {
+            if (k * NT < d) {
+                fetch(k);
+#pragma unroll
+                for (int u = 0; u < G; ++u) {
+                    if (col(k, u) >= d) continue;
+                    if (has_e) load(re, dt_e, xe[u], col(k, u));
+                    if constexpr (OP == kNormInBwd) {
+                        if (p.has_r) load(p.r, p.dtype, xr[u], col(k, u));
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < G; ++u) {
+                    const int i = col(k, u), n = kBwd ? k + u : 0;
+                    if (i >= d) continue;
+                    float a, t, q, g, e = 0.f, r = 0.f;
+                    element(u, a, t, q, g);
+                    if (has_e) xe[u].get(dt_e, &e);
+                    if constexpr (OP == kNormInBwd) {
+                        if (p.has_r) xr[u].get(p.dtype, &r);
+                    }
+                    auto put = [&](const NormRows& to, int dt, float v) { store1(to.p, dt, row_at(to, outer, inner, d) + i, v); };
+                    if constexpr (OP == kNormIn) {
+                        if (p.write_h) put(p.h, p.dtype, a);
+                        put(p.n, p.dtype_out, a * (inv * p.out_scale) * w[u]);
+                    } else if constexpr (OP == kNormInBwd) {
+                        const float gf = g * p.out_scale, o = fmaf(inv, gf * w[u] - a * back, e);
+                        sw[n] = fmaf(gf * inv, a, sw[n]);
+                        sc[n] = fmaf(o * p.res_scale, r, sc[n]);
+                        if (p.write_dr) put(p.dr, p.dtype, o * c[u]);
+                        put(p.dx, p.dtype, o);
+                    } else if constexpr (OP == kNormOut) {
+                        put(p.o, p.dtype_out, fmaf(a * inv * w[u] * t, c[u], e));
+                    } else {
+                        const float yh = a * inv, gc = g * c[u];
+                        sw[n] = fmaf(gc * t, yh, sw[n]);
+                        sc[n] = fmaf(g * p.res_scale * t, w[u] * yh, sc[n]);
+                        if (p.write_dz) put(p.dz, p.dtype_out, gc * w[u] * yh * q);
+                        put(p.dy, p.dtype, inv * (gc * w[u] * t - a * back));
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);           // one group's loads at a time
+        }
+    }
+    if constexpr (kBwd) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            if (!(which ? p.dchan_scale : p.dweight)) continue;
+            float* out = p.part + ((size_t)which * p.n_blocks + blockIdx.x) * d;
+#pragma unroll
+            for (int k = 0; k < NK; ++k)
+                if (k * NT + lane < d) out[k * NT + lane] = which ? sc[k] : sw[k];
         }
     }
 }
@@ -341,9 +471,10 @@ __global__ void __launch_bounds__(16 * kSumGroups) k_norm_sum(const NormParams p
     if (g == 0 && col < p.d) out[col] = s[0][ci] + s[1][ci] + s[2][ci] + s[3][ci];
 }
 
+// K = 0: k_norm_wide.
 template <int OP, int V, int TPR, int K>
 static hipError_t launch_t(const NormParams& p0, hipStream_t s) {
-    constexpr int RPB = kNormThreads / TPR;
+    constexpr int RPB = norm_threads(TPR) / TPR;
     constexpr int U = V == 8 && K == 1 && TPR < 256 && OP == kNormIn ? 2 : 1;
     constexpr bool kBwd = OP == kNormInBwd || OP == kNormOutBwd;
     NormParams p = p0;
@@ -355,10 +486,11 @@ static hipError_t launch_t(const NormParams& p0, hipStream_t s) {
         blocks = 8192;                         // the weights are loaded once per workgroup and kept over its rows
     }
     p.n_blocks = (int32_t)blocks;
-    const dim3 grid((unsigned)blocks), blk(kNormThreads);
+    const dim3 grid((unsigned)blocks), blk(norm_threads(TPR));
     if (blocks > 0) {
         constexpr bool kChoice = OP == kNormInBwd;
-        if (kChoice && !p.has_dh && !p.has_r) k_norm<OP, V, TPR, K, U, !kChoice><<<grid, blk, 0, s>>>(p);
+        if constexpr (K == 0) k_norm_wide<OP><<<grid, blk, 0, s>>>(p);
+        else if (kChoice && !p.has_dh && !p.has_r) k_norm<OP, V, TPR, K, U, !kChoice><<<grid, blk, 0, s>>>(p);
         else k_norm<OP, V, TPR, K, U, true><<<grid, blk, 0, s>>>(p);
     }
     hipError_t e = hipGetLastError();
@@ -386,7 +518,19 @@ static hipError_t launch_op(bool vec, const NormParams& p, hipStream_t s) {
     if (d <= 64) return launch_t<OP, 1, 64, 1>(p, s);
     if (d <= 256) return launch_t<OP, 1, 64, 4>(p, s);
     if (d <= 2048) return launch_t<OP, 1, 256, 8>(p, s);
-    return launch_t<OP, 1, 256, 64>(p, s);
+    // Wider rows take 1024 threads, with at most 8 elements of every array in a thread's registers (the gradients of the second
+    // norm: 4), or k_norm_wide.  With 256 threads of 64 elements they spilled up to 5549 registers.  bfloat16, 16 million
+    // elements, no 16-byte accesses, us now / with 256 threads / plain torch:
+    //   first norm, residual: 2049: 76 / 504 / 215   4095: 56 / 327 / 216   8191: 66 / 220 / 216   16383: 73 / 344 / 212
+    //   its gradients:        2049: 136 / 1256 / 844  4095: 105 / 1017 / 769  8191: 94 / 976 / 732  16383: 226 / 948 / 724
+    //   second norm:          2049: 76 / 568 / 370   4095: 59 / 392 / 371   8191: 74 / 292 / 368   16383: 99 / 376 / 367
+    //   its gradients:        2049: 128 / 2501 / 1325  4095: 98 / 1823 / 1254  8191: 211 / 1453 / 1211  16383: 207 / 1658 / 1202
+    // k_norm_wide from 4097 elements on: 92, 249, 126, 234 us at 4097, where 8 held elements take 86, 118, 95 and (spilled) 367.
+    if (d <= 4096) return launch_t<OP, 1, 1024, 4>(p, s);
+    if constexpr (OP != kNormOutBwd) {
+        if (d <= 8192) return launch_t<OP, 1, 1024, 8>(p, s);
+    }
+    return launch_t<OP, 1, kWideThreads, 0>(p, s);
 }
 
 hipError_t launch_norm(int op, bool vec, const NormParams& p, hipStream_t s) {

@@ -316,3 +316,59 @@ def test_without_a_residual_its_scale_counts_for_nothing(d, dev):
     sq.sq_norm_in(x, want)
     sq.sq_norm_in(x, n, h=h, chan_scale=c)
     assert torch.equal(n, want) and torch.equal(h, x)
+
+
+# rows that are not read 16 bytes at a time and are wider than 2048, on both sides of each of the widths that change the kernel
+WIDE = [((5, 4095), BF16, F32), ((3, 4097), F32, BF16), ((600, 5001), BF16, BF16), ((2, 8191), F16, F16), ((4, 8193), F32, F32),
+        ((3, 12290), BF16, F16), ((2, 2, 9001), F32, F32), ((300, 16381), BF16, BF16)]
+
+
+@pytest.mark.parametrize("shape,dt,do", WIDE, ids=lambda v: str(v).replace("torch.", "").replace(" ", ""))
+@pytest.mark.parametrize("kind", (0, 1), ids=("rms", "l2"))
+@pytest.mark.parametrize("full", (True, False), ids=("all", "bare"))
+def test_norm_in_of_wide_rows(shape, dt, do, kind, full, dev):
+    test_norm_in(shape, dt, do, kind, full, dev)
+
+
+@pytest.mark.parametrize("shape,dt,do", WIDE, ids=lambda v: str(v).replace("torch.", "").replace(" ", ""))
+@pytest.mark.parametrize("act", (0, 1, None), ids=("silu", "sigmoid", "none"))
+def test_norm_out_of_wide_rows(shape, dt, do, act, dev):
+    test_norm_out(shape, dt, do, act, dev)
+
+
+@pytest.mark.parametrize("d", (2048, 4096, 8192, 16384))
+def test_wide_rows_at_an_odd_start(d, dev):
+    """Rows that begin off 16 bytes give what aligned copies of them give, to the roundings of another order of sums; what lies
+    around them stays."""
+    wide = rows((6, d + 3), BF16, dev, 1)
+    x, out = wide[:, 1:1 + d], torch.full((6, d + 3), 7.0, dtype=BF16, device=dev)
+    n, dn, dw = out[:, 2:2 + d], rows((6, d), BF16, dev, 2), torch.empty(d, device=dev)
+    sq.sq_norm_in(x, n)
+    near(n, hat(x.double(), 0, 1e-6), "n")
+    assert (out[:, :2] == 7).all() and (out[:, 2 + d:] == 7).all()
+    sq.sq_norm_in_bwd(x, dn, n, dweight=dw)
+    assert (out[:, :2] == 7).all() and (out[:, 2 + d:] == 7).all()
+    near(dw, (dn.double() * hat(x.double(), 0, 1e-6)).sum(0), "dweight", (dn.double() * hat(x.double(), 0, 1e-6)).abs().sum(0))
+
+
+@pytest.mark.parametrize("d", (4095, 5001, 9001))
+def test_wide_rows_in_place(d, dev):
+    x, r, dh = (rows((40, d), BF16, dev, i) for i in (1, 2, 3))
+    n, h = torch.empty_like(x), torch.empty_like(x)
+    sq.sq_norm_in(x, n, r=r, h=h, res_scale=0.5)
+    x2, r2 = x.clone(), r.clone()
+    sq.sq_norm_in(x2, x2, r=r2, h=r2, res_scale=0.5)
+    assert torch.equal(n, x2) and torch.equal(h, r2)
+    dx, dr, dc = torch.empty_like(x), torch.empty_like(x), [torch.empty(d, device=dev) for _ in range(2)]
+    sq.sq_norm_in_bwd(h, n, dx, r=r, dh=dh, dr=dr, dchan_scale=dc[0], res_scale=0.5)
+    h2, n2, r2, dh2 = h.clone(), n.clone(), r.clone(), dh.clone()
+    sq.sq_norm_in_bwd(h2, n2, dh2, r=r2, dh=dh2, dr=r2, dchan_scale=dc[1], res_scale=0.5)
+    assert torch.equal(dx, dh2) and torch.equal(dr, r2) and torch.equal(*dc)
+    o, dy, dz = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    sq.sq_norm_out(x, o, z=r, x=dh)
+    sq.sq_norm_out_bwd(x, o, dy, z=r, dz=dz)
+    y2, z2, e2 = x.clone(), r.clone(), dh.clone()
+    sq.sq_norm_out(y2, e2, z=z2, x=e2)
+    assert torch.equal(o, e2)
+    sq.sq_norm_out_bwd(y2, e2, y2, z=z2, dz=z2)
+    assert torch.equal(dy, y2) and torch.equal(dz, z2)
