@@ -666,3 +666,43 @@ def test_a_value_that_is_not_finite_stays_in_its_head(form, lens, what, value, d
     assert torch.equal(y[:, others], oy[:, others]) and torch.equal(s1[:, others], os_[:, others])
     assert torch.equal(y[lens[0]:], oy[lens[0]:]) and torch.equal(s1[1:], os_[1:])
     assert torch.equal(y[:before], oy[:before])
+
+
+@pytest.mark.parametrize("form", (0, 1), ids=("gdn", "kda"))
+def test_one_query_head_for_many_value_heads(form, dev):
+    """Sixteen value heads share q and k: dq and dk are sums over all of them."""
+    H, dk, dv, lens = 16, 64, 64, [37, 5]
+    x = scan_inputs(form, H, 1, dk, dv, lens, 85, F32)
+    y, s1 = forward(form, x, lens, dev)
+    yr, sr = scan_ref(x, lens)
+    near(y, yr, "y")
+    near(s1, sr, "s1")
+    g, r = backward(form, x, lens, dev), scan_grad_ref(x, lens)
+    for n in GRADS:
+        near(g[n], r[n], n)
+
+
+@pytest.mark.parametrize("lens", ([40], [6, 3]), ids=("chunks", "tokens"))
+@pytest.mark.parametrize("form", (0, 1), ids=("gdn", "kda"))
+def test_the_widest_strides(form, lens, dev):
+    """float32 rows just below 2^24 elements apart: a chunk of them spans 2 GiB, the arrays more than 4 GiB in between."""
+    H, dk, dv, T, stride = 2, 64, 64, sum(lens), (1 << 24) - 4
+    x = scan_inputs(form, H, H, dk, dv, lens, 86, F32)
+    d = {n: t.to(dev) for n, t in x.items()}
+    buf = torch.empty(T, 2, stride // 2, device=dev).view(T, stride)     # parts of one array, far enough apart
+    at = iter(range(0, stride, stride // 8 // 4 * 4))
+    part = lambda w: buf[:, (i := next(at)):i + H * w].unflatten(1, (H, w))  # noqa: E731
+    q, k, v, y, dq, dk_, dv_, dy = (part(w) for w in (dk, dk, dv, dv, dk, dk, dv, dv))
+    for a, n in ((q, "q"), (k, "k"), (v, "v"), (dy, "dy")):
+        a.copy_(d[n])
+    s1, ds0 = torch.zeros_like(d["s0"]), torch.zeros_like(d["s0"])
+    dgate, dbeta = torch.zeros_like(d["gate"]), torch.zeros_like(d["beta"])
+    sq.sq_delta_scan(form, q, k, v, d["gate"], d["beta"], y, seq_start=starts(lens, dev), s0=d["s0"], s1=s1)
+    sq.sq_delta_scan_bwd(form, q, k, v, d["gate"], d["beta"], dy, dq, dk_, dv_, dgate, dbeta, seq_start=starts(lens, dev),
+                         s0=d["s0"], ds1=d["ds1"], ds0=ds0)
+    yr, sr = scan_ref(x, lens)
+    near(y, yr, "y")
+    near(s1, sr, "s1")
+    r = scan_grad_ref(x, lens)
+    for n, t in zip(GRADS, (dq, dk_, dv_, dgate, dbeta, ds0)):
+        near(t, r[n], n)
