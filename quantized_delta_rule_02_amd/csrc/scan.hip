@@ -34,9 +34,9 @@ struct ScanLds {
     // A y of 16 bits takes three planes too: what two leave out, 2^-16 of an operand, is above the rounding of a y that is small
     // against its terms.
     static constexpr int LDK = (DK < 32 ? 32 : DK) + 8, LDT = 40, NMAT = MODE == kScanKeep ? 1 : 2;
-    // The chunk's matrices go through LDS where the operands are one plane.  With three, LDS is what a step waits for most,
-    // and the computing waves read them from memory, a step ahead (KDA prefill of 6150 tokens: 335 -> 315 us; a prefill of
-    // one-plane operands that way: 288 -> 313).
+    // The chunk's matrices go through LDS where the operands are one or two planes (a prefill of one-plane operands that reads
+    // them from memory: 288 -> 313 us).  With three, both copies (24 KiB) do not fit beside the 144 KiB of 16-bit rows with
+    // a gate per key row, and LDS is what a step waits for most: the computing waves read them from memory, a step ahead.
     static constexpr bool ML = NP < 3;
     struct First {
         uint16_t k[NP][32][LDK];                         // token-major: gamma K forward, (gamma_C / gamma) K in reverse
@@ -56,12 +56,13 @@ struct ScanLds {
 //
 // A computing wave owns 16 value columns and keeps S in its registers.  A step is a chain (S, e, u, S) on one or two waves a
 // SIMD, so its length is instructions issued, four cycles each, plus what the chain waits for.  Measured (one gate per head,
-// bfloat16, 128 x 128): 2.4 us a step where a CU has one state's half to itself, 3.2 us a state where all CUs are full
-// (12301 tokens in 7 prompts, 32 heads: 270 us).  With the staging left out that is 225 us: what bounds it are the chain's own
-// 297 vector instructions (188 of them split float32 operands) and 82 products of 16 cycles a step and wave.  Forms that were
-// slower: loading and staging by the computing waves (309 us; KDA prefill 366 against 315), 32 columns a wave with 32x32x16
-// products (281 us, one prompt of 777 tokens 78 us against 60), LDS reads issued a block ahead (361 us: the registers for it
-// leave room for one workgroup a CU).
+// bfloat16, 128 x 128): 2.2 us a step where a CU has one state's half to itself, 3.3 us a state where all CUs are full
+// (12301 tokens in 7 prompts, 32 heads: 280 us).  The chain's own 309 vector instructions (200 of them split float32 operands)
+// and 96 products of 16 cycles a step and wave are 1.2 us, 2.3 us for the two waves of a full SIMD; the rest is LDS latency
+// and the barriers.  Forms that were slower when y took two planes (270 us then; 225 with the staging left out): loading and
+// staging by the computing waves (309 us; KDA prefill 366 against 315), 32 columns a wave with 32x32x16 products (281 us, one
+// prompt of 777 tokens 78 us against 60), LDS reads issued a block ahead (361 us: the registers for it leave room for one
+// workgroup a CU).
 template <int DK, int DT, bool KDA, int MODE, int NC>
 struct Scan {
     using Lds = ScanLds<DK, DT, KDA, MODE, NC>;
@@ -602,8 +603,10 @@ static hipError_t scan_nc(const ScanParams& p, bool backward, hipStream_t s) {
 template <int DK, int DT, bool KDA>
 static hipError_t scan_t(const ScanParams& p, bool backward, hipStream_t s) {
     // Eight computing waves share the operands of four staging waves where there are more workgroups of four than CUs (256);
-    // below that, four put the columns on twice as many CUs (a prompt of 777 tokens: 61 us, with eight 73; seven prompts of
-    // 12301 tokens, 448 workgroups of four: 288 us, with eight 268).
+    // below that, four put the columns on twice as many CUs (a prompt of 777 tokens: 56 us, with eight 74; seven prompts of
+    // 12301 tokens, 448 workgroups of four: 314 us, with eight 285; both scans of the backward pass, 512 and 8190 tokens: 1004
+    // and 992 us a call).  With a gate per key row a workgroup of either size fills a CU's LDS: there 320 of four, one and a
+    // quarter for each CU, are still a little faster (prefill of 6150 tokens: 426 us a call, with eight 443).
     if constexpr (DK == 128) {
         if ((int64_t)p.n_long * p.n_heads * (p.dv / 64) * (backward ? 2 : 1) > 256) return scan_nc<DK, DT, KDA, 8>(p, backward, s);
     }

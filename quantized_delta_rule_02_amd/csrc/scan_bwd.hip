@@ -18,8 +18,10 @@
 // their dq and dk add up in registers, in a fixed order.
 //
 // Reads 128 KiB of states and gradients per chunk and head (128 x 128), 1.06 GB at 8190 tokens and 32 heads: 174 us at the rate
-// of a copy; the launch takes 490 us there (one gate per head), 266 us at 3001 tokens with gates per key row.  Its vector
-// instructions alone are 141 us, its products 66; the rest is waiting for the states with two waves a SIMD.  A wave per 32 key
+// of a copy; the launch takes 465 us there (one gate per head), 253 us at 3001 tokens with gates per key row.  Its 79 million
+// vector instructions are 128 us at four cycles each on 1024 SIMDs, its 10 million products of 16 cycles 66; the rest is waiting
+// for the states with two waves a SIMD.  The value heads of a q/k head come one after another, so a call of few chunks and q/k
+// heads leaves CUs idle.  A wave per 32 key
 // rows is as fast (480 us) with one gate per head and slower with a gate per key row (307 us), where its registers spill; 16 waves
 // a CU (128 registers, spilling) take 589 and 367 us; all of a workgroup's states in flight at once (spilling) 677 and 322.
 #include <hip/hip_runtime.h>
