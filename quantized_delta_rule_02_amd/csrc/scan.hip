@@ -604,8 +604,8 @@ template <int DK, int DT, bool KDA>
 static hipError_t scan_t(const ScanParams& p, bool backward, hipStream_t s) {
     // Eight computing waves share the operands of four staging waves where there are more workgroups of four than CUs (256);
     // below that, four put the columns on twice as many CUs (a prompt of 777 tokens: 56 us, with eight 74; seven prompts of
-    // 12301 tokens, 448 workgroups of four: 314 us, with eight 285; both scans of the backward pass, 512 and 8190 tokens: 1004
-    // and 992 us a call).  With a gate per key row a workgroup of either size fills a CU's LDS: there 320 of four, one and a
+    // 12301 tokens, 448 workgroups of four: 314 us, with eight 285; a backward call of 8190 tokens, 512 workgroups of four:
+    // 1004 us, with eight 992).  With a gate per key row a workgroup of either size fills a CU's LDS: there 320 of four, one and a
     // quarter for each CU, are still a little faster (prefill of 6150 tokens: 426 us a call, with eight 443).
     if constexpr (DK == 128) {
         if ((int64_t)p.n_long * p.n_heads * (p.dv / 64) * (backward ? 2 : 1) > 256) return scan_nc<DK, DT, KDA, 8>(p, backward, s);
