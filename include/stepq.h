@@ -68,13 +68,17 @@ typedef int32_t sq_status;
 #define SQ_QUANT_DUAL_AXIS 0      /* row factors sqrt(m / w) + impact-weighted column fit (the method) */
 #define SQ_QUANT_ROW_ABSMAX 1     /* per-row absmax r = m / qmax, column scales 1 (ablation: no fit) */
 
-#define SQ_DTYPE_F32  0            /* element types of the scan's and the norms' row arrays */
+#define SQ_DTYPE_F32  0            /* element types of row arrays */
 #define SQ_DTYPE_BF16 1
 #define SQ_DTYPE_F16  2
 #define SQ_NORM_RMS 0             /* divide by sqrt(mean(x^2) + eps) */
 #define SQ_NORM_L2  1             /* divide by sqrt(sum(x^2) + eps)  */
 #define SQ_ACT_SILU    0          /* gate g(z) = z sigmoid(z) */
 #define SQ_ACT_SIGMOID 1          /* gate g(z) = sigmoid(z)   */
+#define SQ_ACT_NONE    2          /* no activation (sq_conv only) */
+#define SQ_CACHE_INT8  0          /* codes -127..127, one byte            */
+#define SQ_CACHE_INT4  1          /* codes -7..7, two a byte, first low   */
+#define SQ_CACHE_E4M3  2          /* 8-bit floats, 3 bits after the point */
 
 #define SQ_MAX_WIDTHS 8
 #define SQ_MAX_GRID   8
@@ -382,6 +386,113 @@ sq_status sq_norm_out(const sq_norm_cfg* cfg, const sq_rows* y, const sq_rows* z
 sq_status sq_norm_out_bwd(const sq_norm_cfg* cfg, const sq_rows* y, const sq_rows* z, const sq_rows* d_o,
                           const float* d_weight, const float* d_chan_scale, const sq_rows* dy, const sq_rows* dz,
                           float* d_dweight, float* d_dchan_scale, void* d_work, size_t work_bytes, void* stream);
+
+/* ---- causal convolution before the recurrence -----------------------------
+ * One short filter a channel over packed sequences (what makes the step's and the scans' q, k, v or u from a layer's projections):
+ *   p_t = bias + sum over j < width of weight[c][j] * x_{t - width + 1 + j};   y_t = p_t (SQ_ACT_NONE) or p_t sigmoid(p_t) (SQ_ACT_SILU)
+ * Sequences are those of sq_delta_scan: d_seq_start (int32, device, n_seq + 1 values, not decreasing, within [0, n_tokens]; NULL: one
+ * sequence of n_tokens); one may be empty; tokens outside all of them are neither read nor written; offsets that break the rules give
+ * unspecified results and touch nothing outside the arrays.  Inputs before a sequence come from d_s0 [n_seq][width - 1][channels],
+ * oldest first (NULL: zeros); d_s1, the same shape, receives each sequence's last width - 1 inputs (bit for bit, from d_s0 where
+ * the sequence is shorter; NULL: not wanted).  d_s0 and d_s1 may be the same array; no other two arrays may overlap, but in
+ * sq_conv_step y may be x's own array.
+ * x, y, the states and all their gradients have the type cfg->dtype; weight [channels][width] and bias [channels] (NULL = 0) are
+ * float32, and so is the arithmetic; each output is rounded once.  Row arrays: element (token, c) at d_ptr[token * stride + c], any
+ * stride of at least `channels`.  Arrays aligned to 16 bytes with strides and channels in multiples of 16 bytes are accessed 16 bytes
+ * at a time, others element by element.
+ *
+ * sq_conv_bwd: from dy and d_ds1 (of the final states, NULL = zero): dx, and, where not NULL, d_dweight, d_dbias and d_ds0.  Sums over
+ * tokens are taken in a fixed order through a workspace of sq_conv_bytes bytes, under the rules of the scan's (used if d_dweight or
+ * d_dbias is given; with no sequences the sums are written as zero).
+ * sq_conv_step: one token of each of cfg->n_tokens requests (n_seq and d_seq_start are not used), its inputs before that in slot
+ * d_slots[b] (int32, device; NULL: b) of d_window [n_slots][width - 1][channels], which moves on by one.  A slot outside [0, n_slots)
+ * skips the request: its y is left as it was.  Slots must be distinct within a call (otherwise what that slot holds is unspecified). */
+typedef struct sq_conv_cfg {
+    int32_t dtype, act;           /* SQ_DTYPE_*; SQ_ACT_SILU or SQ_ACT_NONE */
+    int32_t channels, width;      /* width: 2..8 taps */
+    int32_t n_seq;
+    int64_t n_tokens;             /* below 2^31 */
+    const int32_t* d_seq_start;
+} sq_conv_cfg;
+
+sq_status sq_conv_bytes(const sq_conv_cfg* cfg, size_t* bytes);
+sq_status sq_conv(const sq_conv_cfg* cfg, const sq_rows* x, const float* d_weight, const float* d_bias, const void* d_s0,
+                  const sq_rows* y, void* d_s1, void* stream);
+sq_status sq_conv_bwd(const sq_conv_cfg* cfg, const sq_rows* x, const float* d_weight, const float* d_bias, const void* d_s0,
+                      const sq_rows* dy, const void* d_ds1, const sq_rows* dx, float* d_dweight, float* d_dbias, void* d_ds0,
+                      void* d_work, size_t work_bytes, void* stream);
+sq_status sq_conv_step(const sq_conv_cfg* cfg, const sq_rows* x, const float* d_weight, const float* d_bias,
+                       const int32_t* d_slots, int64_t n_slots, void* d_window, const sq_rows* y, void* stream);
+
+/* ---- selective state space scan --------------------------------------------
+ * The diagonal sibling of the gated delta scan: every channel has d_state states with a decay of their own that follows the input.
+ * Over packed sequences (as above), per sequence and channel c of group g = c / (channels / n_groups), from h = d_s0 (NULL: zero):
+ *   delta = softplus(dt + dt_bias[c]) (softplus = 0: dt + dt_bias[c]);   h[n] = exp(delta a[c][n]) h[n] + delta u B[g][n];
+ *   p = sum over n of C[g][n] h[n] + d[c] u;   y = p, or p z sigmoid(z) with a gate z;   d_s1 = h after the last token.
+ * u, dt, z, y: rows of `channels` elements; b, c: rows of n_groups * d_state; all of type cfg->dtype with any stride.  d_a
+ * [channels][d_state], d_d and d_dt_bias [channels] (NULL = 0), states [n_seq][channels][d_state] and the arithmetic are float32; each
+ * output is rounded once.  d_a and the states are aligned to 16 bytes.  Rows that allow accesses of four elements (addresses,
+ * strides, channels / n_groups) are accessed so, others element by element.  d_s0 and d_s1 may be the same array; no other two
+ * arrays may overlap.  Few long sequences are cut into segments that run side by side (a choice by the call's sizes alone); the
+ * result agrees with the token by token order to float32 rounding.  Nothing depends on what else runs (no atomics, fixed orders).
+ * A result that the formula makes NaN or infinite is not finite here either; other channels (in the gradients: but for those of b
+ * and c of that token and group and what they sum up) and other sequences keep their results.
+ *
+ * sq_ssm_scan_bwd: from dy and d_ds1 (NULL = zero) the gradients of u, dt, b, c (summed over a group's channels), z (NULL: not
+ * wanted), and where not NULL of a, d, dt_bias and the first states (d_ds0 may be d_ds1).  Nothing of the forward call is needed.
+ * With no sequences the sums over tokens are written as zero.
+ * Workspace: sq_ssm_scan_bytes bytes, under the rules of the scan's.
+ * sq_ssm_step: one token of each of cfg->n_tokens requests (n_seq and d_seq_start are not used) with its state in slot d_slots[b]
+ * (int32, device; NULL: b) of d_state [n_slots][channels][d_state], updated in place; slots as in sq_conv_step. */
+typedef struct sq_ssm_cfg {
+    int32_t dtype;
+    int32_t channels, d_state, n_groups;   /* d_state: 8, 16, 32, 64 or 128; n_groups a divisor of channels */
+    int32_t softplus;             /* 1: delta = softplus(dt + dt_bias), 0: delta = dt + dt_bias */
+    int32_t n_seq;
+    int64_t n_tokens;             /* below 2^31 */
+    const int32_t* d_seq_start;
+} sq_ssm_cfg;
+
+typedef struct sq_ssm_in {        /* z, d_d and d_dt_bias may be NULL */
+    const sq_rows *u, *dt, *b, *c, *z;
+    const float *d_a, *d_d, *d_dt_bias;
+} sq_ssm_in;
+
+typedef struct sq_ssm_grads {     /* dz, d_da, d_dd and d_ddt_bias may be NULL */
+    const sq_rows *du, *ddt, *db, *dc, *dz;
+    float *d_da, *d_dd, *d_ddt_bias;
+} sq_ssm_grads;
+
+sq_status sq_ssm_scan_bytes(const sq_ssm_cfg* cfg, int32_t backward, size_t* bytes);
+sq_status sq_ssm_scan(const sq_ssm_cfg* cfg, const sq_ssm_in* in, const float* d_s0, const sq_rows* y, float* d_s1, void* d_work,
+                      size_t work_bytes, void* stream);
+sq_status sq_ssm_scan_bwd(const sq_ssm_cfg* cfg, const sq_ssm_in* in, const float* d_s0, const sq_rows* dy, const float* d_ds1,
+                          const sq_ssm_grads* out, float* d_ds0, void* d_work, size_t work_bytes, void* stream);
+sq_status sq_ssm_step(const sq_ssm_cfg* cfg, const sq_ssm_in* in, const int32_t* d_slots, int64_t n_slots, float* d_state,
+                      const sq_rows* y, void* stream);
+
+/* ---- quantised row cache ----------------------------------------------------
+ * Rows of d elements (keys and values of attention layers beside the recurrent ones, states and windows of requests set aside) held in
+ * 8 or 4 bits, each group of `group` elements with a float32 scale:
+ *   scale = max |x| / Q rounded to float32, Q = 127 (SQ_CACHE_INT8), 7 (SQ_CACHE_INT4), 448 (SQ_CACHE_E4M3);
+ *   code = the format's value nearest to x / scale (of the exact quotient, ties to even, at most Q in magnitude);  value = code * scale.
+ * A group of zeros has the scale 0 and codes 0.  A group with a NaN or an infinity has the scale NaN and codes 0, so that all of it
+ * reads back as NaN.  SQ_CACHE_E4M3 bytes are 8-bit floats (1 sign, 4 exponent bits of bias 7, 3 fraction bits, no infinities).
+ * Slot s holds its codes at d_codes + s * d (s * d / 2 for 4-bit codes, the first of two in the low half of its byte) and its
+ * scales at d_scales + s * (d / group).  Row i is slot d_slots[i] (int32, device; NULL: i) of n_slots; a slot outside [0, n_slots) is
+ * skipped: nothing is written for that row.  Slots written must be distinct within a call (otherwise what that slot holds is
+ * unspecified); slots read may repeat.  Rows x, out: type cfg->dtype, any stride of at least d.
+ * Rows aligned to 16 bytes (with their stride), groups in multiples of 8 and codes aligned to 8 bytes (4 for 4-bit codes) are accessed
+ * 16 bytes at a time, others element by element. */
+typedef struct sq_cache_cfg {
+    int32_t dtype, format;        /* SQ_DTYPE_* of the rows, SQ_CACHE_* */
+    int32_t d, group;             /* group: 1..1024, a divisor of d, even for 4-bit codes */
+    int64_t n_rows, n_slots;      /* below 2^31 */
+} sq_cache_cfg;
+
+sq_status sq_cache_write(const sq_cache_cfg* cfg, const sq_rows* x, const int32_t* d_slots, void* d_codes, float* d_scales, void* stream);
+sq_status sq_cache_read(const sq_cache_cfg* cfg, const void* d_codes, const float* d_scales, const int32_t* d_slots, const sq_rows* out,
+                        void* stream);
 
 /* ---- errors / info ------------------------------------------------------ */
 const char* sq_status_str(sq_status s);

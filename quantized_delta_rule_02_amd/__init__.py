@@ -14,7 +14,7 @@ from ctypes import POINTER, byref, c_double, c_float, c_int32, c_size_t, c_uint6
 import numpy as np
 
 from . import _lib
-from ._lib import (SQ_ACT_SIGMOID, SQ_ACT_SILU, SQ_DTYPE_BF16, SQ_DTYPE_F16, SQ_DTYPE_F32, SQ_NORM_L2, SQ_NORM_RMS, SQ_FORM_GDN, SQ_FORM_KDA, SQ_PIVOT_BITS, SQ_QUANT_DUAL_AXIS, SQ_QUANT_ROW_ABSMAX,
+from ._lib import (SQ_ACT_NONE, SQ_ACT_SIGMOID, SQ_ACT_SILU, SQ_CACHE_E4M3, SQ_CACHE_INT4, SQ_CACHE_INT8, SQ_DTYPE_BF16, SQ_DTYPE_F16, SQ_DTYPE_F32, SQ_NORM_L2, SQ_NORM_RMS, SQ_FORM_GDN, SQ_FORM_KDA, SQ_PIVOT_BITS, SQ_QUANT_DUAL_AXIS, SQ_QUANT_ROW_ABSMAX,
                    SQ_SPLIT_STATIC_MAX_FLOATS, SQ_STEP_NO_JOIN, SQ_STEP_SPLIT, SQ_STEP_VALIDATE, SQ_UNIT_HEAD,
                    SQ_UNIT_ROW)
 
@@ -23,6 +23,8 @@ __all__ = [
     "sq_plan_save", "sq_plan_load", "sq_calib_generate", "sq_pool_bytes", "sq_pool_create", "sq_state_step", "sq_state_step_split_static",
     "sq_pack", "sq_unpack", "sq_export", "sq_import", "sq_int8_step", "sq_fp32_step", "sq_copy", "sq_valu_probe",
     "sq_delta_scan_bytes", "sq_delta_scan", "sq_delta_scan_bwd", "sq_norm_bytes", "sq_norm_in", "sq_norm_in_bwd", "sq_norm_out", "sq_norm_out_bwd",
+    "sq_conv_bytes", "sq_conv", "sq_conv_bwd", "sq_conv_step", "sq_ssm_scan_bytes", "sq_ssm_scan", "sq_ssm_scan_bwd", "sq_ssm_step",
+    "sq_cache_write", "sq_cache_read", "SQ_ACT_NONE", "SQ_CACHE_INT8", "SQ_CACHE_INT4", "SQ_CACHE_E4M3",
     "SQ_DTYPE_F32", "SQ_DTYPE_BF16", "SQ_DTYPE_F16", "SQ_NORM_RMS", "SQ_NORM_L2", "SQ_ACT_SILU", "SQ_ACT_SIGMOID",
     "sq_supported_shapes", "SQ_FORM_GDN", "SQ_FORM_KDA", "SQ_UNIT_HEAD", "SQ_UNIT_ROW", "SQ_STEP_SPLIT",
     "SQ_STEP_VALIDATE", "SQ_STEP_NO_JOIN", "SQ_SPLIT_STATIC_MAX_FLOATS", "SQ_PIVOT_BITS", "SQ_QUANT_DUAL_AXIS", "SQ_QUANT_ROW_ABSMAX",
@@ -618,3 +620,222 @@ def sq_norm_out_bwd(y, do, dy, weight=None, z=None, dz=None, act=SQ_ACT_SILU, ch
     work, nbytes, keep = c.work(workspace, stream, dweight is not None or dchan_scale is not None)
     _call(_lib.load().sq_norm_out_bwd, "sq_norm_out_bwd", c.device, stream, c.cfg(y.dtype, do.dtype, kind, act, eps, res_scale, 1.0), *args, work, nbytes)
     del keep
+
+
+# ---------------------------------------------------------------- convolution, selective scan, row cache
+
+def _first(t, n, what, name):
+    """The device of the tensor that fixes a call's sizes."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must be {what}")
+    return t.device
+
+
+def _seqs(seq_start, device):
+    """n_seq and the address of the offsets (one sequence of all tokens if there are none)."""
+    import torch
+    if seq_start is None:
+        return 1, None
+    _on(seq_start, device, "seq_start")
+    if seq_start.dim() != 1 or seq_start.numel() < 1:
+        raise ValueError("seq_start must hold n_seq + 1 offsets")
+    return seq_start.numel() - 1, _dev(seq_start, torch.int32, seq_start.numel(), "seq_start")
+
+
+def _typed(t, shape, dtype, device, name):
+    """Pointer of a contiguous tensor of exactly this shape and type (None stays NULL)."""
+    if t is None:
+        return None
+    _on(t, device, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _slots(slots, n, device):
+    import torch
+    return _typed(slots, (n,), torch.int32, device, "slots")
+
+
+def _conv_cfg(x, weight, act, n_seq, start):
+    dev = _first(x, 2, "[tokens, channels]", "x")
+    _first(weight, 2, "[channels, width]", "weight")
+    T, C = x.shape
+    return _lib.SqConvCfg(_dtype_code(x.dtype), int(act), C, weight.shape[1], n_seq, T, start), dev
+
+
+def sq_conv_bytes(dtype, channels, width, n_seq, n_tokens) -> int:
+    """Workspace bytes of sq_conv_bwd for arrays of these sizes."""
+    cfg = _lib.SqConvCfg(_dtype_code(dtype), SQ_ACT_NONE, channels, width, n_seq, n_tokens, None)
+    n = c_size_t(0)
+    _check(_lib.load().sq_conv_bytes(byref(cfg), byref(n)), "sq_conv_bytes")
+    return n.value
+
+
+def sq_conv(x, weight, y, bias=None, act=SQ_ACT_SILU, seq_start=None, s0=None, s1=None, stream=None):
+    """The causal convolution of packed sequences: writes y and, if given, each sequence's last inputs s1.
+
+    x, y [tokens, channels] (one type; any token stride); weight [channels, width], bias [channels] float32; s0, s1
+    [n_seq, width - 1, channels] of x's type; seq_start int32 [n_seq + 1].
+    """
+    dev = _first(x, 2, "[tokens, channels]", "x")
+    n_seq, start = _seqs(seq_start, dev)
+    cfg, _ = _conv_cfg(x, weight, act, n_seq, start)
+    C, W = weight.shape
+    st = (n_seq, W - 1, x.shape[1])
+    args = [byref(_row_array(x, x.shape, x.dtype, dev, "x")), _plain(weight, (x.shape[1], W), dev, "weight"), _plain(bias, (C,), dev, "bias"),
+            _typed(s0, st, x.dtype, dev, "s0"), byref(_row_array(y, x.shape, x.dtype, dev, "y")), _typed(s1, st, x.dtype, dev, "s1")]
+    _call(_lib.load().sq_conv, "sq_conv", dev, stream, byref(cfg), *args)
+
+
+def sq_conv_bwd(x, weight, dy, dx, dweight=None, bias=None, dbias=None, act=SQ_ACT_SILU, seq_start=None, s0=None, ds1=None,
+                ds0=None, workspace=None, stream=None):
+    """Gradients of sq_conv, from dy and (optional) ds1, into dx and, if given, dweight, dbias and ds0."""
+    dev = _first(x, 2, "[tokens, channels]", "x")
+    n_seq, start = _seqs(seq_start, dev)
+    cfg, _ = _conv_cfg(x, weight, act, n_seq, start)
+    W, C = weight.shape[1], x.shape[1]
+    st = (n_seq, W - 1, C)
+    rows = lambda t, name: byref(_row_array(t, x.shape, x.dtype, dev, name))  # noqa: E731
+    args = [rows(x, "x"), _plain(weight, (C, W), dev, "weight"), _plain(bias, (C,), dev, "bias"), _typed(s0, st, x.dtype, dev, "s0"),
+            rows(dy, "dy"), _typed(ds1, st, x.dtype, dev, "ds1"), rows(dx, "dx"), _plain(dweight, (C, W), dev, "dweight"),
+            _plain(dbias, (C,), dev, "dbias"), _typed(ds0, st, x.dtype, dev, "ds0")]
+    work, nbytes, keep = None, 0, None
+    if dweight is not None or dbias is not None:
+        n = c_size_t(0)
+        _check(_lib.load().sq_conv_bytes(byref(cfg), byref(n)), "sq_conv_bytes")
+        work, nbytes, keep = _workspace(workspace, n.value, dev, stream)
+    _call(_lib.load().sq_conv_bwd, "sq_conv_bwd", dev, stream, byref(cfg), *args, work, nbytes)
+    del keep
+
+
+def sq_conv_step(x, weight, window, y, slots=None, bias=None, act=SQ_ACT_SILU, stream=None):
+    """One token of each request: x, y [batch, channels]; window [n_slots, width - 1, channels] of x's type, updated in place."""
+    cfg, dev = _conv_cfg(x, weight, act, 0, None)
+    _first(window, 3, "[n_slots, width - 1, channels]", "window")
+    (T, C), W = x.shape, weight.shape[1]
+    args = [byref(_row_array(x, x.shape, x.dtype, dev, "x")), _plain(weight, (C, W), dev, "weight"), _plain(bias, (C,), dev, "bias"),
+            _slots(slots, T, dev), window.shape[0], _typed(window, (window.shape[0], W - 1, C), x.dtype, dev, "window"),
+            byref(_row_array(y, x.shape, x.dtype, dev, "y"))]
+    _call(_lib.load().sq_conv_step, "sq_conv_step", dev, stream, byref(cfg), *args)
+
+
+class _SsmCall:
+    """The configuration and inputs of one call of the selective scan; u, a and b fix its sizes."""
+
+    def __init__(self, u, dt, a, b, c, d, dt_bias, z, softplus, seq_start=None, step=False):
+        self.dev = dev = _first(u, 2, "[tokens, channels]", "u")
+        _first(a, 2, "[channels, d_state]", "a")
+        _first(b, 3, "[tokens, groups, d_state]", "b")
+        self.T, self.C = T, C = u.shape
+        self.N, self.G = N, G = a.shape[1], b.shape[1]
+        self.dtype = u.dtype
+        self.n_seq, start = (0, None) if step else _seqs(seq_start, dev)
+        self.cfg = _lib.SqSsmCfg(_dtype_code(u.dtype), C, N, G, int(bool(softplus)), self.n_seq, T, start)
+        self.keep = []
+        self.inputs = _lib.SqSsmIn(self.rows(u, "u"), self.rows(dt, "dt"), self.bc(b, "b"), self.bc(c, "c"), self.rows(z, "z"),
+                                   self.vec(a, (C, N), "a"), self.vec(d, (C,), "d"), self.vec(dt_bias, (C,), "dt_bias"))
+        self.states = (self.n_seq, C, N)
+
+    def _ptr(self, t, shape, name):
+        if t is None:
+            return None
+        p = ctypes.pointer(_row_array(t, shape, self.dtype, self.dev, name))
+        self.keep.append(p)
+        return p
+
+    def rows(self, t, name):
+        return self._ptr(t, (self.T, self.C), name)
+
+    def bc(self, t, name):
+        return self._ptr(t, (self.T, self.G, self.N), name)
+
+    def vec(self, t, shape, name):
+        return _plain(t, shape, self.dev, name)
+
+    def work(self, workspace, backward, stream):
+        n = c_size_t(0)
+        _check(_lib.load().sq_ssm_scan_bytes(byref(self.cfg), backward, byref(n)), "sq_ssm_scan_bytes")
+        return _workspace(workspace, n.value, self.dev, stream) if n.value else (None, 0, None)
+
+
+def sq_ssm_scan_bytes(dtype, channels, d_state, n_groups, n_seq, n_tokens, backward=False) -> int:
+    """Workspace bytes of sq_ssm_scan (or of sq_ssm_scan_bwd) for arrays of these sizes."""
+    cfg = _lib.SqSsmCfg(_dtype_code(dtype), channels, d_state, n_groups, 1, n_seq, n_tokens, None)
+    n = c_size_t(0)
+    _check(_lib.load().sq_ssm_scan_bytes(byref(cfg), int(backward), byref(n)), "sq_ssm_scan_bytes")
+    return n.value
+
+
+def sq_ssm_scan(u, dt, a, b, c, y, d=None, dt_bias=None, z=None, softplus=True, seq_start=None, s0=None, s1=None, workspace=None,
+                stream=None):
+    """The selective scan over packed sequences: writes y and, if given, the final states s1.
+
+    u, dt, z, y [tokens, channels], b, c [tokens, groups, d_state] (one type; any token stride); a [channels, d_state], d,
+    dt_bias [channels], s0, s1 [n_seq, channels, d_state] float32; seq_start int32 [n_seq + 1].
+    """
+    call = _SsmCall(u, dt, a, b, c, d, dt_bias, z, softplus, seq_start)
+    args = [call.vec(s0, call.states, "s0"), call.rows(y, "y"), call.vec(s1, call.states, "s1")]
+    work, nbytes, keep = call.work(workspace, 0, stream)
+    _call(_lib.load().sq_ssm_scan, "sq_ssm_scan", call.dev, stream, byref(call.cfg), byref(call.inputs), *args, work, nbytes)
+    del keep
+
+
+def sq_ssm_scan_bwd(u, dt, a, b, c, dy, du, ddt, da, db, dc, d=None, dt_bias=None, z=None, dz=None, dd=None, ddt_bias=None, softplus=True,
+                    seq_start=None, s0=None, ds1=None, ds0=None, workspace=None, stream=None):
+    """Gradients of sq_ssm_scan, from dy and (optional) ds1: du, ddt, db, dc and, where not None, da, dz, dd, ddt_bias and ds0."""
+    call = _SsmCall(u, dt, a, b, c, d, dt_bias, z, softplus, seq_start)
+    C, N = call.C, call.N
+    grads = _lib.SqSsmGrads(call.rows(du, "du"), call.rows(ddt, "ddt"), call.bc(db, "db"), call.bc(dc, "dc"), call.rows(dz, "dz"),
+                            call.vec(da, (C, N), "da"), call.vec(dd, (C,), "dd"), call.vec(ddt_bias, (C,), "ddt_bias"))
+    args = [call.vec(s0, call.states, "s0"), call.rows(dy, "dy"), call.vec(ds1, call.states, "ds1"), byref(grads), call.vec(ds0, call.states, "ds0")]
+    work, nbytes, keep = call.work(workspace, 1, stream)
+    _call(_lib.load().sq_ssm_scan_bwd, "sq_ssm_scan_bwd", call.dev, stream, byref(call.cfg), byref(call.inputs), *args, work, nbytes)
+    del keep
+
+
+def sq_ssm_step(u, dt, a, b, c, state, y, slots=None, d=None, dt_bias=None, z=None, softplus=True, stream=None):
+    """One token of each request: u, dt, z, y [batch, channels], b, c [batch, groups, d_state]; state [n_slots, channels,
+    d_state] float32, updated in place."""
+    call = _SsmCall(u, dt, a, b, c, d, dt_bias, z, softplus, step=True)
+    _first(state, 3, "[n_slots, channels, d_state]", "state")
+    n = state.shape[0]
+    args = [_slots(slots, call.T, call.dev), n, call.vec(state, (n, call.C, call.N), "state"), call.rows(y, "y")]
+    _call(_lib.load().sq_ssm_step, "sq_ssm_step", call.dev, stream, byref(call.cfg), byref(call.inputs), *args)
+
+
+def _cache_call(rows, codes, scales, slots, format, name):
+    import torch
+    dev = _first(rows, 2, "[rows, d]", name)
+    _first(codes, 2, "[n_slots, bytes of a row]", "codes")
+    _first(scales, 2, "[n_slots, d / group]", "scales")
+    R, d = rows.shape
+    S, groups = scales.shape
+    if groups < 1 or d % groups:
+        raise ValueError(f"scales: {groups} a row of {d} elements")
+    cfg = _lib.SqCacheCfg(_dtype_code(rows.dtype), int(format), d, d // groups, R, S)
+    if codes.dtype not in (torch.uint8, torch.int8):
+        raise TypeError(f"codes must be uint8 or int8, got {codes.dtype}")
+    held = (S, d // 2 if format == SQ_CACHE_INT4 else d)
+    return (dev, byref(cfg), byref(_row_array(rows, rows.shape, rows.dtype, dev, name)), _slots(slots, R, dev),
+            _typed(codes, held, codes.dtype, dev, "codes"), _plain(scales, (S, groups), dev, "scales"))
+
+
+def sq_cache_write(x, codes, scales, slots=None, format=SQ_CACHE_INT8, stream=None):
+    """Quantises rows x [rows, d] into slots of a cache: codes [n_slots, d] (4-bit codes: d / 2) bytes, scales [n_slots, d / group]
+    float32; slots int32 [rows] (None: row i is slot i)."""
+    dev, cfg, rows, at, held, scale = _cache_call(x, codes, scales, slots, format, "x")
+    _call(_lib.load().sq_cache_write, "sq_cache_write", dev, stream, cfg, rows, at, held, scale)
+
+
+def sq_cache_read(codes, scales, out, slots=None, format=SQ_CACHE_INT8, stream=None):
+    """Reads slots of a cache back into rows out [rows, d]."""
+    dev, cfg, rows, at, held, scale = _cache_call(out, codes, scales, slots, format, "out")
+    _call(_lib.load().sq_cache_read, "sq_cache_read", dev, stream, cfg, held, scale, at, rows)

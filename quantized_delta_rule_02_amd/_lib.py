@@ -18,7 +18,8 @@ SQ_STEP_SPLIT, SQ_STEP_VALIDATE, SQ_STEP_NO_JOIN = 1, 2, 4
 SQ_PIVOT_BITS = 16
 SQ_DTYPE_F32, SQ_DTYPE_BF16, SQ_DTYPE_F16 = 0, 1, 2
 SQ_NORM_RMS, SQ_NORM_L2 = 0, 1
-SQ_ACT_SILU, SQ_ACT_SIGMOID = 0, 1
+SQ_ACT_SILU, SQ_ACT_SIGMOID, SQ_ACT_NONE = 0, 1, 2
+SQ_CACHE_INT8, SQ_CACHE_INT4, SQ_CACHE_E4M3 = 0, 1, 2
 SQ_MAX_WIDTHS, SQ_MAX_GRID = 8, 8
 SQ_SPLIT_STATIC_MAX_FLOATS = 8 << 20
 
@@ -65,6 +66,28 @@ class SqNormCfg(ctypes.Structure):
                 ("n_inner", c_int32), ("d", c_int32), ("eps", c_float), ("res_scale", c_float), ("out_scale", c_float)]
 
 
+class SqConvCfg(ctypes.Structure):
+    _fields_ = [("dtype", c_int32), ("act", c_int32), ("channels", c_int32), ("width", c_int32), ("n_seq", c_int32),
+                ("n_tokens", c_int64), ("d_seq_start", c_void_p)]
+
+
+class SqSsmCfg(ctypes.Structure):
+    _fields_ = [("dtype", c_int32), ("channels", c_int32), ("d_state", c_int32), ("n_groups", c_int32), ("softplus", c_int32),
+                ("n_seq", c_int32), ("n_tokens", c_int64), ("d_seq_start", c_void_p)]
+
+
+class SqSsmIn(ctypes.Structure):
+    _fields_ = [(n, POINTER(SqRows)) for n in ("u", "dt", "b", "c", "z")] + [(n, c_void_p) for n in ("d_a", "d_d", "d_dt_bias")]
+
+
+class SqSsmGrads(ctypes.Structure):
+    _fields_ = [(n, POINTER(SqRows)) for n in ("du", "ddt", "db", "dc", "dz")] + [(n, c_void_p) for n in ("d_da", "d_dd", "d_ddt_bias")]
+
+
+class SqCacheCfg(ctypes.Structure):
+    _fields_ = [("dtype", c_int32), ("format", c_int32), ("d", c_int32), ("group", c_int32), ("n_rows", c_int64), ("n_slots", c_int64)]
+
+
 _P = c_void_p
 _R = POINTER(SqRows)
 _SIGS = {
@@ -103,6 +126,16 @@ _SIGS = {
     "sq_norm_in_bwd": (c_int32, [POINTER(SqNormCfg), _R, _R, _R, _R, _P, _P, _R, _R, _P, _P, _P, c_size_t, _P]),
     "sq_norm_out": (c_int32, [POINTER(SqNormCfg), _R, _R, _R, _P, _P, _R, _P]),
     "sq_norm_out_bwd": (c_int32, [POINTER(SqNormCfg), _R, _R, _R, _P, _P, _R, _R, _P, _P, _P, c_size_t, _P]),
+    "sq_conv_bytes": (c_int32, [POINTER(SqConvCfg), POINTER(c_size_t)]),
+    "sq_conv": (c_int32, [POINTER(SqConvCfg), _R, _P, _P, _P, _R, _P, _P]),
+    "sq_conv_bwd": (c_int32, [POINTER(SqConvCfg), _R, _P, _P, _P, _R, _P, _R, _P, _P, _P, _P, c_size_t, _P]),
+    "sq_conv_step": (c_int32, [POINTER(SqConvCfg), _R, _P, _P, _P, c_int64, _P, _R, _P]),
+    "sq_ssm_scan_bytes": (c_int32, [POINTER(SqSsmCfg), c_int32, POINTER(c_size_t)]),
+    "sq_ssm_scan": (c_int32, [POINTER(SqSsmCfg), POINTER(SqSsmIn), _P, _R, _P, _P, c_size_t, _P]),
+    "sq_ssm_scan_bwd": (c_int32, [POINTER(SqSsmCfg), POINTER(SqSsmIn), _P, _R, _P, POINTER(SqSsmGrads), _P, _P, c_size_t, _P]),
+    "sq_ssm_step": (c_int32, [POINTER(SqSsmCfg), POINTER(SqSsmIn), _P, c_int64, _P, _R, _P]),
+    "sq_cache_write": (c_int32, [POINTER(SqCacheCfg), _R, _P, _P, _P, _P]),
+    "sq_cache_read": (c_int32, [POINTER(SqCacheCfg), _P, _P, _P, _R, _P]),
     "sq_status_str": (ctypes.c_char_p, [c_int32]),
     "sq_last_error": (ctypes.c_char_p, []),
     "sq_supported_shapes": (c_int32, [POINTER(c_int32), c_int32]),

@@ -16,7 +16,8 @@ OUT = os.path.join(HERE, "libstepq.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 ARCH = os.environ.get("STEPQ_ARCH", "gfx950")
 
-SOURCES = ["api.cpp", "ops_api.cpp", "planner.cpp", "kernels.hip", "probe.hip", "norm.hip", "scan.hip", "scan_prep.hip", "scan_bwd.hip"]
+SOURCES = ["api.cpp", "ops_api.cpp", "mix_api.cpp", "planner.cpp", "kernels.hip", "probe.hip", "norm.hip", "scan.hip", "scan_prep.hip",
+           "scan_bwd.hip", "conv.hip", "ssm.hip", "ssm_bwd.hip", "cache.hip"]
 
 
 def _hipcc() -> str:
@@ -36,9 +37,9 @@ def build(verbose: bool = False) -> str:
     # v_max/v_min instead of being preceded by canonicalizing copies of their operands
     device = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
     step = ["-munsafe-fp-atomics", "-mno-amdgpu-ieee", "-fno-honor-nans"]
-    # the norms and the scan take NaN and infinities as inputs like others (the norms give what their formulas give, the scan
-    # what include/stepq.h says), so they are compiled without the assumption that there are none
-    ieee = {"norm.hip", "scan.hip", "scan_prep.hip", "scan_bwd.hip"}
+    # the norms, the scans, the convolution and the cache take NaN and infinities as inputs like others (and give what include/stepq.h
+    # says), so they are compiled without the assumption that there are none
+    ieee = {"norm.hip", "scan.hip", "scan_prep.hip", "scan_bwd.hip", "conv.hip", "ssm.hip", "ssm_bwd.hip", "cache.hip"}
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD_DIR, src.replace(".", "_") + ".o")

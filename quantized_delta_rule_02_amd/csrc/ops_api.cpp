@@ -4,20 +4,11 @@
 
 #include <cmath>
 
-#include "host.h"
+#include "checks.h"
 #include "norm.h"
 #include "scan.h"
 
 using namespace sq;
-
-static sq_status fail_hip(hipError_t e, const char* what) {
-    set_error("%s: %s", what, hipGetErrorString(e));
-    return SQ_ERR_HIP;
-}
-
-static bool dtype_ok(int32_t dt) { return dt == SQ_DTYPE_F32 || dt == SQ_DTYPE_BF16 || dt == SQ_DTYPE_F16; }
-static int64_t esize(int32_t dt) { return dt == SQ_DTYPE_F32 ? 4 : 2; }
-static bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 
 // ------------------------------------------------------------------ scan
 
@@ -100,19 +91,7 @@ sq_status check_rows(const sq_rows* a, const char* name, int64_t heads, int64_t 
     return SQ_OK;
 }
 
-sq_status check_f32(const float* a, const char* name, uintptr_t to) {
-    if (!a) { set_error("%s is NULL", name); return SQ_ERR_ARG; }
-    if (!aligned(a, to)) { set_error("%s must be aligned to %u bytes", name, unsigned(to)); return SQ_ERR_ARG; }
-    return SQ_OK;
-}
-
 sq_status check_states(const float* a, const char* name) { return a ? check_f32(a, name, 4) : SQ_OK; }
-
-sq_status check_work(const void* work, size_t bytes, size_t need) {
-    if (bytes < need) { set_error("workspace of %zu bytes, the call needs %zu", bytes, need); return SQ_ERR_SHAPE; }
-    if (need && (!work || !aligned(work, 256))) { set_error("workspace NULL or not 256-byte aligned"); return SQ_ERR_ARG; }
-    return SQ_OK;
-}
 
 ScanRows rows_of(const sq_rows* a) { return a ? ScanRows{a->d_ptr, a->stride} : ScanRows{nullptr, 0}; }
 
@@ -135,8 +114,6 @@ ScanParams scan_params(const sq_scan_cfg& c, const ScanWork& w, void* work, bool
 }
 
 }  // namespace
-
-#define SQ_TRY(x) do { const sq_status st_ = (x); if (st_ != SQ_OK) return st_; } while (0)
 
 extern "C" sq_status sq_delta_scan_bytes(const sq_scan_cfg* cfg, int32_t backward, size_t* bytes) {
     if (!bytes) { set_error("bytes is NULL"); return SQ_ERR_ARG; }

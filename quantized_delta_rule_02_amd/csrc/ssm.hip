@@ -1,0 +1,287 @@
+// Selective state space scan over packed sequences: a gate for every channel and state (gfx950).
+//
+//   delta = softplus(dt + bias),  h_t = exp(delta_t a) h_{t-1} + delta_t u_t B_t,  p_t = C_t . h_t + d u_t,  y_t = p_t silu(z_t)
+//
+// There is no matrix product in it: the decay differs from state to state of every channel.  What bounds it is the vector unit,
+// one exponential (a quarter of the rate) and five operations for every token, channel and state.  Four states a lane: a channel
+// of 16 states is four lanes, so one sequence of 4096 channels is 256 waves.  A workgroup's tile of tokens is prepared in LDS,
+// every step (softplus) and product delta u once; B and C are read from there by all lanes, and y, complete after a sum over a
+// channel's lanes, goes back through LDS so that gate and stores are made in rows.
+//
+// Few and long sequences leave most of the GPU idle that way, so they are cut into segments that run side by side: each from a
+// state of zero (k_ssm with LOCAL: the state after it, and the sum of its steps, whose exponential is the product of its
+// decays), then the states before the segments one after another (k_ssm_join), then each segment with its outputs.
+#include <hip/hip_runtime.h>
+
+#include "ssm_dev.h"
+
+namespace sq {
+
+template <int DT, int N, bool VEC, bool LOCAL>
+__global__ void __launch_bounds__(kSsmThreads) k_ssm(const SsmParams p, int n_blocks) {
+    using L = SsmLane<N>;
+    constexpr int TT = 32, CB = L::kBlockCh, NV = CB / 4, kItems = (TT * NV + kSsmThreads - 1) / kSsmThreads;
+    constexpr int kRows = LOCAL ? 1 : 2, kBc = (TT * kRows * (N / 4) + kSsmThreads - 1) / kSsmThreads;
+    __shared__ float2 s_d[TT][CB];                        // delta, delta u
+    __shared__ float s_y[LOCAL ? 1 : TT][CB];
+    __shared__ f32x4 s_bc[kRows][TT][N / 4];
+    const int tid = (int)threadIdx.x, blk = (int)blockIdx.x % n_blocks;
+    const int64_t slot = (int)blockIdx.x / n_blocks;
+    const bool seg = p.runs.log >= 0;
+    int seq, len;
+    int64_t tok0;
+    if (seg) {
+        const RunAt r = run_of_slot(p.runs, slot);
+        if (r.n == 0) return;
+        seq = r.seq; len = r.n; tok0 = r.tok0;
+    } else {
+        const Span q = span_of(p.runs, (int)slot);
+        seq = (int)slot; len = (int)q.len; tok0 = q.start;
+    }
+    const SsmBlock bc = block_channels(p, blk, CB);
+    const int ch = tid / L::kPer, quarter = tid % L::kPer;            // the lane's channel of the block, its four states
+    const bool there = ch < bc.n;
+    const int64_t at = ((int64_t)bc.c0 + ch) * N + 4 * quarter;
+    const int64_t states = (int64_t)p.channels * N;
+    f32x4 a2 = load_states(p.a, at, there), h{0.f, 0.f, 0.f, 0.f};
+    if constexpr (!LOCAL) {
+        if (seg) h = load_states(p.hseg, slot * states + at, there);
+        else if (p.s0) h = load_states(p.s0, seq * states + at, there);
+    }
+    float dsum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a2[j] *= kLog2e;
+    // staging: item i of a thread is four channels of one token
+    Four<DT, VEC> ru[kItems], rd[kItems], rbc[kBc];
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int e = i * kSsmThreads + tid, t = t0 + e / NV, c = e % NV * 4;
+            const int n = e < TT * NV && t < len ? bc.n - c : 0;
+            ru[i].load(p.u.p, (tok0 + t) * p.u.stride + bc.c0 + c, n);
+            rd[i].load(p.dt.p, (tok0 + t) * p.dt.stride + bc.c0 + c, n);
+        }
+#pragma unroll
+        for (int i = 0; i < kBc; ++i) {
+            const int e = i * kSsmThreads + tid, k = e % (N / 4), t = t0 + e / (N / 4) % TT, w = e / (N / 4 * TT);
+            const int n = w < kRows && t < len ? 4 : 0;
+            const Rows& r = w ? p.c : p.b;
+            rbc[i].load(r.p, (tok0 + t) * r.stride + bc.group * N + 4 * k, n);
+        }
+    };
+    fetch(0);
+    for (int t0 = 0; t0 < len; t0 += TT) {
+        const int nt = len - t0 < TT ? len - t0 : TT;
+        Four<DT, VEC> cu[kItems], cz[LOCAL ? 1 : kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int e = i * kSsmThreads + tid, t = e / NV, c = e % NV * 4;
+            cu[i] = ru[i];
+            if (e < TT * NV && t < nt) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float bias = p.dt_bias && c + j < bc.n ? p.dt_bias[bc.c0 + c + j] : 0.f;
+                    float x = rd[i].at(j) + bias;
+                    x = p.softplus ? softplus(x) : x;
+                    s_d[t][c + j] = float2{x, x * ru[i].at(j)};
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBc; ++i) {
+            const int e = i * kSsmThreads + tid, k = e % (N / 4), t = e / (N / 4) % TT, w = e / (N / 4 * TT);
+            f32x4 x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = rbc[i].at(j);
+            if (w < kRows) s_bc[w][t][k] = x;
+        }
+        __syncthreads();
+        if (t0 + TT < len) fetch(t0 + TT);
+        if constexpr (!LOCAL) {
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int e = i * kSsmThreads + tid, t = e / NV, c = e % NV * 4;
+                cz[i].load(p.z.p, (tok0 + t0 + t) * p.z.stride + bc.c0 + c, p.z.p && e < TT * NV && t < nt ? bc.n - c : 0);
+            }
+        }
+        auto step = [&](int t) {
+            const float2 d = s_d[t][ch];
+            const f32x4 b = s_bc[0][t][quarter];
+            f32x4 c;
+            if constexpr (!LOCAL) c = s_bc[kRows - 1][t][quarter];
+            float y = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = fmaf(__builtin_amdgcn_exp2f(d.x * a2[j]), h[j], d.y * b[j]);
+                if constexpr (!LOCAL) y = fmaf(h[j], c[j], y);
+            }
+            if constexpr (LOCAL) {
+                dsum += d.x;
+            } else {
+                y = channel_sum<L::kPer>(y);
+                if (quarter == 0) s_y[t][ch] = y;
+            }
+        };
+        int t = 0;
+        for (; t + 4 <= nt; t += 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) step(t + k);
+        }
+        for (; t < nt; ++t) step(t);
+        __syncthreads();
+        if constexpr (!LOCAL) {
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int e = i * kSsmThreads + tid, t = e / NV, c = e % NV * 4;
+                if (e >= TT * NV || t >= nt) continue;
+                float y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float d = p.d && c + j < bc.n ? p.d[bc.c0 + c + j] : 0.f;
+                    y[j] = s_y[t][c + j];
+                    if (p.d) y[j] = fmaf(d, cu[i].at(j), y[j]);
+                    if (p.z.p) {
+                        const float z = cz[i].at(j);
+                        y[j] *= z * sigmoid<DT == SQ_DTYPE_F32>(z);
+                    }
+                }
+                Four<DT, VEC>::store(p.y.p, (tok0 + t0 + t) * p.y.stride + bc.c0 + c, bc.n - c, y);
+            }
+        }
+    }
+    if (!there) return;
+    if constexpr (LOCAL) {
+        *reinterpret_cast<f32x4*>(p.hseg + slot * states + at) = h;
+        if (quarter == 0) p.dsum[slot * p.channels + bc.c0 + ch] = dsum;
+    } else if (!seg && p.s1) {
+        *reinterpret_cast<f32x4*>(p.s1 + seq * states + at) = h;
+    }
+}
+
+// The states before a sequence's segments, one after another (blockIdx.y of 1: the gradients of the states after them,
+// from the last to the first): h <- exp(a sum of steps) h + what the segment makes from zero.  Four states a thread; the
+// loads of eight segments are in flight together.
+__global__ void __launch_bounds__(256) k_ssm_join(const SsmParams p, int n_blocks) {
+    const int blk = (int)blockIdx.x % n_blocks, seq = (int)blockIdx.x / n_blocks;
+    const bool rev = blockIdx.y != 0;
+    const int64_t states = (int64_t)p.channels * p.d_state, at = ((int64_t)blk * 256 + (int)threadIdx.x) * 4;
+    if (at >= states) return;
+    const int64_t c = at / p.d_state;
+    const Span q = span_of(p.runs, seq);
+    const int64_t slot0 = run_slot0(p.runs, q, seq), n = (q.len + (int64_t(1) << p.runs.log) - 1) >> p.runs.log;
+    const float* first = rev ? p.ds1 : p.s0;
+    float* last = rev ? p.ds0 : p.s1;
+    float* w = (rev ? p.kseg : p.hseg) + at;
+    f32x4 h = load_states(first, seq * states + at, first != nullptr), a2 = load_states(p.a, at, true);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a2[j] *= kLog2e;
+    constexpr int K = 8;
+    for (int64_t i0 = 0; i0 < n; i0 += K) {
+        f32x4 x[K];
+        float ds[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t s = slot0 + (rev ? n - 1 - (i0 + k) : i0 + k);
+            if (i0 + k < n) {
+                x[k] = *reinterpret_cast<const f32x4*>(w + s * states);
+                ds[k] = p.dsum[s * p.channels + c];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t s = slot0 + (rev ? n - 1 - (i0 + k) : i0 + k);
+            if (i0 + k >= n) break;
+            *reinterpret_cast<f32x4*>(w + s * states) = h;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(ds[k] * a2[j]), h[j], x[k][j]);
+        }
+    }
+    if (last) *reinterpret_cast<f32x4*>(last + seq * states + at) = h;
+}
+
+// One token of each request, the state in a slot of the pool: bound by reading and writing the states.
+template <int DT, int N, bool VEC>
+__global__ void __launch_bounds__(kSsmThreads) k_ssm_step(const SsmParams p, int n_blocks) {
+    using L = SsmLane<N>;
+    const int tid = (int)threadIdx.x, blk = (int)blockIdx.x % n_blocks;
+    const int64_t r = (int)blockIdx.x / n_blocks;
+    const int64_t slot = p.slots ? (int64_t)p.slots[r] : r;
+    const SsmBlock bc = block_channels(p, blk, L::kBlockCh);
+    const int ch = tid / L::kPer, quarter = tid % L::kPer;
+    if (slot < 0 || slot >= p.n_slots || ch >= bc.n) return;
+    const int64_t c = bc.c0 + ch;
+    float* state = p.state + (slot * p.channels + c) * N + 4 * quarter;
+    f32x4 h = *reinterpret_cast<const f32x4*>(state);
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p.a + c * N + 4 * quarter);
+    Elems<DT, 1> eu, ed, ez;
+    Four<DT, VEC> eb, ec;
+    eu.load(p.u.p, r * p.u.stride + c);
+    ed.load(p.dt.p, r * p.dt.stride + c);
+    if (p.z.p) ez.load(p.z.p, r * p.z.stride + c);
+    eb.load(p.b.p, r * p.b.stride + bc.group * N + 4 * quarter, 4);
+    ec.load(p.c.p, r * p.c.stride + bc.group * N + 4 * quarter, 4);
+    float delta = ed.at(0) + (p.dt_bias ? p.dt_bias[c] : 0.f);
+    if (p.softplus) delta = softplus(delta);
+    const float du = delta * eu.at(0);
+    float y = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        h[j] = fmaf(__builtin_amdgcn_exp2f(delta * (a[j] * kLog2e)), h[j], du * eb.at(j));
+        y = fmaf(h[j], ec.at(j), y);
+    }
+    *reinterpret_cast<f32x4*>(state) = h;
+    y = channel_sum<L::kPer>(y);
+    if (quarter != 0) return;
+    if (p.d) y = fmaf(p.d[c], eu.at(0), y);
+    if (p.z.p) {
+        const float z = ez.at(0);
+        y *= z * sigmoid<DT == SQ_DTYPE_F32>(z);
+    }
+    Elems<DT, 1> o;
+    o.set(&y);
+    o.store(p.y.p, r * p.y.stride + c);
+}
+
+// ------------------------------------------------------------------ launches
+
+int ssm_segment_log(int64_t n_tokens, int64_t n_seq, int64_t blocks, bool backward) {
+    if (backward) return 6;
+    if (n_seq < 1 || n_tokens / n_seq < 128 || n_seq * blocks >= 1024) return -1;
+    int log = 6;
+    while (log < 12 && (n_tokens >> (log + 1)) * blocks >= 2048) ++log;
+    return log;
+}
+
+hipError_t launch_ssm_join(const SsmParams& p, int directions, hipStream_t s) {
+    const int jb = (int)(((int64_t)p.channels * p.d_state + 1023) / 1024);
+    k_ssm_join<<<dim3((unsigned)((int64_t)p.runs.n_seq * jb), (unsigned)directions), 256, 0, s>>>(p, jb);
+    return hipGetLastError();
+}
+
+template <int DT, int N, bool VEC>
+static hipError_t scan_n(const SsmParams& p, hipStream_t s) {
+    const int blocks = (int)ssm_blocks(p.channels, p.n_groups, N);
+    if (p.runs.log < 0) {
+        k_ssm<DT, N, VEC, false><<<dim3((unsigned)((int64_t)p.runs.n_seq * blocks)), kSsmThreads, 0, s>>>(p, blocks);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)(run_slots(p.runs.n_tokens, p.runs.n_seq, p.runs.log) * blocks));
+    k_ssm<DT, N, VEC, true><<<grid, kSsmThreads, 0, s>>>(p, blocks);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    e = launch_ssm_join(p, 1, s);
+    if (e != hipSuccess) return e;
+    k_ssm<DT, N, VEC, false><<<grid, kSsmThreads, 0, s>>>(p, blocks);
+    return hipGetLastError();
+}
+template <int DT, int N, bool VEC>
+static hipError_t step_n(const SsmParams& p, hipStream_t s) {
+    const int blocks = (int)ssm_blocks(p.channels, p.n_groups, N);
+    k_ssm_step<DT, N, VEC><<<dim3((unsigned)(p.batch * blocks)), kSsmThreads, 0, s>>>(p, blocks);
+    return hipGetLastError();
+}
+
+hipError_t launch_ssm(const SsmParams& p, bool vec, hipStream_t s) { SQ_SSM_DISPATCH(scan_n, p, s); }
+hipError_t launch_ssm_step(const SsmParams& p, bool vec, hipStream_t s) { SQ_SSM_DISPATCH(step_n, p, s); }
+
+}  // namespace sq
