@@ -185,7 +185,7 @@ extern "C" sq_status sq_conv_step(const sq_conv_cfg* cfg, const sq_rows* x, cons
 namespace {
 
 struct SsmWork {                     // byte offsets of the workspace's parts
-    size_t hseg, kseg, dsum, da, dd, bc, total;
+    size_t hseg, kseg, dsum, htile, dtile, da, dd, bc, total;
 };
 
 int64_t ssm_fwd_blocks(const sq_ssm_cfg& c) { return ssm_blocks(c.channels, c.n_groups, c.d_state); }
@@ -200,6 +200,8 @@ SsmWork ssm_work(const sq_ssm_cfg& c, bool backward, int log) {
         w.dsum = take(slots * size_t(c.channels) * 4);
         if (backward) {
             w.kseg = take(states);
+            w.htile = take((states << log) / kSsmTile);
+            w.dtile = take(((slots << log) / kSsmTile) * size_t(c.channels) * 4);
             w.da = take(states);
             w.dd = take(slots * 2 * size_t(c.channels) * 4);
             w.bc = take(size_t(ssm_grad_blocks(c.channels, c.n_groups, c.d_state)) * size_t(c.n_tokens) * 2 * size_t(c.d_state) * 4);
@@ -256,14 +258,14 @@ sq_status take_inputs(const sq_ssm_cfg& c, SsmParams& p, RowCheck& ck, const sq_
     return SQ_OK;
 }
 
-int ssm_forward_log(const sq_ssm_cfg& c) { return ssm_segment_log(c.n_tokens, c.n_seq, ssm_fwd_blocks(c), false); }
+int ssm_log(const sq_ssm_cfg& c, bool backward) { return ssm_segment_log(c.n_tokens, c.n_seq, ssm_fwd_blocks(c), backward); }
 
 }  // namespace
 
 extern "C" sq_status sq_ssm_scan_bytes(const sq_ssm_cfg* cfg, int32_t backward, size_t* bytes) {
     if (!bytes) { set_error("bytes is NULL"); return SQ_ERR_ARG; }
     SQ_TRY(check_ssm_cfg(cfg));
-    *bytes = ssm_work(*cfg, backward != 0, backward ? ssm_segment_log(0, 0, 0, true) : ssm_forward_log(*cfg)).total;
+    *bytes = ssm_work(*cfg, backward != 0, ssm_log(*cfg, backward != 0)).total;
     return SQ_OK;
 }
 
@@ -272,7 +274,7 @@ extern "C" sq_status sq_ssm_scan(const sq_ssm_cfg* cfg, const sq_ssm_in* in, con
     SQ_TRY(check_ssm_cfg(cfg));
     if (cfg->n_seq == 0) return SQ_OK;
     SQ_TRY(check_start(cfg->n_seq, cfg->d_seq_start));
-    const int log = ssm_forward_log(*cfg);
+    const int log = ssm_log(*cfg, false);
     SsmParams p = ssm_params(*cfg, log);
     RowCheck ck{cfg->dtype, cfg->n_tokens, 4};
     p.y = ck(y, "y", cfg->channels, cfg->n_tokens > 0);
@@ -297,7 +299,7 @@ extern "C" sq_status sq_ssm_scan_bwd(const sq_ssm_cfg* cfg, const sq_ssm_in* in,
     SQ_TRY(check_ssm_cfg(cfg));
     SQ_TRY(check_start(cfg->n_seq, cfg->d_seq_start));
     if (!out) { set_error("gradients are NULL"); return SQ_ERR_ARG; }
-    const int log = ssm_segment_log(0, 0, 0, true);
+    const int log = ssm_log(*cfg, true);
     const bool rows = cfg->n_tokens > 0 && cfg->n_seq > 0;
     SsmParams p = ssm_params(*cfg, log);
     RowCheck ck{cfg->dtype, cfg->n_tokens, 4};
@@ -321,7 +323,7 @@ extern "C" sq_status sq_ssm_scan_bwd(const sq_ssm_cfg* cfg, const sq_ssm_in* in,
     const SsmWork w = ssm_work(*cfg, true, log);
     SQ_TRY(check_work(d_work, work_bytes, w.total));
     auto f32 = [d_work](size_t o) { return reinterpret_cast<float*>(static_cast<char*>(d_work) + o); };
-    p.hseg = f32(w.hseg); p.kseg = f32(w.kseg); p.dsum = f32(w.dsum); p.da_part = f32(w.da); p.dd_part = f32(w.dd); p.bc_part = f32(w.bc);
+    p.hseg = f32(w.hseg); p.kseg = f32(w.kseg); p.dsum = f32(w.dsum); p.htile = f32(w.htile); p.dtile = f32(w.dtile); p.da_part = f32(w.da); p.dd_part = f32(w.dd); p.bc_part = f32(w.bc);
     p.s0 = d_s0; p.ds1 = d_ds1; p.ds0 = d_ds0;
     p.da = out->d_da; p.dd = out->d_dd; p.ddt_bias = out->d_ddt_bias;
     const hipError_t e = launch_ssm_bwd(p, ck.vec, static_cast<hipStream_t>(stream));

@@ -17,6 +17,8 @@ struct SsmParams {
     float* hseg;                     // [slot][channels][d_state] state after the segment from zero, then the state before it
     float* kseg;                     // backward: the same of the state's gradient, in the other direction
     float* dsum;                     // [slot][channels] sum of the steps
+    float* htile;                    // backward: [slot][tokens / 8][channels][d_state] state before every 8th token, from zero
+    float* dtile;                    // [slot][tokens / 8][channels] sum of the steps up to there
     // backward
     Rows dy, du, ddt, db, dc, dz;
     const float* ds1;
@@ -34,6 +36,7 @@ struct SsmParams {
 };
 
 constexpr int kSsmWaves = 4;         // of a workgroup
+constexpr int kSsmTile = 8;          // tokens whose decays a lane of the gradients' main kernel holds in registers
 // Channels of a workgroup: a lane holds four states of one channel.
 inline int ssm_block_channels(int d_state) { return kSsmWaves * 256 / d_state; }
 // Workgroups' blocks of channels; none holds channels of two groups.

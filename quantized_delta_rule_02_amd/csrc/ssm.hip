@@ -22,8 +22,8 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm(const SsmParams p, int n_bl
     using L = SsmLane<N>;
     constexpr int TT = 32, CB = L::kBlockCh, NV = CB / 4, kItems = (TT * NV + kSsmThreads - 1) / kSsmThreads;
     constexpr int kRows = LOCAL ? 1 : 2, kBc = (TT * kRows * (N / 4) + kSsmThreads - 1) / kSsmThreads;
-    __shared__ float2 s_d[TT][CB];                        // delta, delta u
-    __shared__ float s_y[LOCAL ? 1 : TT][CB];
+    __shared__ __attribute__((aligned(16))) float2 s_d[TT][CB];           // delta, delta u
+    __shared__ __attribute__((aligned(16))) float s_y[LOCAL ? 1 : TT][CB + L::kWaveCh];     // rows apart so that four tokens of a wave meet no bank twice
     __shared__ f32x4 s_bc[kRows][TT][N / 4];
     const int tid = (int)threadIdx.x, blk = (int)blockIdx.x % n_blocks;
     const int64_t slot = (int)blockIdx.x / n_blocks;
@@ -51,15 +51,23 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm(const SsmParams p, int n_bl
     float dsum = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) a2[j] *= kLog2e;
-    // staging: item i of a thread is four channels of one token
+    // staging: item i of a thread is four channels of one token, the same channels for all its items
+    static_assert(kSsmThreads % NV == 0, "a thread's items have one column");
+    const int c4 = tid % NV * 4;
+    float bias[4], dw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        bias[j] = p.dt_bias && c4 + j < bc.n ? p.dt_bias[bc.c0 + c4 + j] : 0.f;
+        dw[j] = !LOCAL && p.d && c4 + j < bc.n ? p.d[bc.c0 + c4 + j] : 0.f;
+    }
     Four<DT, VEC> ru[kItems], rd[kItems], rbc[kBc];
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int e = i * kSsmThreads + tid, t = t0 + e / NV, c = e % NV * 4;
-            const int n = e < TT * NV && t < len ? bc.n - c : 0;
-            ru[i].load(p.u.p, (tok0 + t) * p.u.stride + bc.c0 + c, n);
-            rd[i].load(p.dt.p, (tok0 + t) * p.dt.stride + bc.c0 + c, n);
+            const int e = i * kSsmThreads + tid, t = t0 + e / NV;
+            const int n = e < TT * NV && t < len ? bc.n - c4 : 0;
+            ru[i].load(p.u.p, (tok0 + t) * p.u.stride + bc.c0 + c4, n);
+            rd[i].load(p.dt.p, (tok0 + t) * p.dt.stride + bc.c0 + c4, n);
         }
 #pragma unroll
         for (int i = 0; i < kBc; ++i) {
@@ -75,16 +83,19 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm(const SsmParams p, int n_bl
         Four<DT, VEC> cu[kItems], cz[LOCAL ? 1 : kItems];
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int e = i * kSsmThreads + tid, t = e / NV, c = e % NV * 4;
+            const int e = i * kSsmThreads + tid, t = e / NV;
             cu[i] = ru[i];
             if (e < TT * NV && t < nt) {
+                float x[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float bias = p.dt_bias && c + j < bc.n ? p.dt_bias[bc.c0 + c + j] : 0.f;
-                    float x = rd[i].at(j) + bias;
-                    x = p.softplus ? softplus(x) : x;
-                    s_d[t][c + j] = float2{x, x * ru[i].at(j)};
+                for (int j = 0; j < 4; ++j) x[j] = rd[i].at(j) + bias[j];
+                if (p.softplus) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = softplus(x[j]).value;
                 }
+#pragma unroll
+                for (int j = 0; j < 4; j += 2)
+                    *reinterpret_cast<f32x4*>(&s_d[t][c4 + j]) = f32x4{x[j], x[j] * ru[i].at(j), x[j + 1], x[j + 1] * ru[i].at(j + 1)};
             }
         }
 #pragma unroll
@@ -100,52 +111,66 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm(const SsmParams p, int n_bl
         if constexpr (!LOCAL) {
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int e = i * kSsmThreads + tid, t = e / NV, c = e % NV * 4;
-                cz[i].load(p.z.p, (tok0 + t0 + t) * p.z.stride + bc.c0 + c, p.z.p && e < TT * NV && t < nt ? bc.n - c : 0);
+                const int e = i * kSsmThreads + tid, t = e / NV;
+                cz[i].load(p.z.p, (tok0 + t0 + t) * p.z.stride + bc.c0 + c4, p.z.p && e < TT * NV && t < nt ? bc.n - c4 : 0);
             }
         }
-        auto step = [&](int t) {
-            const float2 d = s_d[t][ch];
-            const f32x4 b = s_bc[0][t][quarter];
-            f32x4 c;
-            if constexpr (!LOCAL) c = s_bc[kRows - 1][t][quarter];
+        auto step = [&](const float2& d, const f32x4& b, const f32x4& c) {
             float y = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 h[j] = fmaf(__builtin_amdgcn_exp2f(d.x * a2[j]), h[j], d.y * b[j]);
                 if constexpr (!LOCAL) y = fmaf(h[j], c[j], y);
             }
-            if constexpr (LOCAL) {
-                dsum += d.x;
-            } else {
-                y = channel_sum<L::kPer>(y);
-                if (quarter == 0) s_y[t][ch] = y;
-            }
+            if constexpr (LOCAL) dsum += d.x;
+            return y;
         };
         int t = 0;
         for (; t + 4 <= nt; t += 4) {
+            float2 d[4];
+            f32x4 b[4], c[4];
+            float y[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) step(t + k);
+            for (int k = 0; k < 4; ++k) {
+                d[k] = s_d[t + k][ch];
+                b[k] = s_bc[0][t + k][quarter];
+                if constexpr (!LOCAL) c[k] = s_bc[kRows - 1][t + k][quarter];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = step(d[k], b[k], c[k]);
+            if constexpr (!LOCAL) {
+                channel_sums4<L::kPer>(y);
+                put_sums4<L::kPer>(y, quarter, [&](int k, float v) { s_y[t + k][ch] = v; });
+            }
         }
-        for (; t < nt; ++t) step(t);
+        for (; t < nt; ++t) {
+            f32x4 c{0.f, 0.f, 0.f, 0.f};
+            if constexpr (!LOCAL) c = s_bc[kRows - 1][t][quarter];
+            float y = step(s_d[t][ch], s_bc[0][t][quarter], c);
+            if constexpr (!LOCAL) {
+                y = channel_sum<L::kPer>(y);
+                if (quarter == 0) s_y[t][ch] = y;
+            }
+        }
         __syncthreads();
         if constexpr (!LOCAL) {
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int e = i * kSsmThreads + tid, t = e / NV, c = e % NV * 4;
+                const int e = i * kSsmThreads + tid, t = e / NV;
                 if (e >= TT * NV || t >= nt) continue;
+                const f32x4 sum = *reinterpret_cast<const f32x4*>(&s_y[t][c4]);
                 float y[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float d = p.d && c + j < bc.n ? p.d[bc.c0 + c + j] : 0.f;
-                    y[j] = s_y[t][c + j];
-                    if (p.d) y[j] = fmaf(d, cu[i].at(j), y[j]);
-                    if (p.z.p) {
-                        const float z = cz[i].at(j);
-                        y[j] *= z * sigmoid<DT == SQ_DTYPE_F32>(z);
-                    }
+                for (int j = 0; j < 4; ++j) y[j] = sum[j];
+                if (p.d) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = fmaf(dw[j], cu[i].at(j), y[j]);
                 }
-                Four<DT, VEC>::store(p.y.p, (tok0 + t0 + t) * p.y.stride + bc.c0 + c, bc.n - c, y);
+                if (p.z.p) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] *= cz[i].at(j) * sigmoid<DT == SQ_DTYPE_F32>(cz[i].at(j));
+                }
+                Four<DT, VEC>::store(p.y.p, (tok0 + t0 + t) * p.y.stride + bc.c0 + c4, bc.n - c4, y);
             }
         }
     }
@@ -221,7 +246,7 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm_step(const SsmParams p, int
     eb.load(p.b.p, r * p.b.stride + bc.group * N + 4 * quarter, 4);
     ec.load(p.c.p, r * p.c.stride + bc.group * N + 4 * quarter, 4);
     float delta = ed.at(0) + (p.dt_bias ? p.dt_bias[c] : 0.f);
-    if (p.softplus) delta = softplus(delta);
+    if (p.softplus) delta = softplus(delta).value;
     const float du = delta * eu.at(0);
     float y = 0.f;
 #pragma unroll
@@ -245,8 +270,8 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm_step(const SsmParams p, int
 // ------------------------------------------------------------------ launches
 
 int ssm_segment_log(int64_t n_tokens, int64_t n_seq, int64_t blocks, bool backward) {
-    if (backward) return 6;
-    if (n_seq < 1 || n_tokens / n_seq < 128 || n_seq * blocks >= 1024) return -1;
+    if (backward) return (n_tokens >> 7) * blocks >= 2048 ? 7 : 6;
+    if (n_seq < 1 || n_tokens / n_seq < 128 || n_seq * blocks >= 224) return -1;
     int log = 6;
     while (log < 12 && (n_tokens >> (log + 1)) * blocks >= 2048) ++log;
     return log;

@@ -20,21 +20,32 @@ struct SsmLane {
     static constexpr int kBlockCh = kSsmWaves * kWaveCh;
 };
 
-// ln(1 + e^x) = max(x, 0) + ln(1 + w), w = e^-|x|, by the series of the inverse hyperbolic tangent:
-// ln(1 + w) = 2 artanh(v) = 2 v (1 + v^2 / 3 + v^4 / 5 + ...), v = w / (2 + w) <= 1 / 3.  The first term left out, v^16 / 17, is
-// below 2^-29; small w keep their digits, which a logarithm of the rounded 1 + w would lose.
-__device__ __forceinline__ float softplus(float x) {
-    const float w = exp_minus<true>(fabsf(x));
-    const float v = w * __builtin_amdgcn_rcpf(2.f + w), q = v * v;
-    float s = 1.f / 15.f;
-    s = fmaf(s, q, 1.f / 13.f);
-    s = fmaf(s, q, 1.f / 11.f);
-    s = fmaf(s, q, 1.f / 9.f);
-    s = fmaf(s, q, 1.f / 7.f);
-    s = fmaf(s, q, 1.f / 5.f);
-    s = fmaf(s, q, 1.f / 3.f);
-    s = fmaf(s, q, 1.f);
-    return fmaf(2.f * v, s, x > 0.f ? x : x <= 0.f ? 0.f : x);
+// ln(1 + e^x) = max(x, 0) + ln(1 + w), w = e^-|x|.  w comes from 2^y with the rounding of y = -|x| log2(e) put back (|x| + y ln 2 is
+// exact but for ln 2's own rounding, 2^-28); beyond 150 it is below every float32 (min drops a NaN there, the last line brings it
+// back).  ln(1 + w) = w P(w) with the polynomial of degree 8 that has the least relative error on [0, 1], 2^-25 (by Remez exchange),
+// so that small w keep their digits, which a logarithm of the rounded 1 + w would lose.
+struct SoftPlus {
+    float w, value;
+};
+__device__ __forceinline__ SoftPlus softplus(float x) {
+    const float m = fminf(fabsf(x), 150.f), y = -m * kLog2e;
+    float w = __builtin_amdgcn_exp2f(y);
+    w = fmaf(w, fmaf(-y, 0.69314718056f, -m), w);
+    float s = 0.0052326940931379795f;
+    s = fmaf(s, w, -0.02950523979961872f);
+    s = fmaf(s, w, 0.07822595536708832f);
+    s = fmaf(s, w, -0.13663245737552643f);
+    s = fmaf(s, w, 0.19106006622314453f);
+    s = fmaf(s, w, -0.2484298199415207f);
+    s = fmaf(s, w, 0.3331909775733948f);
+    s = fmaf(s, w, -0.4999949336051941f);
+    s = fmaf(s, w, 0.9999999403953552f);
+    return SoftPlus{w, fmaf(w, s, x <= 0.f ? 0.f : x)};
+}
+// its derivative 1 / (1 + e^-x) from the same w
+__device__ __forceinline__ float softplus_slope(float x, float w) {
+    const float r = __builtin_amdgcn_rcpf(1.f + w);
+    return x <= 0.f ? w * r : r;
 }
 
 template <int CTRL>
@@ -42,6 +53,7 @@ __device__ __forceinline__ float dpp(float x) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
 }
 constexpr int kDppXor1 = 0xb1, kDppXor2 = 0x4e, kDppHalfMirror = 0x141, kDppMirror = 0x140, kDppRor4 = 0x124, kDppRor8 = 0x128;
+constexpr int kDppShl4 = 0x104, kDppShl8 = 0x108;      // lane i gets lane i + 4, i + 8 of its row of 16
 
 // a of lanes l and l ^ 32 (16) exchanged so that each sum of the two results is a sum over both: after it the lower half (even
 // rows) has a's sums and the upper half (odd rows) b's.
@@ -63,6 +75,41 @@ __device__ __forceinline__ float channel_sum(float x) {
     if constexpr (PER >= 16) x += dpp<kDppMirror>(x);
     if constexpr (PER >= 32) x = join16(x, x);
     return x;
+}
+
+// Sums over a channel's lanes of four tokens' values at a time: lane q < 4 of the channel gets token q's (PER = 2: lane q < 2 those of
+// tokens q and q + 2).  Each exchange sends the half of the tokens that the lane does not keep, so four sums take nine instructions
+// instead of the eight and four masked stores of one after another.  The order of the additions is channel_sum's.
+template <int PER>
+__device__ __forceinline__ void channel_sums4(float (&v)[4]) {
+    const int lane = (int)threadIdx.x;
+    const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {                        // tokens 2 k and 2 k + 1
+        const float keep = odd ? v[2 * k + 1] : v[2 * k], send = odd ? v[2 * k] : v[2 * k + 1];
+        v[2 * k] = keep + dpp<kDppXor1>(send);
+    }
+    if constexpr (PER >= 4) {
+        const float keep = high ? v[2] : v[0], send = high ? v[0] : v[2];
+        v[0] = keep + dpp<kDppXor2>(send);
+        // lanes q, q + 4, ... now hold the same token's sums of their quads
+        if constexpr (PER >= 8) v[0] += dpp<kDppShl4>(v[0]);
+        if constexpr (PER >= 16) v[0] += dpp<kDppShl8>(v[0]);
+        if constexpr (PER >= 32) v[0] = join16(v[0], v[0]);
+    }
+}
+
+// Where lane `quarter` of a channel puts what channel_sums4 left it: put(token, value).
+template <int PER, class Put>
+__device__ __forceinline__ void put_sums4(const float (&v)[4], int quarter, Put put) {
+    if constexpr (PER == 2) {
+        put(quarter, v[0]);
+        put(quarter + 2, v[2]);
+    } else if constexpr (PER == 4) {
+        put(quarter, v[0]);
+    } else {
+        if (quarter < 4) put(quarter, v[0]);
+    }
 }
 
 // Where block `blk` of a launch has its channels: the first one, and how many (none of two groups).

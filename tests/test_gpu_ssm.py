@@ -166,6 +166,36 @@ def test_segments(lens, C, N, dev):
     check(C, N, 1, lens, F32, dev, s0=False, seed=6)
 
 
+def test_long_and_short_segments_of_the_gradients(dev):
+    """A call that is large enough for segments of 128 tokens against its channels in four calls, whose segments have 64."""
+    C, N, lens, parts = 2048, 16, [5000, 1, 3300], 4
+    T = sum(lens)
+    rn = lambda *s: torch.randn(*s, device=dev, generator=gen)  # noqa: E731
+    gen = torch.Generator(device=dev).manual_seed(3)
+    u, dt, z, dy, b, c = rn(T, C), 0.5 * rn(T, C) - 3.0, rn(T, C), rn(T, C), rn(T, 1, N), rn(T, 1, N)
+    a, d = -(1.0 + torch.arange(N, device=dev)) * (1 + 0.1 * rn(C, N)).clamp(0.5, 2), rn(C)
+    s0, ds1, start = rn(3, C, N), rn(3, C, N), ref.starts(lens).to(dev)
+
+    def run(k):
+        at = lambda t: t[:, k].contiguous() if t.dim() < 3 else t[:, k].contiguous()  # noqa: E731
+        v = {n: at(t) for n, t in (("u", u), ("dt", dt), ("z", z), ("dy", dy))}
+        o = {n: torch.empty_like(t) for n, t in (("du", v["u"]), ("ddt", v["u"]), ("dz", v["u"]), ("da", a[k].contiguous()), ("db", b), ("dc", c),
+                                                ("dd", d[k].contiguous()), ("ds0", at(s0)))}
+        sq.sq_ssm_scan_bwd(v["u"], v["dt"], a[k].contiguous(), b, c, v["dy"], o["du"], o["ddt"], o["da"], o["db"], o["dc"], d=d[k].contiguous(), z=v["z"],
+                           dz=o["dz"], dd=o["dd"], seq_start=start, s0=at(s0), ds1=at(ds1), ds0=o["ds0"])
+        return o
+
+    whole = run(slice(0, C))
+    some = [run(slice(i * C // parts, (i + 1) * C // parts)) for i in range(parts)]
+    assert (T >> 7) * 32 >= 2048 > (T >> 7) * 8                # workgroups of segments of 128
+    rel = lambda x, y: float((x.double() - y.double()).norm() / y.double().norm())  # noqa: E731
+    # both are float32 sums of the same terms in other orders: a few roundings of 2^-24 for each of some hundred tokens that last
+    for n, dim in (("du", 1), ("ddt", 1), ("dz", 1), ("da", 0), ("dd", 0), ("ds0", 1)):
+        assert rel(whole[n], torch.cat([s[n] for s in some], dim)) < 300 * 2.0 ** -24, n
+    for n in ("db", "dc"):
+        assert rel(whole[n], sum(s[n].double() for s in some)) < 300 * 2.0 ** -24, n
+
+
 @pytest.mark.parametrize("N,C,G", ((8, 130, 1), (16, 72, 2), (64, 21, 1), (128, 16, 4)))
 @pytest.mark.parametrize("dtype", (F32, BF16, F16), ids=NAMES.get)
 def test_step(N, C, G, dtype, dev):
