@@ -9,6 +9,7 @@ constexpr int kConvMaxWidth = 8;
 struct ConvParams {
     Runs runs;
     int32_t channels, dtype, act, width;
+    int32_t once;                    // forward: y is written past the caches' usual order
     Rows x, y, dy, dx;
     const float* weight;             // [channels][width]
     const float* bias;               // [channels] or NULL
@@ -25,7 +26,7 @@ struct ConvParams {
     void* window;                    // [n_slots][width - 1][channels]
 };
 
-constexpr int kConvBwdLog = 6;       // tokens of a run of the backward pass: 64
+constexpr int kConvBwdLog = 6, kConvBwdRuns = 8;     // log2 of the tokens of a wave and of a workgroup of the backward pass
 int conv_run_log(int64_t n_tokens, int64_t n_seq, int32_t channels);    // of the forward pass
 // `vec`: every array allows the accesses of `vec` elements at a time (conv_vec) that the kernels make.
 int conv_vec(int32_t dtype);

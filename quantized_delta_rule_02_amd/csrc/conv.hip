@@ -9,17 +9,19 @@
 // after its reads), so that both may be the same array.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "conv.h"
 #include "elems.h"
 
 namespace sq {
 
-constexpr int kThreads = 256, kU = 4;          // threads of a workgroup; tokens whose loads are in flight together
+constexpr int kThreads = 256, kU = 8, kUb = 4;         // threads of a workgroup; tokens whose loads are in flight together (gradients)
 
 template <int DT, int W, int V>
 struct Filter {
     float w[V][W], b[V];
-    __device__ __forceinline__ void load(const ConvParams& p, int c) {
+    __device__ __forceinline__ void load(const ConvParams& p, uint32_t c) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
 #pragma unroll
@@ -31,41 +33,41 @@ struct Filter {
 
 // The last W - 1 inputs of a sequence: rows of x, or of s0 where the sequence is shorter.  All reads come before the writes.
 template <int DT, int W, int V>
-__device__ __forceinline__ void last_inputs(const ConvParams& p, const RunAt& r, int c) {
+__device__ __forceinline__ void last_inputs(const ConvParams& p, const RunAt& r, uint32_t c) {
     Elems<DT, V> e[W - 1];
     const int64_t s = (int64_t)r.seq * (W - 1);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         const int64_t at = r.len - (W - 1) + j;
-        if (at >= 0) e[j].load(p.x.p, (r.start + at) * p.x.stride + c);
-        else if (p.s0) e[j].load(p.s0, (s + at + W - 1) * p.channels + c);
+        if (at >= 0) e[j].load(p.x.p, (r.start + at) * p.x.stride, c);
+        else if (p.s0) e[j].load(p.s0, (s + at + W - 1) * p.channels, c);
         else e[j].zero();
     }
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) e[j].store(p.s1, (s + j) * p.channels + c);
+    for (int j = 0; j < W - 1; ++j) e[j].store(p.s1, (s + j) * p.channels, c);
 }
 
 // Inputs W - 1 .. 1 places before the run's first token.
 template <int DT, int W, int V>
-__device__ __forceinline__ void inputs_before(const ConvParams& p, const RunAt& r, int c, Elems<DT, V> (&e)[W - 1]) {
+__device__ __forceinline__ void inputs_before(const ConvParams& p, const RunAt& r, uint32_t c, Elems<DT, V> (&e)[W - 1]) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-        if (!r.first) e[j].load(p.x.p, (r.tok0 - (W - 1) + j) * p.x.stride + c);     // a run has at least W - 1 tokens before the next
-        else if (p.s0) e[j].load(p.s0, ((int64_t)r.seq * (W - 1) + j) * p.channels + c);
+        if (!r.first) e[j].load(p.x.p, (r.tok0 - (W - 1) + j) * p.x.stride, c);     // a run has at least W - 1 tokens before the next
+        else if (p.s0) e[j].load(p.s0, ((int64_t)r.seq * (W - 1) + j) * p.channels, c);
         else e[j].zero();
     }
 }
 
 template <int DT, int W, int V, bool SILU>
 __global__ void __launch_bounds__(kThreads) k_conv(const ConvParams p, int n_blocks) {
-    const int c = (((int)blockIdx.x % n_blocks) * kThreads + (int)threadIdx.x) * V;
-    const RunAt r = run_of_slot(p.runs, (int64_t)((int)blockIdx.x / n_blocks));
-    if (c >= p.channels) return;
+    const uint32_t c = (((int)blockIdx.x % n_blocks) * kThreads + (int)threadIdx.x) * V;
     Filter<DT, W, V> f;
+    if (c < (uint32_t)p.channels) f.load(p, c);
+    const RunAt r = run_of_slot(p.runs, (int64_t)((int)blockIdx.x / n_blocks));
+    if (c >= (uint32_t)p.channels) return;
     Elems<DT, V> before[W - 1];
     float x[W - 1 + kU][V];
     if (r.n > 0) {
-        f.load(p, c);
         inputs_before<DT, W, V>(p, r, c, before);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) k_conv(const ConvParams p, int n_blo
     auto fetch = [&](int t, Elems<DT, V>(&e)[kU]) {
 #pragma unroll
         for (int u = 0; u < kU; ++u)
-            if (t + u < r.n) e[u].load(p.x.p, (r.tok0 + t + u) * p.x.stride + c);
+            if (t + u < r.n) e[u].load(p.x.p, (r.tok0 + t + u) * p.x.stride, c);
     };
     fetch(0, next);
     for (int t = 0; t < r.n; t += kU) {
@@ -99,7 +101,8 @@ __global__ void __launch_bounds__(kThreads) k_conv(const ConvParams p, int n_blo
             }
             Elems<DT, V> o;
             o.set(y);
-            o.store(p.y.p, (r.tok0 + t + u) * p.y.stride + c);
+            if (p.once) o.store_once(p.y.p, (r.tok0 + t + u) * p.y.stride, c);
+            else o.store(p.y.p, (r.tok0 + t + u) * p.y.stride, c);
         }
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
@@ -111,15 +114,15 @@ __global__ void __launch_bounds__(kThreads) k_conv(const ConvParams p, int n_blo
 // One token of each request, its last W - 1 inputs in a slot of the pool: window and x in, y and the window moved by one out.
 template <int DT, int W, int V, bool SILU>
 __global__ void __launch_bounds__(kThreads) k_conv_step(const ConvParams p, int n_blocks) {
-    const int c = (((int)blockIdx.x % n_blocks) * kThreads + (int)threadIdx.x) * V;
+    const uint32_t c = (((int)blockIdx.x % n_blocks) * kThreads + (int)threadIdx.x) * V;
     const int64_t b = (int)blockIdx.x / n_blocks;
     const int64_t slot = p.slots ? (int64_t)p.slots[b] : b;
-    if (c >= p.channels || slot < 0 || slot >= p.n_slots) return;
+    if (c >= (uint32_t)p.channels || slot < 0 || slot >= p.n_slots) return;
     const int64_t base = slot * (W - 1) * p.channels + c;
     Elems<DT, V> e[W];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) e[j].load(p.window, base + (int64_t)j * p.channels);
-    e[W - 1].load(p.x.p, b * p.x.stride + c);
+    e[W - 1].load(p.x.p, b * p.x.stride, c);
     Filter<DT, W, V> f;
     f.load(p, c);
     float y[V];
@@ -134,17 +137,26 @@ __global__ void __launch_bounds__(kThreads) k_conv_step(const ConvParams p, int 
     for (int j = 0; j < W - 1; ++j) e[j + 1].store(p.window, base + (int64_t)j * p.channels);
     Elems<DT, V> o;
     o.set(y);
-    o.store(p.y.p, b * p.y.stride + c);
+    o.store(p.y.p, b * p.y.stride, c);
 }
 
-// Gradients of a run: the walk goes W - 1 tokens past its end (their dp belongs to the run's last dx), and dx follows W - 1
-// tokens behind.  What reaches inputs before the sequence is ds0's.  Sums over the run go to one row of `part`.
+// Gradients.  A workgroup has kThreads / 64 runs of 2^kConvBwdLog tokens one after the other, a wave each, over 64 V channels: their sums
+// meet in LDS and go out as one row of `part`.  A wave's walk goes W - 1 tokens past its run's end (their dp belongs to the run's
+// last dx), and dx follows W - 1 tokens behind.  What reaches inputs before the sequence is ds0's.
 template <int DT, int W, int V, bool SILU>
 __global__ void __launch_bounds__(kThreads) k_conv_bwd(const ConvParams p, int n_blocks) {
-    const int c = (((int)blockIdx.x % n_blocks) * kThreads + (int)threadIdx.x) * V;
+    constexpr int kWaves = kThreads / 64;
+    __shared__ float s_sum[kWaves][(W + 1) * V][64];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const uint32_t c = (((int)blockIdx.x % n_blocks) * 64 + lane) * V;
     const int64_t slot = (int)blockIdx.x / n_blocks;
-    const RunAt r = run_of_slot(p.runs, slot);
-    if (c >= p.channels) return;
+    RunAt r = run_of_slot(p.runs, slot);
+    {                                                          // the wave's part of it
+        const int at = __builtin_amdgcn_readfirstlane(wave << kConvBwdLog), most = 1 << kConvBwdLog, n = r.n - at;
+        r.n = n < 0 ? 0 : n < most ? n : most;
+        r.tok0 += at;
+        r.first = r.first && at == 0;
+    }
     float dw[V][W], db[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -152,98 +164,120 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const ConvParams p, int n
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[v][j] = 0.f;
     }
-    if (r.n > 0 || r.first) {
+    if (c < (uint32_t)p.channels && (r.n > 0 || r.first)) {
         Filter<DT, W, V> f;
         f.load(p, c);
-        float x[W][V], dp[W][V];               // the last W inputs and gradients, the newest last
+        float x[W - 1 + kUb][V], dp[W - 1 + kUb][V];           // W - 1 inputs and gradients before a step's kUb tokens, and these
         {
             Elems<DT, V> before[W - 1];
             inputs_before<DT, W, V>(p, r, c, before);
 #pragma unroll
-            for (int j = 0; j < W; ++j)
+            for (int j = 0; j < W - 1; ++j)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    x[j][v] = j ? before[j - 1].at(v) : 0.f;
+                    x[j][v] = before[j].at(v);
                     dp[j][v] = 0.f;
                 }
         }
-        const int64_t left = r.start + r.len - r.tok0;         // tokens to the sequence's end
-        const int64_t s = (int64_t)r.seq * (W - 1);
-        const int end = r.n + W - 1;                           // dx of token t - (W - 1) of the run at step t
-        Elems<DT, V> ex, ey;
-        ex.zero();
-        ey.zero();
-        if (left > 0) {
-            ex.load(p.x.p, r.tok0 * p.x.stride + c);
-            ey.load(p.dy.p, r.tok0 * p.dy.stride + c);
-        }
-        for (int t = 0; t < end; ++t) {
-            Elems<DT, V> nx, ny;
-            nx.zero();
-            ny.zero();
-            if (t + 1 < left && t + 1 < end) {
-                nx.load(p.x.p, (r.tok0 + t + 1) * p.x.stride + c);
-                ny.load(p.dy.p, (r.tok0 + t + 1) * p.dy.stride + c);
-            }
-            const int64_t at = r.tok0 - r.start + t - (W - 1);                 // dx's token in its sequence; below 0: of s0
-            const bool wanted = at >= 0 ? t >= W - 1 : true;
+        const int64_t off = r.tok0 - r.start, s = (int64_t)r.seq * (W - 1);
+        const int left = (int)(r.len - off), end = r.n + W - 1;        // tokens to the sequence's end; dx of token t - (W - 1) at step t
+        Elems<DT, V> ex[kUb], ey[kUb];
+        auto fetch = [&](int t) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) {
-                    x[j][v] = x[j + 1][v];
-                    dp[j][v] = dp[j + 1][v];
+            for (int u = 0; u < kUb; ++u) {
+                ex[u].zero();
+                ey[u].zero();
+                if (t + u < left && t + u < end) {
+                    ex[u].load(p.x.p, (r.tok0 + t + u) * p.x.stride, c);
+                    ey[u].load(p.dy.p, (r.tok0 + t + u) * p.dy.stride, c);
                 }
-                x[W - 1][v] = ex.at(v);
-                float g = 0.f;
-                if (t < left) {
-                    g = ey.at(v);
-                    if constexpr (SILU) {
-                        float a = f.b[v];
+            }
+        };
+        // kUb steps; INNER: all of them the run's own tokens, their dx rows the run's too and none of them among the last inputs
+        auto steps = [&](auto inner, int t) {
+            constexpr bool INNER = decltype(inner)::value;
 #pragma unroll
-                        for (int j = 0; j < W; ++j) a = fmaf(f.w[v][j], x[j][v], a);
-                        const float sg = sigmoid<DT == SQ_DTYPE_F32>(a);
-                        g *= sg * fmaf(a, 1.f - sg, 1.f);
+            for (int u = 0; u < kUb; ++u)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    x[W - 1 + u][v] = ex[u].at(v);
+                    dp[W - 1 + u][v] = ey[u].at(v);
+                }
+            fetch(t + kUb);
+#pragma unroll
+            for (int u = 0; u < kUb; ++u) {
+                if (!INNER && t + u >= end) break;
+                if (INNER || t + u < left) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        float g = dp[W - 1 + u][v];
+                        if constexpr (SILU) {
+                            float a = f.b[v];
+#pragma unroll
+                            for (int j = 0; j < W; ++j) a = fmaf(f.w[v][j], x[u + j][v], a);
+                            const float sg = sigmoid<DT == SQ_DTYPE_F32>(a);
+                            g *= sg * fmaf(a, 1.f - sg, 1.f);
+                            dp[W - 1 + u][v] = g;
+                        }
+                        if (INNER || t + u < r.n) {
+                            db[v] += g;
+#pragma unroll
+                            for (int j = 0; j < W; ++j) dw[v][j] = fmaf(g, x[u + j][v], dw[v][j]);
+                        }
                     }
                 }
-                dp[W - 1][v] = g;
-                if (t < r.n) {
-                    db[v] += g;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[v][j] = fmaf(g, x[j][v], dw[v][j]);
-                }
-            }
-            // a later run's first steps see inputs of the run before it: theirs to write
-            if (wanted && (at >= 0 || (r.first && p.ds0))) {
+                // dx's token in its sequence; below 0: a row of s0.  A later run's first steps see inputs of the run before it: theirs.
+                const int64_t at = off + t + u - (W - 1);
+                if (!INNER && (at >= 0 ? t + u < W - 1 : !r.first || !p.ds0)) continue;
                 float d[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     d[v] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < W; ++j) d[v] = fmaf(f.w[v][W - 1 - j], dp[j][v], d[v]);
+                    for (int j = 0; j < W; ++j) d[v] = fmaf(f.w[v][W - 1 - j], dp[u + j][v], d[v]);
                 }
-                const int64_t kept = at - (r.len - (W - 1));                   // its row of s1, where it is one of the last inputs
-                if (p.ds1 && kept >= 0) {
+                const int64_t kept = at - (r.len - (W - 1));           // its row of s1, where it is one of the last inputs
+                if (!INNER && p.ds1 && kept >= 0) {
                     Elems<DT, V> e;
-                    e.load(p.ds1, (s + kept) * p.channels + c);
+                    e.load(p.ds1, (s + kept) * p.channels, c);
 #pragma unroll
                     for (int v = 0; v < V; ++v) d[v] += e.at(v);
                 }
                 Elems<DT, V> o;
                 o.set(d);
-                if (at >= 0) o.store(p.dx.p, (r.start + at) * p.dx.stride + c);
-                else o.store(p.ds0, (s + at + W - 1) * p.channels + c);
+                if (INNER || at >= 0) o.store(p.dx.p, (r.start + at) * p.dx.stride, c);
+                else o.store(p.ds0, (s + at + W - 1) * p.channels, c);
             }
-            ex = nx;
-            ey = ny;
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    x[j][v] = x[j + kUb][v];
+                    dp[j][v] = dp[j + kUb][v];
+                }
+        };
+        fetch(0);
+        for (int t = 0; t < end; t += kUb) {
+            if (t >= W - 1 && t + kUb <= r.n && off + t + kUb <= r.len) steps(std::true_type{}, t);
+            else steps(std::false_type{}, t);
         }
     }
     if (!p.part) return;
-    float* part = p.part + slot * (W + 1) * p.channels + c;
 #pragma unroll
-    for (int j = 0; j <= W; ++j)
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int v = 0; v < V; ++v) part[(int64_t)j * p.channels + v] = j < W ? dw[v][j < W ? j : 0] : db[v];
+        for (int j = 0; j <= W; ++j) s_sum[wave][j * V + v][lane] = j < W ? dw[v][j < W ? j : 0] : db[v];
+    __syncthreads();
+    float* part = p.part + slot * (W + 1) * p.channels;
+    const int c0 = ((int)blockIdx.x % n_blocks) * 64 * V;
+    for (int i = (int)threadIdx.x; i < (W + 1) * V * 64; i += kThreads) {          // in the order of the row's columns
+        const int j = i / (V * 64), at = i % (V * 64);
+        if (c0 + at >= p.channels) continue;
+        float s = s_sum[0][j * V + at % V][at / V];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) s += s_sum[w][j * V + at % V][at / V];
+        part[(int64_t)j * p.channels + c0 + at] = s;
+    }
 }
 
 // dweight and dbias: the rows of `part` added in a fixed order, 64 columns a workgroup, the rows in 16 interleaved parts.
@@ -274,7 +308,8 @@ enum { kOpFwd, kOpStep, kOpBwd };
 
 template <int OP, int DT, int W, int V>
 static hipError_t launch_w(const ConvParams& p, hipStream_t s) {
-    const int n_blocks = (p.channels + kThreads * V - 1) / (kThreads * V);
+    constexpr int kCols = (OP == kOpBwd ? 64 : kThreads) * V;          // channels of a workgroup
+    const int n_blocks = (p.channels + kCols - 1) / kCols;
     const int64_t n = OP == kOpStep ? p.batch : p.runs.n_seq > 0 ? run_slots(p.runs.n_tokens, p.runs.n_seq, p.runs.log) : 0;
     if (n == 0) return hipSuccess;
     const dim3 grid((unsigned)(n * n_blocks));
@@ -302,7 +337,7 @@ static hipError_t launch_v(const ConvParams& p, hipStream_t s) {
 
 template <int OP>
 static hipError_t launch_op(const ConvParams& p, bool vec, hipStream_t s) {
-    constexpr int kDiv = OP == kOpBwd ? 2 : 1;         // of the vector: the gradients keep W + 1 sums an element
+    constexpr int kDiv = OP == kOpBwd ? 4 : OP == kOpFwd ? 2 : 1;         // of the vector: the gradients keep W + 1 sums an element
     if (p.dtype == SQ_DTYPE_BF16)
         return vec ? launch_v<OP, SQ_DTYPE_BF16, kVec<SQ_DTYPE_BF16> / kDiv>(p, s) : launch_v<OP, SQ_DTYPE_BF16, 1>(p, s);
     if (p.dtype == SQ_DTYPE_F16)
@@ -310,7 +345,7 @@ static hipError_t launch_op(const ConvParams& p, bool vec, hipStream_t s) {
     return vec ? launch_v<OP, SQ_DTYPE_F32, kVec<SQ_DTYPE_F32> / kDiv>(p, s) : launch_v<OP, SQ_DTYPE_F32, 1>(p, s);
 }
 
-int conv_run_log(int64_t, int64_t, int32_t) { return 5; }
+int conv_run_log(int64_t, int64_t, int32_t) { return 4; }
 
 hipError_t launch_conv(const ConvParams& p, bool vec, hipStream_t s) { return launch_op<kOpFwd>(p, vec, s); }
 hipError_t launch_conv_step(const ConvParams& p, bool vec, hipStream_t s) { return launch_op<kOpStep>(p, vec, s); }

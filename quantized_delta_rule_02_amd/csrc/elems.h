@@ -36,6 +36,16 @@ struct Elems {
             }
         }
     }
+    // element `lane` of the row at element `row` of p: the row the same for the wave, so that it stays in scalar registers
+    __device__ __forceinline__ void load(const void* p, int64_t row, uint32_t lane) {
+        load(static_cast<const char*>(p) + row * kBytes<DT> + (uint64_t)(lane * (uint32_t)kBytes<DT>), 0);
+    }
+    __device__ __forceinline__ void store(void* p, int64_t row, uint32_t lane) const {
+        store(static_cast<char*>(p) + row * kBytes<DT> + (uint64_t)(lane * (uint32_t)kBytes<DT>), 0);
+    }
+    __device__ __forceinline__ void store_once(void* p, int64_t row, uint32_t lane) const {
+        store_once(static_cast<char*>(p) + row * kBytes<DT> + (uint64_t)(lane * (uint32_t)kBytes<DT>), 0);
+    }
     // the bits as they are
     __device__ __forceinline__ void store(void* p, int64_t i) const {
         char* s = static_cast<char*>(p) + i * kBytes<DT>;
@@ -50,6 +60,15 @@ struct Elems {
                 for (int j = 0; j < 4; ++j) x[j] = w[4 * k + j];
                 reinterpret_cast<u32x4v*>(s)[k] = x;
             }
+        }
+    }
+    // the same past the caches' usual order: rows that the launch does not read again
+    __device__ __forceinline__ void store_once(void* p, int64_t i) const {
+        char* s = static_cast<char*>(p) + i * kBytes<DT>;
+        if constexpr (V * kBytes<DT> == 2) __builtin_nontemporal_store((uint16_t)w[0], reinterpret_cast<uint16_t*>(s));
+        else {
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) __builtin_nontemporal_store(w[k], reinterpret_cast<uint32_t*>(s) + k);
         }
     }
     __device__ __forceinline__ float at(int j) const {

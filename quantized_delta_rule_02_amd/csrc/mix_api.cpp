@@ -78,8 +78,9 @@ sq_status check_conv_cfg(const sq_conv_cfg* c) {
         return SQ_ERR_UNSUPPORTED;
     }
     SQ_TRY(check_seqs(c->n_seq, c->n_tokens, c->d_seq_start));
-    // a thread an element where accesses are single, in the shortest runs
+    // a thread an element where accesses are single, in the shortest runs; the gradients' workgroups have 64 channels there
     if (((c->n_tokens >> 4) + c->n_seq) * ((int64_t(c->channels) + 255) / 256) * 256 > kMaxThreads ||
+        run_slots(c->n_tokens, c->n_seq, kConvBwdRuns) * ((int64_t(c->channels) + 63) / 64) * 256 > kMaxThreads ||
         int64_t(c->width + 1) * c->channels * 16 > kMaxThreads) {
         set_error("%lld tokens of %d channels in %d sequences: too many for one call", (long long)c->n_tokens, c->channels, c->n_seq);
         return SQ_ERR_ARG;
@@ -88,7 +89,7 @@ sq_status check_conv_cfg(const sq_conv_cfg* c) {
 }
 
 size_t conv_bytes(const sq_conv_cfg& c) {
-    return size_t(run_slots(c.n_tokens, c.n_seq, kConvBwdLog)) * size_t(c.width + 1) * size_t(c.channels) * 4;
+    return size_t(run_slots(c.n_tokens, c.n_seq, kConvBwdRuns)) * size_t(c.width + 1) * size_t(c.channels) * 4;
 }
 
 ConvParams conv_params(const sq_conv_cfg& c, int log, const float* weight, const float* bias) {
@@ -123,6 +124,9 @@ extern "C" sq_status sq_conv(const sq_conv_cfg* cfg, const sq_rows* x, const flo
     ck.plain(d_s1, "s1");
     if (ck.st != SQ_OK) return ck.st;
     p.s0 = d_s0; p.s1 = d_s1;
+    // x and y beyond what the last cache holds: y would push out x's rows, and be gone itself when the next call reads it (12301 tokens of
+    // 8192 channels in bfloat16: 82 us so, 88 otherwise; below, the next call finds y there)
+    p.once = cfg->n_tokens * cfg->channels * esize(cfg->dtype) * 2 > (int64_t(256) << 20);
     const hipError_t e = launch_conv(p, ck.vec && cfg->channels % ck.v == 0, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? SQ_OK : fail_hip(e, "convolution launch");
 }
@@ -136,7 +140,7 @@ extern "C" sq_status sq_conv_bwd(const sq_conv_cfg* cfg, const sq_rows* x, const
     SQ_TRY(check_optional(d_bias, "bias"));
     SQ_TRY(check_optional(d_dweight, "dweight"));
     SQ_TRY(check_optional(d_dbias, "dbias"));
-    ConvParams p = conv_params(*cfg, kConvBwdLog, d_weight, d_bias);
+    ConvParams p = conv_params(*cfg, kConvBwdRuns, d_weight, d_bias);
     RowCheck ck{cfg->dtype, cfg->n_tokens, conv_vec(cfg->dtype)};
     const bool rows = cfg->n_tokens > 0 && cfg->n_seq > 0;
     p.x = ck(x, "x", cfg->channels, rows);
