@@ -393,28 +393,44 @@ def sq_valu_probe(waves_per_simd, out, stream=None):
 _DTYPES = {}                 # torch's element types to SQ_DTYPE_*
 
 
+def _types() -> dict:
+    import torch
+    _DTYPES.update({torch.float32: SQ_DTYPE_F32, torch.bfloat16: SQ_DTYPE_BF16, torch.float16: SQ_DTYPE_F16})
+    return _DTYPES
+
+
 def _dtype_code(dtype) -> int:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: SQ_DTYPE_F32, torch.bfloat16: SQ_DTYPE_BF16, torch.float16: SQ_DTYPE_F16})
-    code = _DTYPES.get(dtype)
+    code = (_DTYPES or _types()).get(dtype)
     if code is None:
         raise TypeError(f"element type {dtype}: float32, bfloat16 or float16")
     return code
 
 
+_raw_stream = None           # (device index) -> handle of its current stream, and the current device's index
+
+
+def _stream_calls():
+    """torch's own lookups behind torch.cuda.current_stream and current_device, without the objects they build (2 us a call)."""
+    global _raw_stream
+    import torch
+    torch.cuda.current_stream()                          # initialises torch's side
+    _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    return _raw_stream
+
+
 def _call(fn, name, device, stream, *args):
     """fn(*args, stream handle) with `device` current (None: the device's current stream)."""
-    import torch
+    raw, current = _raw_stream or _stream_calls()
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = raw(device.index)
     elif getattr(stream, "device", device) != device:
         raise ValueError(f"stream on {stream.device}, tensors on {device}")
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == device.index:
+    if current() == device.index:
         status = fn(*args, handle)
     else:
+        import torch
         with torch.cuda.device(device):
             status = fn(*args, handle)
     if status != 0:
@@ -462,15 +478,14 @@ def _row_array(t, shape, dtype, device, name):
 
 def _plain(t, shape, device, name):
     """Pointer of a contiguous float32 tensor of exactly this shape (None stays NULL)."""
-    import torch
     if t is None:
         return None
     if getattr(t, "device", None) != device:
         _on(t, device, name)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype is not torch.float32:
-        raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
+    if (_DTYPES or _types()).get(t.dtype) != SQ_DTYPE_F32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -626,10 +641,9 @@ def sq_norm_out_bwd(y, do, dy, weight=None, z=None, dz=None, act=SQ_ACT_SILU, ch
 
 def _first(t, n, what, name):
     """The device of the tensor that fixes a call's sizes."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != n:
+    if len(t.shape) != n:
         raise ValueError(f"{name} must be {what}")
     return t.device
 
@@ -649,7 +663,8 @@ def _typed(t, shape, dtype, device, name):
     """Pointer of a contiguous tensor of exactly this shape and type (None stays NULL)."""
     if t is None:
         return None
-    _on(t, device, name)
+    if getattr(t, "device", None) != device:
+        _on(t, device, name)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
@@ -739,7 +754,6 @@ class _SsmCall:
         self.dtype = u.dtype
         self.n_seq, start = (0, None) if step else _seqs(seq_start, dev)
         self.cfg = _lib.SqSsmCfg(_dtype_code(u.dtype), C, N, G, int(bool(softplus)), self.n_seq, T, start)
-        self.keep = []
         self.inputs = _lib.SqSsmIn(self.rows(u, "u"), self.rows(dt, "dt"), self.bc(b, "b"), self.bc(c, "c"), self.rows(z, "z"),
                                    self.vec(a, (C, N), "a"), self.vec(d, (C,), "d"), self.vec(dt_bias, (C,), "dt_bias"))
         self.states = (self.n_seq, C, N)
@@ -747,9 +761,7 @@ class _SsmCall:
     def _ptr(self, t, shape, name):
         if t is None:
             return None
-        p = ctypes.pointer(_row_array(t, shape, self.dtype, self.dev, name))
-        self.keep.append(p)
-        return p
+        return ctypes.pointer(_row_array(t, shape, self.dtype, self.dev, name))     # the structure it goes into keeps it
 
     def rows(self, t, name):
         return self._ptr(t, (self.T, self.C), name)
