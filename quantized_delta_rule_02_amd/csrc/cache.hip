@@ -58,6 +58,20 @@ __device__ __forceinline__ float code_of(const Scale& k, float x) {
     return fminf(fmaxf(n, -kTop<F>), kTop<F>);
 }
 
+// n / d for n below 2^31: with l = ceil(log2 d) and m = floor(2^(31 + l) / d) + 1, m d is 2^(31 + l) + e, 0 < e <= d <= 2^l, so that
+// n m / 2^(31 + l) exceeds n / d by less than 1 / d.
+struct Div {
+    uint32_t m;
+    int32_t s;
+    explicit Div(uint32_t d) {
+        int l = 0;
+        while ((uint64_t(1) << l) < d) ++l;
+        s = 31 + l;
+        m = (uint32_t)((uint64_t(1) << s) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (uint32_t)(((uint64_t)n * m) >> s); }
+};
+
 // Eight codes as stored: 8 bytes, or 4 for 4-bit codes (the first of two in the low half of its byte).
 template <int F>
 __device__ __forceinline__ uint2 pack8(const float* v) {
@@ -85,15 +99,79 @@ __device__ __forceinline__ float unpack1(uint32_t c) {           // of a code in
     else return (float)((int32_t)(c << 28) >> 28);
 }
 
-// K vectors of eight elements a thread; `lanes` threads (a power of two) belong to a group, of which those with elements work.
+// Eight codes by the approximate quotient; `near` grows to 1 or more where one of them comes within 2^-11 of half a step of the
+// middle between two codes (the quotient is off by 2^-22 of itself, 2^-15 of a step at most): there only the exact remainder tells.
+template <int F>
+__device__ __forceinline__ uint2 quick8(const Scale& k, const float* x, float& near) {
+    uint2 w{0, 0};
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = x[j] * k.inv;
+    if constexpr (F == SQ_CACHE_E4M3) {
+        w.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+        w.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], (int)w.x, true);
+        w.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
+        w.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], (int)w.y, true);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int word = (int)(j < 4 ? w.x : w.y);
+            const float v = j % 4 == 0 ? __builtin_amdgcn_cvt_f32_fp8(word, 0) : j % 4 == 1 ? __builtin_amdgcn_cvt_f32_fp8(word, 1)
+                          : j % 4 == 2 ? __builtin_amdgcn_cvt_f32_fp8(word, 2) : __builtin_amdgcn_cvt_f32_fp8(word, 3);
+            // half a step is 2^(e - 4), e the exponent but not below -6
+            const float top = fmaxf(__uint_as_float(__float_as_uint(y[j]) & 0x7f800000u), 0x1p-6f);
+            near = fmaxf(near, fabsf(y[j] - v) >= top * (0.0625f * (1.f - 0x1p-11f)) ? 1.f : 0.f);
+        }
+    } else {
+        // adding 1.5 2^23 rounds to an integer, ties to even, and leaves it in the low bits
+        constexpr float kRound = 12582912.f;
+        uint32_t b[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float t = y[j] + kRound;
+            b[j] = __float_as_uint(t);
+            near = fmaxf(near, fabsf(y[j] - (t - kRound)) * (2.f * (1.f + 0x1p-11f)));
+        }
+        if constexpr (F == SQ_CACHE_INT4) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w.x |= (b[j] & 15u) << (4 * j);
+        } else {
+            // bytes 0 of the two sources, then the pairs
+            w.x = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u), __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
+            w.y = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[7], b[6], 0x0c0c0400u), __builtin_amdgcn_perm(b[5], b[4], 0x0c0c0400u), 0x05040100u);
+        }
+    }
+    return w;
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t x) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
+    return o > x ? o : x;
+}
+// The maximum over 2^log adjacent lanes; all of them get it.
+__device__ __forceinline__ uint32_t group_max(uint32_t x, int log) {
+    if (log > 0) x = max_dpp<0xb1>(x);                           // lane ^ 1
+    if (log > 1) x = max_dpp<0x4e>(x);                           // lane ^ 2
+    if (log > 2) x = max_dpp<0x141>(x);                          // 7 - lane of 8
+    if (log > 3) x = max_dpp<0x140>(x);                          // 15 - lane of 16
+    if (log > 4) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        x = r[0] > r[1] ? r[0] : r[1];
+    }
+    if (log > 5) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        x = r[0] > r[1] ? r[0] : r[1];
+    }
+    return x;
+}
+
+// K vectors of eight elements a thread; 2^lanes_log threads belong to a group, of which those with elements work.
 template <int DT, int F, int K>
-__global__ void __launch_bounds__(kThreads) k_cache_write(const CacheParams p, int lanes_log, uint32_t groups) {
+__global__ void __launch_bounds__(kThreads) k_cache_write(const CacheParams p, int lanes_log, uint32_t groups, Div by_groups) {
     const int lanes = 1 << lanes_log, lane = (int)threadIdx.x & (lanes - 1);
     const int64_t item = (int64_t)blockIdx.x * (kThreads >> lanes_log) + ((int)threadIdx.x >> lanes_log);
-    if (item >= p.n_rows * groups) return;                       // by whole groups
-    const uint32_t row = (uint32_t)item / groups, g = (uint32_t)item - row * groups;
-    const int64_t slot = p.slots ? (int64_t)p.slots[row] : (int64_t)row;
-    if (slot < 0 || slot >= p.n_slots) return;
+    const uint32_t row = by_groups((uint32_t)item), g = (uint32_t)item - row * groups;
+    const bool in = item < p.n_rows * groups;
     const int64_t e0 = (int64_t)g * p.group;
     Elems<DT, 8> x[K];
     uint32_t most = 0;
@@ -101,8 +179,10 @@ __global__ void __launch_bounds__(kThreads) k_cache_write(const CacheParams p, i
     for (int k = 0; k < K; ++k) {
         const int at = (k * lanes + lane) * 8;
         x[k].zero();
-        if (at < p.group) x[k].load(p.x.p, (int64_t)row * p.x.stride + e0 + at);
+        if (in && at < p.group) x[k].load(p.x.p, (int64_t)row * p.x.stride + e0 + at);
     }
+    // in flight beside the row, which is read whether its slot is there or not
+    const int64_t slot = !in ? -1 : p.slots ? (int64_t)p.slots[row] : (int64_t)row;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -110,20 +190,23 @@ __global__ void __launch_bounds__(kThreads) k_cache_write(const CacheParams p, i
             const uint32_t b = __float_as_uint(x[k].at(j)) & 0x7fffffffu;
             most = b > most ? b : most;
         }
-    for (int m = 1; m < lanes; m <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)most, m);
-        most = o > most ? o : most;
-    }
-    const Scale s = scale_of<F>(most);
-    if (lane == 0) p.scales[slot * groups + g] = s.s;
+    const bool live = slot >= 0 && slot < p.n_slots;             // the same for a group; the wave's other groups go on
+    const Scale s = scale_of<F>(group_max(most, lanes_log));
+    if (live && lane == 0) p.scales[slot * groups + g] = s.s;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int at = (k * lanes + lane) * 8;
-        if (at >= p.group) continue;
-        float v[8];
+        float v[8], near = s.up == 1.f ? 0.f : 1.f;              // scaled quotients go the exact way
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = code_of<F>(s, x[k].at(j));
-        const uint2 w = pack8<F>(v);
+        for (int j = 0; j < 8; ++j) v[j] = x[k].at(j);
+        uint2 w = quick8<F>(s, v, near);
+        if (s.inv == 0.f) w = uint2{0, 0};                       // a group of zeros, or one with a value that is not finite
+        else if (near >= 1.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = code_of<F>(s, v[j]);
+            w = pack8<F>(v);
+        }
+        if (!live || at >= p.group) continue;
         uint8_t* to = p.codes + slot * p.row_bytes + (F == SQ_CACHE_INT4 ? (e0 + at) / 2 : e0 + at);
         if constexpr (F == SQ_CACHE_INT4) *reinterpret_cast<uint32_t*>(to) = w.x;
         else *reinterpret_cast<uint2*>(to) = w;
@@ -178,27 +261,30 @@ __global__ void __launch_bounds__(kThreads) k_cache_write_any(const CacheParams 
 
 // V elements a thread (8, or 2 for any alignment), U of them with their loads in flight together.
 template <int DT, int F, int V, int U>
-__global__ void __launch_bounds__(kThreads) k_cache_read(const CacheParams p, uint32_t groups, uint32_t per_row, int64_t n_items) {
+__global__ void __launch_bounds__(kThreads) k_cache_read(const CacheParams p, uint32_t groups, uint32_t per_row, int64_t n_items, Div by_row, Div by_group) {
     const int64_t base = (int64_t)blockIdx.x * (kThreads * U) + (int)threadIdx.x;
-    uint32_t c[U][2];
+    uint32_t c[U][2], row[U];
     float s[U], s2[U];
-    int64_t to[U];
+    int64_t to[U], slot[U];
     int at[U];
+    // all slots, then all codes and scales: two latencies for U items
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t item = base + u * kThreads;
-        to[u] = -1;
+        const int64_t i = base + u * kThreads;
+        const uint32_t item = (uint32_t)(i < n_items ? i : n_items - 1);
+        row[u] = by_row(item);
+        at[u] = (int)(item - row[u] * per_row) * V;
+        slot[u] = p.slots ? (int64_t)p.slots[row[u]] : (int64_t)row[u];
+        to[u] = i < n_items ? (int64_t)row[u] * p.x.stride + at[u] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
         c[u][0] = c[u][1] = 0;
         s[u] = s2[u] = 0.f;
-        at[u] = 0;
-        if (item >= n_items) continue;
-        const uint32_t row = (uint32_t)item / per_row;
-        at[u] = (int)((uint32_t)item - row * per_row) * V;
-        const int64_t slot = p.slots ? (int64_t)p.slots[row] : (int64_t)row;
-        if (slot < 0 || slot >= p.n_slots) continue;
-        to[u] = (int64_t)row * p.x.stride + at[u];
-        const uint8_t* from = p.codes + slot * p.row_bytes + (F == SQ_CACHE_INT4 ? at[u] / 2 : at[u]);
-        s[u] = p.scales[slot * groups + (uint32_t)at[u] / (uint32_t)p.group];
+        if (slot[u] < 0 || slot[u] >= p.n_slots) to[u] = -1;
+        if (to[u] < 0) continue;
+        const uint8_t* from = p.codes + slot[u] * p.row_bytes + (F == SQ_CACHE_INT4 ? at[u] / 2 : at[u]);
+        s[u] = p.scales[slot[u] * groups + by_group((uint32_t)at[u])];
         if constexpr (V == 8) {
             if constexpr (F == SQ_CACHE_INT4) {
                 c[u][0] = *reinterpret_cast<const uint32_t*>(from);
@@ -211,7 +297,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(const CacheParams p, ui
             c[u][0] = from[0];
             if (at[u] + 1 < p.d) {
                 if constexpr (F != SQ_CACHE_INT4) c[u][0] |= (uint32_t)from[1] << 8;
-                s2[u] = p.scales[slot * groups + (uint32_t)(at[u] + 1) / (uint32_t)p.group];
+                s2[u] = p.scales[slot[u] * groups + by_group((uint32_t)(at[u] + 1))];
             }
         }
     }
@@ -255,8 +341,8 @@ static hipError_t launch_write(const CacheParams& p, bool vec, hipStream_t s) {
     while (lanes_log < 6 && (8 << lanes_log) < p.group) ++lanes_log;
     const int64_t per = kThreads >> lanes_log;
     const dim3 grid((unsigned)((items + per - 1) / per));
-    if (p.group <= 512) k_cache_write<DT, F, 1><<<grid, kThreads, 0, s>>>(p, lanes_log, groups);
-    else k_cache_write<DT, F, 2><<<grid, kThreads, 0, s>>>(p, lanes_log, groups);
+    if (p.group <= 512) k_cache_write<DT, F, 1><<<grid, kThreads, 0, s>>>(p, lanes_log, groups, Div(groups));
+    else k_cache_write<DT, F, 2><<<grid, kThreads, 0, s>>>(p, lanes_log, groups, Div(groups));
     return hipGetLastError();
 }
 
@@ -266,8 +352,8 @@ static hipError_t launch_read(const CacheParams& p, bool vec, hipStream_t s) {
     const int64_t items = p.n_rows * per_row;
     constexpr int kU = 4;
     const dim3 grid((unsigned)((items + kThreads * kU - 1) / (kThreads * kU)));
-    if (vec) k_cache_read<DT, F, 8, kU><<<grid, kThreads, 0, s>>>(p, groups, per_row, items);
-    else k_cache_read<DT, F, 2, kU><<<grid, kThreads, 0, s>>>(p, groups, per_row, items);
+    if (vec) k_cache_read<DT, F, 8, kU><<<grid, kThreads, 0, s>>>(p, groups, per_row, items, Div(per_row), Div((uint32_t)p.group));
+    else k_cache_read<DT, F, 2, kU><<<grid, kThreads, 0, s>>>(p, groups, per_row, items, Div(per_row), Div((uint32_t)p.group));
     return hipGetLastError();
 }
 
