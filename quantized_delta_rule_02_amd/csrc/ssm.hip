@@ -17,10 +17,11 @@
 
 namespace sq {
 
-template <int DT, int N, bool VEC, bool LOCAL>
+// TT: tokens staged at a time.
+template <int DT, int N, bool VEC, bool LOCAL, int TT>
 __global__ void __launch_bounds__(kSsmThreads) k_ssm(const SsmParams p, int n_blocks) {
     using L = SsmLane<N>;
-    constexpr int TT = 32, CB = L::kBlockCh, NV = CB / 4, kItems = (TT * NV + kSsmThreads - 1) / kSsmThreads;
+    constexpr int CB = L::kBlockCh, NV = CB / 4, kItems = (TT * NV + kSsmThreads - 1) / kSsmThreads;
     constexpr int kRows = LOCAL ? 1 : 2, kBc = (TT * kRows * (N / 4) + kSsmThreads - 1) / kSsmThreads;
     __shared__ __attribute__((aligned(16))) float2 s_d[TT][CB];           // delta, delta u
     __shared__ __attribute__((aligned(16))) float s_y[LOCAL ? 1 : TT][CB + L::kWaveCh];     // rows apart so that four tokens of a wave meet no bank twice
@@ -269,9 +270,16 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm_step(const SsmParams p, int
 
 // ------------------------------------------------------------------ launches
 
+// The gradients always go by segments; of 128 tokens where they still give every CU several workgroups (less to join: 16 us instead of 27
+// of 850 for 8190 tokens of 4096 x 16).  The forward pass walks the tokens twice with segments, so it takes them only where whole
+// sequences leave much of the GPU idle, below 352 workgroups (us with segments / without, bfloat16, 16 states, sequences x channels):
+//   1 x 4096 of 777: 41/89   1 x 4096 of 4000: 145/443   2 x 4096 of 2000: 142/335   3 x 4096 of 2000: 188/298   4 x 4096 of 2000: 239/308
+//   1 x 2048 of 2000: 50/218   4 x 2048 of 2000: 131/304   8 x 2048 of 1500: 179/247   8 x 1024 of 1500: 106/246   16 x 256 of 500: 37/85
+//   7 x 4096 of 1757 (448 workgroups): 440/376.
+// Sequences of fewer than 128 tokens have no room for segments.  A segment is at least 64 tokens, longer once 2048 workgroups are there.
 int ssm_segment_log(int64_t n_tokens, int64_t n_seq, int64_t blocks, bool backward) {
     if (backward) return (n_tokens >> 7) * blocks >= 2048 ? 7 : 6;
-    if (n_seq < 1 || n_tokens / n_seq < 128 || n_seq * blocks >= 224) return -1;
+    if (n_seq < 1 || n_tokens / n_seq < 128 || n_seq * blocks >= 352) return -1;
     int log = 6;
     while (log < 12 && (n_tokens >> (log + 1)) * blocks >= 2048) ++log;
     return log;
@@ -287,16 +295,20 @@ template <int DT, int N, bool VEC>
 static hipError_t scan_n(const SsmParams& p, hipStream_t s) {
     const int blocks = (int)ssm_blocks(p.channels, p.n_groups, N);
     if (p.runs.log < 0) {
-        k_ssm<DT, N, VEC, false><<<dim3((unsigned)((int64_t)p.runs.n_seq * blocks)), kSsmThreads, 0, s>>>(p, blocks);
+        // Long sequences leave one or two workgroups on a CU, each waiting at its own barriers: 64 tokens between them (7 sequences of 1757 x 4096 x 16:
+        // 355 us, 375 with 32, 408 with 16).  Short ones want many workgroups there, so little LDS (64 of 4 tokens: 30 us with 64, 19 with 32).
+        const dim3 grid((unsigned)((int64_t)p.runs.n_seq * blocks));
+        if (p.runs.n_tokens >= 64 * (int64_t)p.runs.n_seq) k_ssm<DT, N, VEC, false, 64><<<grid, kSsmThreads, 0, s>>>(p, blocks);
+        else k_ssm<DT, N, VEC, false, 32><<<grid, kSsmThreads, 0, s>>>(p, blocks);
         return hipGetLastError();
     }
     const dim3 grid((unsigned)(run_slots(p.runs.n_tokens, p.runs.n_seq, p.runs.log) * blocks));
-    k_ssm<DT, N, VEC, true><<<grid, kSsmThreads, 0, s>>>(p, blocks);
+    k_ssm<DT, N, VEC, true, 32><<<grid, kSsmThreads, 0, s>>>(p, blocks);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     e = launch_ssm_join(p, 1, s);
     if (e != hipSuccess) return e;
-    k_ssm<DT, N, VEC, false><<<grid, kSsmThreads, 0, s>>>(p, blocks);
+    k_ssm<DT, N, VEC, false, 32><<<grid, kSsmThreads, 0, s>>>(p, blocks);
     return hipGetLastError();
 }
 template <int DT, int N, bool VEC>
