@@ -435,8 +435,8 @@ sq_status sq_conv_step(const sq_conv_cfg* cfg, const sq_rows* x, const float* d_
  * strides, channels / n_groups) are accessed so, others element by element.  d_s0 and d_s1 may be the same array; no other two
  * arrays may overlap.  Few long sequences are cut into segments that run side by side (a choice by the call's sizes alone); the
  * result agrees with the token by token order to float32 rounding.  Nothing depends on what else runs (no atomics, fixed orders).
- * A result that the formula makes NaN or infinite is not finite here either; other channels (in the gradients: but for those of b
- * and c of that token and group and what they sum up) and other sequences keep their results.
+ * A result that the formula makes NaN or infinite is not finite here either.  Such a value in a channel's inputs leaves the other
+ * channels and the other sequences as they are, but for the gradients of b and c of its group in its sequence, sums over channels.
  *
  * sq_ssm_scan_bwd: from dy and d_ds1 (NULL = zero) the gradients of u, dt, b, c (summed over a group's channels), z (NULL: not
  * wanted), and where not NULL of a, d, dt_bias and the first states (d_ds0 may be d_ds1).  Nothing of the forward call is needed.

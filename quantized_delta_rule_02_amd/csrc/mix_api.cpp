@@ -165,6 +165,7 @@ extern "C" sq_status sq_conv_step(const sq_conv_cfg* cfg, const sq_rows* x, cons
     SQ_TRY(check_conv_cfg(cfg));
     if (cfg->n_tokens == 0) return SQ_OK;
     if (n_slots < 0 || n_slots > 0x7fffffff) { set_error("n_slots %lld", (long long)n_slots); return SQ_ERR_ARG; }
+    if (n_slots == 0) return SQ_OK;          // every slot is outside
     SQ_TRY(check_f32(d_weight, "weight", 4));
     SQ_TRY(check_optional(d_bias, "bias"));
     if (!aligned(d_slots, 4)) { set_error("d_slots is not aligned"); return SQ_ERR_ARG; }
@@ -339,6 +340,7 @@ extern "C" sq_status sq_ssm_step(const sq_ssm_cfg* cfg, const sq_ssm_in* in, con
     SQ_TRY(check_ssm_cfg(cfg));
     if (cfg->n_tokens == 0) return SQ_OK;
     if (n_slots < 0 || n_slots > 0x7fffffff) { set_error("n_slots %lld", (long long)n_slots); return SQ_ERR_ARG; }
+    if (n_slots == 0) return SQ_OK;          // every slot is outside
     if (!aligned(d_slots, 4)) { set_error("d_slots is not aligned"); return SQ_ERR_ARG; }
     if (cfg->n_tokens * ssm_fwd_blocks(*cfg) * 256 > kMaxThreads) {
         set_error("%lld requests of %d channels: too many for one call", (long long)cfg->n_tokens, cfg->channels);
@@ -377,7 +379,7 @@ sq_status cache_call(const sq_cache_cfg* c, const sq_rows* x, const int32_t* d_s
         set_error("%lld rows of %d elements: too many for one call", (long long)c->n_rows, c->d);
         return SQ_ERR_SHAPE;
     }
-    empty = c->n_rows == 0;
+    empty = c->n_rows == 0 || c->n_slots == 0;      // with no slots every slot is outside
     if (empty) return SQ_OK;
     RowCheck ck{c->dtype, c->n_rows, 8};
     ck.v = 16 / int(esize(c->dtype));                // float32 rows of eight elements are two accesses

@@ -177,7 +177,7 @@ def test_long_and_short_segments_of_the_gradients(dev):
     s0, ds1, start = rn(3, C, N), rn(3, C, N), ref.starts(lens).to(dev)
 
     def run(k):
-        at = lambda t: t[:, k].contiguous() if t.dim() < 3 else t[:, k].contiguous()  # noqa: E731
+        at = lambda t: t[:, k].contiguous()  # noqa: E731
         v = {n: at(t) for n, t in (("u", u), ("dt", dt), ("z", z), ("dy", dy))}
         o = {n: torch.empty_like(t) for n, t in (("du", v["u"]), ("ddt", v["u"]), ("dz", v["u"]), ("da", a[k].contiguous()), ("db", b), ("dc", c),
                                                 ("dd", d[k].contiguous()), ("ds0", at(s0)))}

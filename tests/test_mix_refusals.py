@@ -171,6 +171,9 @@ def test_cache(fn):
 def test_nothing_to_do():
     assert conv("sq_conv", make(_lib.SqConvCfg, CONV, dict(n_seq=0)), x=None, y=None, w=None) == 0
     assert conv("sq_conv_step", make(_lib.SqConvCfg, CONV, dict(n_tokens=0)), x=None, y=None, w=None, window=None) == 0
+    assert conv("sq_conv_step", make(_lib.SqConvCfg, CONV, {}), n_slots=0, window=None) == 0           # every slot is outside
+    assert ssm("sq_ssm_step", make(_lib.SqSsmCfg, SSM, {}), n_slots=0, state=None) == 0
+    assert cache("sq_cache_write", make(_lib.SqCacheCfg, CACHE, dict(n_slots=0)), codes=None, scales=None) == 0
     assert ssm("sq_ssm_scan", make(_lib.SqSsmCfg, SSM, dict(n_seq=0)), u=None, y=None, a=None, work=None, nbytes=0) == 0
     assert ssm("sq_ssm_step", make(_lib.SqSsmCfg, SSM, dict(n_tokens=0)), u=None, y=None, a=None, state=None) == 0
 
