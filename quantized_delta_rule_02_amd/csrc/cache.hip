@@ -8,6 +8,11 @@
 // multiply-add: k u has at most 8 bits, so k u s and x differ by a multiple of the last place of u s of at most half of u s or a
 // little more; comparing it with u s / 2 tells whether k is the nearest one.
 //
+// An approximate quotient settles nearly all codes: with x / s to 2^-22, only values within 2^-11 of half a step of a middle take the
+// exact way (one wave in ten has one).  12301 rows of 1024 bfloat16 elements into int8: 11.4 us (3.3 TB/s; every code the exact way:
+// 13.1), of which 3 are the launch; 65536 such rows read back from slots in any order: 44 us, 4.6 TB/s (52 with each row's slot,
+// codes and scale one after another instead of four of each in flight).  64 rows: the launch, 4 us on the GPU, 8.5 of host time.
+//
 // Memory bounds both: every row is read and written once.  A thread holds eight elements (16 bytes of a 16-bit type) and the
 // threads of a group, a power of two of one wave, find its maximum by lane exchanges; the group's bits are compared as
 // integers, so that a NaN or an infinity is the maximum and makes the scale NaN.

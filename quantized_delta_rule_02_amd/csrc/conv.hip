@@ -3,10 +3,15 @@
 //   p_t = bias + sum_j w_j x_{t - W + 1 + j},   y_t = p_t or p_t sigmoid(p_t)        (x before a sequence: s0, or zero)
 //   dp = dy act'(p),  dx_t = sum_j w_j dp_{t + W - 1 - j} (+ ds1),  dw_j = sum_t dp_t x_{t - W + 1 + j},  dbias = sum_t dp_t
 //
-// Memory bounds it: x is read once and y written once.  A thread owns V adjacent channels (16 bytes) and walks a run of tokens
+// Memory bounds the forward pass: x is read once and y written once.  A thread owns V adjacent channels and walks a run of tokens
 // with the last W - 1 inputs in registers; the only inputs read twice are the W - 1 before each run.  Runs start at a sequence's
 // start, so no run holds two sequences, and the run that reads s0 is also the one that writes s1 (each thread its own channels,
-// after its reads), so that both may be the same array.
+// after its reads), so that both may be the same array.  12301 tokens of 8192 channels in bfloat16, four taps, new inputs every pass:
+// 84 us, 4.8 TB/s (a copy: 6.0).  Four channels a thread (8-byte accesses) leave 62 registers, so that 8 waves a SIMD hide the
+// latency: eight channels took 97 us on one set of inputs, four 85.  Runs of 16 tokens with 8 loads in flight: 82 us, of 32: 86, of 8: 92.
+// The gradients are bound by the vector unit, 37 instructions an element (p again, its derivative, W products each for dx and
+// dweight) with 69 to 80 % of its time used: 8190 tokens of 8192 channels 96 us, floor by memory 67.  Two channels a thread (82
+// registers) 89 us, four 97; runs of 64 tokens a wave 87 us, of 32: 89, of 16: 97 (W - 1 more steps each).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
