@@ -225,6 +225,39 @@ def test_graphs_streams_and_calls_at_once(dev):
             assert torch.equal(other[k], eager[0][k]), k
 
 
+def test_thousands_of_sequences(dev):
+    """More sequences than two rounds of the search for a run's sequence cover (64 x 64)."""
+    check(8, 4, [(i * 5) % 4 for i in range(5000)], F32, dev)
+
+
+def test_offsets_that_break_the_rules_touch_nothing_else(dev):
+    C, W, T, n = 40, 4, 100, 4
+    x = ref.conv_inputs(C, W, [25] * n, 71, BF16)
+    g = {k: v.to(dev) for k, v in x.items()}
+
+    def fenced(shape, dtype):
+        size = 1
+        for s in shape:
+            size *= s
+        buf = torch.full((size + 2 * 4096,), 3.0, dtype=dtype, device=dev)
+        return buf, buf[4096:4096 + size].view(shape)
+
+    for at in ([0, 60, 20, 90, 100], [-50, 10, 20, 30, 4000], [100, 80, 60, 40, 20], [2 ** 31 - 1, -2 ** 31, 5, 2 ** 30, -7]):
+        start = torch.tensor(at, dtype=torch.int32, device=dev)
+        outs = {k: fenced(s, d) for k, s, d in (("y", (T, C), BF16), ("s1", (n, W - 1, C), BF16), ("dx", (T, C), BF16), ("ds0", (n, W - 1, C), BF16),
+                                                ("dw", (C, W), F32), ("db", (C,), F32))}
+        nbytes = sq.sq_conv_bytes(BF16, C, W, n, T)
+        buf = torch.full((nbytes + 2 * 4096,), 7, dtype=torch.uint8, device=dev)
+        v = {k: o[1] for k, o in outs.items()}
+        sq.sq_conv(g["x"], g["weight"], v["y"], bias=g["bias"], seq_start=start, s0=g["s0"], s1=v["s1"])
+        sq.sq_conv_bwd(g["x"], g["weight"], g["dy"], v["dx"], dweight=v["dw"], dbias=v["db"], bias=g["bias"], seq_start=start, s0=g["s0"], ds1=g["ds1"],
+                       ds0=v["ds0"], workspace=buf[4096:4096 + nbytes])
+        torch.cuda.synchronize()
+        for k, (b, _) in outs.items():
+            assert bool((b[:4096] == 3).all()) and bool((b[-4096:] == 3).all()), (at, k)
+        assert bool((buf[:4096] == 7).all()) and bool((buf[4096 + nbytes:] == 7).all()), at
+
+
 def test_no_sequences_and_no_tokens(dev):
     C, W = 24, 4
     w, b = torch.randn(C, W, device=dev), torch.randn(C, device=dev)

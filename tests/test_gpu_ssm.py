@@ -354,6 +354,32 @@ def test_graphs_streams_and_calls_at_once(lens, dev):
             assert torch.equal(other[k], eager[0][k]), k
 
 
+def test_offsets_that_break_the_rules_touch_nothing_else(dev):
+    C, N, n, T = 24, 16, 3, 900
+    x = ref.ssm_inputs(C, N, 1, [300] * n, 71, F32)
+    g = put(x, dev)
+    names = {"y": "u", "s1": "s0", "du": "u", "ddt": "dt", "da": "a", "db": "b", "dc": "c", "dz": "z", "dd": "d", "ddt_bias": "dt_bias", "ds0": "s0"}
+    size = [sq.sq_ssm_scan_bytes(F32, C, N, 1, n, T, backward=b) for b in (False, True)]
+    assert size[0] > 0                                  # goes by segments
+    for at in ([0, 600, 100, 900], [-50, 10, 20, 4000], [900, 800, 600, 40], [2 ** 31 - 1, -2 ** 31, 5, 2 ** 30]):
+        start = torch.tensor(at, dtype=torch.int32, device=dev)
+        bufs, o = {}, {}
+        for k, s in names.items():
+            bufs[k] = torch.full((g[s].numel() + 2 * 4096,), 3.0, device=dev)
+            o[k] = bufs[k][4096:4096 + g[s].numel()].view(g[s].shape)
+        work = [torch.full((b + 2 * 4096,), 7, dtype=torch.uint8, device=dev) for b in size]
+        ins = [g[k] for k in ("u", "dt", "a", "b", "c")]
+        kw = dict(d=g["d"], dt_bias=g["dt_bias"], z=g["z"], seq_start=start, s0=g["s0"])
+        sq.sq_ssm_scan(*ins, o["y"], s1=o["s1"], workspace=work[0][4096:4096 + size[0]], **kw)
+        sq.sq_ssm_scan_bwd(*ins, g["dy"], o["du"], o["ddt"], o["da"], o["db"], o["dc"], dz=o["dz"], dd=o["dd"], ddt_bias=o["ddt_bias"], ds1=g["ds1"],
+                           ds0=o["ds0"], workspace=work[1][4096:4096 + size[1]], **kw)
+        torch.cuda.synchronize()
+        for k, b in bufs.items():
+            assert bool((b[:4096] == 3).all()) and bool((b[-4096:] == 3).all()), (at, k)
+        for b, w in zip(size, work):
+            assert bool((w[:4096] == 7).all()) and bool((w[4096 + b:] == 7).all()), at
+
+
 def test_no_sequences_and_no_tokens(dev):
     C, N = 24, 16
     x = ref.ssm_inputs(C, N, 1, [10], 3, F32)
