@@ -17,7 +17,7 @@ BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 ARCH = os.environ.get("STEPQ_ARCH", "gfx950")
 
 SOURCES = ["api.cpp", "ops_api.cpp", "mix_api.cpp", "planner.cpp", "kernels.hip", "probe.hip", "norm.hip", "scan.hip", "scan_prep.hip",
-           "scan_bwd.hip", "conv.hip", "ssm.hip", "ssm_bwd.hip", "cache.hip"]
+           "scan_bwd.hip", "conv.hip", "conv_bwd.hip", "ssm.hip", "ssm_bwd.hip", "cache.hip"]
 
 
 def _hipcc() -> str:
@@ -39,7 +39,7 @@ def build(verbose: bool = False) -> str:
     step = ["-munsafe-fp-atomics", "-mno-amdgpu-ieee", "-fno-honor-nans"]
     # the norms, the scans, the convolution and the cache take NaN and infinities as inputs like others (and give what include/stepq.h
     # says), so they are compiled without the assumption that there are none
-    ieee = {"norm.hip", "scan.hip", "scan_prep.hip", "scan_bwd.hip", "conv.hip", "ssm.hip", "ssm_bwd.hip", "cache.hip"}
+    ieee = {"norm.hip", "scan.hip", "scan_prep.hip", "scan_bwd.hip", "conv.hip", "conv_bwd.hip", "ssm.hip", "ssm_bwd.hip", "cache.hip"}
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD_DIR, src.replace(".", "_") + ".o")
