@@ -274,15 +274,16 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm_step(const SsmParams p, int
 
 // ------------------------------------------------------------------ launches
 
-// The gradients always go by segments; of 128 tokens where they still give every CU several workgroups (less to join: 16 us instead of 27
-// of 850 for 8190 tokens of 4096 x 16).  The forward pass walks the tokens twice with segments, so it takes them only where whole
+// The gradients always go by segments: of 128 tokens where they still give every CU several workgroups (less to join: 16 us instead of 27
+// of 850 for 8190 tokens of 4096 x 16), of 32 where 64 would leave CUs without one (us with 32 / 64 tokens: 500 tokens of 256 x 16: 42/54, of
+// 1024 x 16: 42/55, of 256 x 128: 49/63; 1000 of 1024 x 16: 51/60; 250 of 4096 x 16: 49/61).  The forward pass walks the tokens twice with segments, so it takes them only where whole
 // sequences leave much of the GPU idle, below 352 workgroups (us with segments / without, bfloat16, 16 states, sequences x channels):
 //   1 x 4096 of 777: 41/89   1 x 4096 of 4000: 145/443   2 x 4096 of 2000: 142/335   3 x 4096 of 2000: 188/298   4 x 4096 of 2000: 239/308
 //   1 x 2048 of 2000: 50/218   4 x 2048 of 2000: 131/304   8 x 2048 of 1500: 179/247   8 x 1024 of 1500: 106/246   16 x 256 of 500: 37/85
 //   7 x 4096 of 1757 (448 workgroups): 440/376.
 // Sequences of fewer than 128 tokens have no room for segments.  A segment is at least 64 tokens, longer once 2048 workgroups are there.
 int ssm_segment_log(int64_t n_tokens, int64_t n_seq, int64_t blocks, bool backward) {
-    if (backward) return (n_tokens >> 7) * blocks >= 2048 ? 7 : 6;
+    if (backward) return (n_tokens >> 7) * blocks >= 2048 ? 7 : (n_tokens >> 6) * blocks >= 512 ? 6 : 5;
     if (n_seq < 1 || n_tokens / n_seq < 128 || n_seq * blocks >= 352) return -1;
     int log = 6;
     while (log < 12 && (n_tokens >> (log + 1)) * blocks >= 2048) ++log;

@@ -4,7 +4,7 @@
 //   dC_t = sum_c dp h_t,  dB_t = sum_c G_t delta u,  du = d dp + delta sum_n G B,  ddelta = sum_n G (a e h_{t-1} + u B),
 //   ddt = ddelta sigmoid(dt + bias),  da = sum_t G delta e h_{t-1},  dd = sum_t dp u,  dz = dy p silu'(z),  ds0 = e_1 G_1
 //
-// Nothing of the forward call is kept.  Sequences are cut into segments of 64 or 128 tokens.  k_ssm_ends finds, for all of them side by
+// Nothing of the forward call is kept.  Sequences are cut into segments of 32 to 128 tokens.  k_ssm_ends finds, for all of them side by
 // side, the state after a segment from a state of zero and the gradient before it from a gradient of zero, in one walk: the
 // latter is sum_t (e_1 ... e_t) C_t dp_t; it also keeps the state before every 8th token.  k_ssm_join turns the ends into the states
 // before and the gradients after the segments.  k_ssm_grad takes a segment's tiles of 8 tokens from the last to the first: the state
@@ -19,7 +19,7 @@
 // channel, written and read) instead of walking the segment again: 689 -> 604 us.  What staging makes stays in LDS, and the products of
 // two tokens are scheduled apart, or the loads of all eight move up: three waves a SIMD (168 registers, some 20 of them spilled) 557 us,
 // two (no spills) 605; in float32 and from 64 states on, where 26 to 44 would spill, two waves are faster (36 against 29 us for 515
-// tokens of 256 x 64).
+// tokens of 256 x 64 in segments of 64).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

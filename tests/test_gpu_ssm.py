@@ -166,6 +166,13 @@ def test_segments(lens, C, N, dev):
     check(C, N, 1, lens, F32, dev, s0=False, seed=6)
 
 
+def test_segments_of_64_tokens_of_the_gradients(dev):
+    """The calls of the other tests are small enough for segments of 32 tokens; this one is above the border."""
+    C, N, lens = 376, 128, [460, 1, 250]
+    assert (sum(lens) >> 6) * (C // 8) >= 512                  # workgroups of segments of 64
+    check(C, N, 1, lens, BF16, dev)
+
+
 def test_long_and_short_segments_of_the_gradients(dev):
     """A call that is large enough for segments of 128 tokens against its channels in four calls, whose segments have 64."""
     C, N, lens, parts = 2048, 16, [5000, 1, 3300], 4
