@@ -190,7 +190,7 @@ extern "C" sq_status sq_conv_step(const sq_conv_cfg* cfg, const sq_rows* x, cons
 namespace {
 
 struct SsmWork {                     // byte offsets of the workspace's parts
-    size_t hseg, kseg, dsum, htile, dtile, da, dd, bc, total;
+    size_t hseg, kseg, dsum, htile, dtile, dd, bc, total;
 };
 
 int64_t ssm_fwd_blocks(const sq_ssm_cfg& c) { return ssm_blocks(c.channels, c.n_groups, c.d_state); }
@@ -205,9 +205,9 @@ SsmWork ssm_work(const sq_ssm_cfg& c, bool backward, int log) {
         w.dsum = take(slots * size_t(c.channels) * 4);
         if (backward) {
             w.kseg = take(states);
-            w.htile = take((states << log) / kSsmTile);
-            w.dtile = take(((slots << log) / kSsmTile) * size_t(c.channels) * 4);
-            w.da = take(states);
+            const size_t tiles = (size_t(c.n_tokens) + kSsmTile - 1) / kSsmTile;
+            w.htile = take(tiles * size_t(c.channels) * size_t(c.d_state) * 4);
+            w.dtile = take(tiles * size_t(c.channels) * 4);
             w.dd = take(slots * 2 * size_t(c.channels) * 4);
             w.bc = take(size_t(ssm_grad_blocks(c.channels, c.n_groups, c.d_state)) * size_t(c.n_tokens) * 2 * size_t(c.d_state) * 4);
         }
@@ -328,7 +328,7 @@ extern "C" sq_status sq_ssm_scan_bwd(const sq_ssm_cfg* cfg, const sq_ssm_in* in,
     const SsmWork w = ssm_work(*cfg, true, log);
     SQ_TRY(check_work(d_work, work_bytes, w.total));
     auto f32 = [d_work](size_t o) { return reinterpret_cast<float*>(static_cast<char*>(d_work) + o); };
-    p.hseg = f32(w.hseg); p.kseg = f32(w.kseg); p.dsum = f32(w.dsum); p.htile = f32(w.htile); p.dtile = f32(w.dtile); p.da_part = f32(w.da); p.dd_part = f32(w.dd); p.bc_part = f32(w.bc);
+    p.hseg = f32(w.hseg); p.kseg = f32(w.kseg); p.dsum = f32(w.dsum); p.htile = f32(w.htile); p.dtile = f32(w.dtile); p.dd_part = f32(w.dd); p.bc_part = f32(w.bc);
     p.s0 = d_s0; p.ds1 = d_ds1; p.ds0 = d_ds0;
     p.da = out->d_da; p.dd = out->d_dd; p.ddt_bias = out->d_ddt_bias;
     const hipError_t e = launch_ssm_bwd(p, ck.vec, static_cast<hipStream_t>(stream));

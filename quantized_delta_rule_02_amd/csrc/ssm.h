@@ -14,11 +14,14 @@ struct SsmParams {
     const float* s0;                 // [n_seq][channels][d_state] or NULL
     float* s1;
     // workspace, per segment
-    float* hseg;                     // [slot][channels][d_state] state after the segment from zero, then the state before it
+    float* hseg;                     // [slot][channels][d_state] state after the segment from zero, then the state before it; the gradients'
+                                     // main kernel, its last reader, leaves the segment's sum of da there
     float* kseg;                     // backward: the same of the state's gradient, in the other direction
     float* dsum;                     // [slot][channels] sum of the steps
-    float* htile;                    // backward: [slot][tokens / 8][channels][d_state] state before every 8th token, from zero
-    float* dtile;                    // [slot][tokens / 8][channels] sum of the steps up to there
+    // State before a segment's tiles of 8 tokens but the first, from zero, and the sum of the steps up to there: of the tile that starts at
+    // token t in row t / 8.  Such a tile starts 8 tokens or more behind its sequence's start, so no two of them share a row.
+    float* htile;                    // backward: [(n_tokens + 7) / 8][channels][d_state]
+    float* dtile;                    // [(n_tokens + 7) / 8][channels]
     // backward
     Rows dy, du, ddt, db, dc, dz;
     const float* ds1;
@@ -26,7 +29,6 @@ struct SsmParams {
     float* da;
     float* dd;
     float* ddt_bias;
-    float* da_part;                  // [slot][channels][d_state]
     float* dd_part;                  // [slot][2][channels]: of dd and ddt_bias
     float* bc_part;                  // [block of channels][n_tokens][2][d_state]
     // one token of each request

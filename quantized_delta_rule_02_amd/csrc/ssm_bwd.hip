@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm_ends(const SsmParams p, int
         __syncthreads();
         for (int t8 = 0; t8 < nt; t8 += kTile) {
             if (there && t0 + t8 > 0) {                   // what k_ssm_grad starts its tiles from
-                const int64_t tile = ((slot << p.runs.log) + t0 + t8) / kTile;
+                const int64_t tile = (r.tok0 + t0 + t8) / kTile;
                 *reinterpret_cast<f32x4*>(p.htile + tile * p.channels * N + at) = h;
                 if (quarter == 0) p.dtile[tile * p.channels + bc.c0 + ch] = dsum;
             }
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(Grad<N>::kThreads, DT != SQ_DTYPE_F32 && N <= 
         f32x4 hl;
         float dl;
         auto fetch_state = [&](int tile) {
-            const int64_t i = (slot << p.runs.log) / kTile + tile;
+            const int64_t i = r.tok0 / kTile + tile;             // (r.tok0 + kTile tile) / kTile
             hl = load_states(p.htile, i * states + at, there);
             dl = there ? p.dtile[i * p.channels + bc.c0 + ch] : 0.f;
         };
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(Grad<N>::kThreads, DT != SQ_DTYPE_F32 && N <= 
         }
     }
     // the segment's sums (of zero for a slot without tokens)
-    if (there) *reinterpret_cast<f32x4*>(p.da_part + slot * states + at) = da;
+    if (there) *reinterpret_cast<f32x4*>(p.hseg + slot * states + at) = da;           // read above by this lane alone
     __syncthreads();
     if (tid < 2 * CB) {                                   // the threads of four channels in order
         const int which = tid / CB, c = tid % CB;
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(1024) k_ssm_sum(const SsmParams p, int64_t n_r
     const int lane = (int)threadIdx.x & 63, sub = (int)threadIdx.x >> 6;
     const int64_t states = (int64_t)p.channels * p.d_state, col = (int64_t)blockIdx.x * 64 + lane, c = col - states;
     const bool in_da = c < 0, in = c < 2 * (int64_t)p.channels;
-    const float* part = in_da ? p.da_part + col : p.dd_part + c;
+    const float* part = in_da ? p.hseg + col : p.dd_part + c;
     const int64_t row = in_da ? states : 2 * (int64_t)p.channels;
     float s = 0.f;
     if (in) {

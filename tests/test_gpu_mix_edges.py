@@ -1,0 +1,46 @@
+"""Calls of the convolution and the selective scan where their tiles, segments and alignments end, on the GPU against float64.
+
+The tolerances are those of test_gpu_conv.py and test_gpu_ssm.py (derived there) unless a test derives its own.
+"""
+import pytest
+import torch
+
+import _mix_ref as ref
+import quantized_delta_rule_02_amd as sq
+import test_gpu_conv as conv
+import test_gpu_ssm as ssm
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+NAMES = {F32: "f32", BF16: "bf16", F16: "f16"}
+
+
+@pytest.mark.parametrize("lead", (0, 3, 5))
+@pytest.mark.parametrize("N", (16, 128))
+def test_scan_gradients_of_many_short_sequences(N, lead, dev):
+    """Tiles of 8 tokens and segments of 32 that begin anywhere in the packed rows, each with states of its own before it."""
+    lens = [1, 9, 7, 8, 15, 16, 17, 0, 23, 25, 33, 31, 2, 41, 9, 0, 0, 65, 10, 11, 12, 13, 14] * 2
+    ssm.check(20, N, 1, lens, F32, dev, lead=lead, behind=2)
+    ssm.check(20, N, 1, lens, BF16, dev, lead=lead, seed=9)
+
+
+def test_scan_gradients_stay_in_their_workspace(dev):
+    """Exactly the bytes that the library asks for, fenced; what was there before does not matter."""
+    C, N, lens = 40, 16, [9, 1, 17, 0, 8, 33, 40, 2, 16, 25] * 20
+    T, n = sum(lens), len(lens)
+    g, start = ssm.put(ref.ssm_inputs(C, N, 1, lens, 5, F32), dev), ref.starts(lens).to(dev)
+    size = sq.sq_ssm_scan_bytes(F32, C, N, 1, n, T, backward=True)
+    outs = []
+    for fill in (0, 0x7f):
+        buf = torch.full((size + 2 * 4096,), fill, dtype=torch.uint8, device=dev)
+        o = {k: torch.empty_like(g[s]) for k, s in (("du", "u"), ("ddt", "dt"), ("da", "a"), ("db", "b"), ("dc", "c"), ("dz", "z"), ("dd", "d"),
+                                                    ("ddt_bias", "dt_bias"), ("ds0", "s0"))}
+        sq.sq_ssm_scan_bwd(g["u"], g["dt"], g["a"], g["b"], g["c"], g["dy"], o["du"], o["ddt"], o["da"], o["db"], o["dc"], d=g["d"], dt_bias=g["dt_bias"],
+                           z=g["z"], dz=o["dz"], dd=o["dd"], ddt_bias=o["ddt_bias"], seq_start=start, s0=g["s0"], ds1=g["ds1"], ds0=o["ds0"],
+                           workspace=buf[4096:4096 + size])
+        torch.cuda.synchronize()
+        assert bool((buf[:4096] == fill).all()) and bool((buf[4096 + size:] == fill).all())
+        outs.append(o)
+    for k in outs[0]:
+        assert torch.equal(outs[0][k], outs[1][k]), k
