@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm(const SsmParams p, int n_bl
     constexpr int CB = L::kBlockCh, NV = CB / 4, kItems = (TT * NV + kSsmThreads - 1) / kSsmThreads;
     constexpr int kRows = LOCAL ? 1 : 2, kBc = (TT * kRows * (N / 4) + kSsmThreads - 1) / kSsmThreads;
     __shared__ __attribute__((aligned(16))) float2 s_d[TT][CB];           // delta, delta u
-    __shared__ __attribute__((aligned(16))) float s_y[LOCAL ? 1 : TT][CB + L::kWaveCh];     // rows apart so that four tokens of a wave meet no bank twice
+    __shared__ __attribute__((aligned(16))) float s_y[LOCAL ? 1 : TT][CB + L::kPad];
     __shared__ f32x4 s_bc[kRows][TT][N / 4];
     const int tid = (int)threadIdx.x, blk = (int)blockIdx.x % n_blocks;
     const int64_t slot = (int)blockIdx.x / n_blocks;

@@ -146,10 +146,11 @@ struct Grad {
     static constexpr int kWaves = N == 8 ? 2 : N <= 64 ? 4 : 8, kThreads = kWaves * 64;
     static constexpr int kPer = N / 4, kWaveCh = 64 / kPer, CB = kWaves * kWaveCh;
     static constexpr int TS = 16;                         // tokens staged at a time
-    static constexpr int kPad = kWaveCh;                  // rows apart so that a wave's tokens meet no bank twice
+    static constexpr int kPad = (kWaveCh + 3) / 4 * 4;    // rows apart so that a wave's tokens meet no bank twice, and aligned to four elements
     static constexpr int NV = CB / 4, kItems = (TS * NV + kThreads - 1) / kThreads;
     static constexpr int kBc = (TS * 2 * kPer + kThreads - 1) / kThreads;
     static constexpr int kGroups = kThreads / NV;         // threads that share a channel in the sums over tokens
+    static_assert(CB % 4 == 0 && (CB + kPad) % 4 == 0, "rows are accessed four elements at a time");
 };
 
 // One token's v[0..3], of the lane's four states, summed over the wave's channels.  Each exchange joins two values' halves, so that

@@ -18,6 +18,9 @@ struct SsmLane {
     static constexpr int kPer = N / 4;                  // lanes of a channel
     static constexpr int kWaveCh = 64 / kPer;           // channels of a wave
     static constexpr int kBlockCh = kSsmWaves * kWaveCh;
+    static constexpr int kPad = (kWaveCh + 3) / 4 * 4;  // between rows of a tile: four tokens of a wave meet no bank twice, and rows
+                                                        // stay aligned to the four elements that are read from them at a time
+    static_assert(kBlockCh % 4 == 0 && (kBlockCh + kPad) % 4 == 0, "rows are accessed four elements at a time");
 };
 
 // ln(1 + e^x) = max(x, 0) + ln(1 + w), w = e^-|x|.  w comes from 2^y with the rounding of y = -|x| log2(e) put back (|x| + y ln 2 is
