@@ -296,15 +296,33 @@ hipError_t launch_ssm_join(const SsmParams& p, int directions, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Up to how many workgroups whole sequences of 64 tokens and more are staged 64 tokens at a time: as many as their LDS lets the GPU's 256 CUs of
+// 160 KB hold at once, each waiting at its own barriers; beyond that the workgroups that 32 tokens leave room for hide more.
+// us with 64 / 32 tokens, bfloat16, C x N = 65536 (64 workgroups a sequence), sequences x tokens:
+//    N = 8:    7 x 1757: 688/550   16 x 700: 477/336   64 x 188: 512/344   7 x 100: 38/27   1 x 100: 19/19
+//    N = 16:   7 x 1757: 415/444   8 x 1500: 324/350   12 x 1000: 299/248   64 x 188: 256/211   7 x 100: 21.7/21.9
+//    N = 32:   7 x 1757: 351/380   12 x 1000: 208/213   16 x 700: 175/183   64 x 188: 182/179   7 x 100: 19.5/19.7
+//    N = 64:   7 x 1757: 349/366   12 x 1000: 205/212   16 x 700: 173/178   64 x 188: 181/176   7 x 100: 19.0/19.7
+//    N = 128:  7 x 1757: 368/387   8 x 1500: 288/303   12 x 1000: 264/219   64 x 188: 228/183   7 x 100: 20.5/20.9
+// float32 is alike (7 x 1757: 748/584, 435/454, 366/401, 348/369, 378/391).  With 8 states one workgroup of 64 tokens fills a CU, and it is never
+// faster.  Sequences of a few tokens need no more than 32 (64 of 4 tokens: 30 us with 64, 19 with 32).
+template <int N>
+constexpr int64_t kSsmLong = N == 8 ? 0 : 256 * (160 * 1024 / int64_t(sizeof(float) * 64 * (3 * SsmLane<N>::kBlockCh + SsmLane<N>::kPad + 2 * N)));
+static_assert(kSsmLong<16> == 512 && kSsmLong<32> == 768 && kSsmLong<64> == 768 && kSsmLong<128> == 512, "workgroups that 160 KB hold");
+
 template <int DT, int N, bool VEC>
 static hipError_t scan_n(const SsmParams& p, hipStream_t s) {
     const int blocks = (int)ssm_blocks(p.channels, p.n_groups, N);
     if (p.runs.log < 0) {
-        // Long sequences leave one or two workgroups on a CU, each waiting at its own barriers: 64 tokens between them (7 sequences of 1757 x 4096 x 16:
-        // 355 us, 375 with 32, 408 with 16).  Short ones want many workgroups there, so little LDS (64 of 4 tokens: 30 us with 64, 19 with 32).
-        const dim3 grid((unsigned)((int64_t)p.runs.n_seq * blocks));
-        if (p.runs.n_tokens >= 64 * (int64_t)p.runs.n_seq) k_ssm<DT, N, VEC, false, 64><<<grid, kSsmThreads, 0, s>>>(p, blocks);
-        else k_ssm<DT, N, VEC, false, 32><<<grid, kSsmThreads, 0, s>>>(p, blocks);
+        const int64_t groups = (int64_t)p.runs.n_seq * blocks;
+        const dim3 grid((unsigned)groups);
+        if constexpr (kSsmLong<N> > 0) {
+            if (groups <= kSsmLong<N> && p.runs.n_tokens >= 64 * (int64_t)p.runs.n_seq) {
+                k_ssm<DT, N, VEC, false, 64><<<grid, kSsmThreads, 0, s>>>(p, blocks);
+                return hipGetLastError();
+            }
+        }
+        k_ssm<DT, N, VEC, false, 32><<<grid, kSsmThreads, 0, s>>>(p, blocks);
         return hipGetLastError();
     }
     const dim3 grid((unsigned)(run_slots(p.runs.n_tokens, p.runs.n_seq, p.runs.log) * blocks));

@@ -44,3 +44,24 @@ def test_scan_gradients_stay_in_their_workspace(dev):
         outs.append(o)
     for k in outs[0]:
         assert torch.equal(outs[0][k], outs[1][k]), k
+
+
+@pytest.mark.parametrize("N", (8, 16, 32, 64, 128))
+@pytest.mark.parametrize("dtype", (F32, BF16, F16), ids=NAMES.get)
+def test_scan_of_64_tokens_and_more_in_one_piece(N, dtype, dev):
+    """Too short for segments, long enough for the larger tiles: two whole blocks of channels and a part of a third, in fours and in ones."""
+    per = 1024 // N                                            # channels of a workgroup
+    for C, lens in ((2 * per + 4, [100, 64, 91, 127, 66]), (2 * per + 3, [65, 63, 128, 1, 96, 70])):
+        assert 64 * len(lens) <= sum(lens) < 128 * len(lens)
+        assert sq.sq_ssm_scan_bytes(dtype, C, N, 1, len(lens), sum(lens)) == 0
+        ssm.check(C, N, 1, lens, dtype, dev, grads=False, lead=2, behind=1)
+
+
+@pytest.mark.parametrize("n_seq", (30, 44))
+@pytest.mark.parametrize("N,C", ((8, 1536), (16, 768), (128, 96)))
+def test_scan_of_many_long_sequences(N, C, n_seq, dev):
+    """Enough workgroups to go without segments; 360 of them are staged 64 tokens at a time where their LDS allows it, 528 are not (nor with 8 states)."""
+    assert n_seq * (C * N // 1024) in (360, 528)
+    lens = [70 + 37 * i % 130 for i in range(n_seq)]
+    assert sum(lens) >= 128 * n_seq and sq.sq_ssm_scan_bytes(BF16, C, N, 1, n_seq, sum(lens)) == 0
+    ssm.check(C, N, 1, lens, BF16, dev, grads=False)
