@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) k_conv(const ConvParams p, int n_blo
                 float s = f.b[v];
 #pragma unroll
                 for (int j = 0; j < W; ++j) s = fmaf(f.w[v][j], x[u + j][v], s);
-                y[v] = SILU ? s * sigmoid<DT == SQ_DTYPE_F32>(s) : s;
+                y[v] = SILU ? s * sigmoid(s) : s;
             }
             Elems<DT, V> o;
             o.set(y);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_step(const ConvParams p, int 
         float s = f.b[v];
 #pragma unroll
         for (int j = 0; j < W; ++j) s = fmaf(f.w[v][j], e[j].at(v), s);
-        y[v] = SILU ? s * sigmoid<DT == SQ_DTYPE_F32>(s) : s;
+        y[v] = SILU ? s * sigmoid(s) : s;
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) e[j + 1].store(p.window, base + (int64_t)j * p.channels);

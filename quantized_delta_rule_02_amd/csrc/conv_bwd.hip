@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const ConvParams p, int n
                             float a = f.b[v];
 #pragma unroll
                             for (int j = 0; j < W; ++j) a = fmaf(f.w[v][j], x[u + j][v], a);
-                            const float sg = sigmoid<DT == SQ_DTYPE_F32>(a);
+                            const float sg = sigmoid(a);
                             g *= sg * fmaf(a, 1.f - sg, 1.f);
                             dp[W - 1 + u][v] = g;
                         }

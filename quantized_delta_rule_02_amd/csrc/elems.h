@@ -90,20 +90,13 @@ struct Elems {
     }
 };
 
-// exp(-z) from the hardware's 2^x.  EXACT: the rounding of z log2(e) is put back as a factor, so that its error does not grow with
-// |z| (up to 5e-6 of the value at 88 without); results that 16 bits round by 2^-12 or more need it not.  From a = 128 on 2^a is
-// infinity, and infinity times a remainder of zero or below would be NaN; far below -126 it is zero: there 2^a stays as it is.
-template <bool EXACT>
-__device__ __forceinline__ float exp_minus(float z) {
-    constexpr float l2e = 1.44269504089f, ln2 = 0.69314718056f;
-    const float a = -z * l2e;
-    const float e = __builtin_amdgcn_exp2f(a);
-    if constexpr (!EXACT) return e;
-    const float lo = fmaf(-z, l2e, -a);
-    return a < 128.f && a > -200.f ? fmaf(e, lo * ln2, e) : e;
+// 1 / (1 + exp(-z)) to 9 2^-24 of itself for |z| up to 64, with exp(-z) = 2^a (1 - r): a = -z log2(e) rounded, r = a ln 2 + z, exact but for ln 2's own
+// rounding (2^-28), so that the error does not grow with |z| by more than that.  Beyond 200 the power is zero or infinite either way, and r
+// stays small.  The reciprocal is the hardware's, off by at most one unit in the last place.  A NaN gives a number: every gate is
+// multiplied by z itself.  Rows of 16 bits have float32 results too (sums over tokens, gradients of states), so they get the same gates.
+__device__ __forceinline__ float sigmoid(float z) {
+    const float x = __builtin_amdgcn_fmed3f(z, -200.f, 200.f), a = -x * 1.44269504089f;
+    return __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_exp2f(a), 1.f - fmaf(a, 0.69314718056f, x), 1.f));
 }
-// 1 / (1 + exp(-z)); the reciprocal is the hardware's, off by at most one unit in the last place
-template <bool EXACT>
-__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + exp_minus<EXACT>(z)); }
 
 }  // namespace sq

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm(const SsmParams p, int n_bl
                 }
                 if (p.z.p) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] *= cz[i].at(j) * sigmoid<DT == SQ_DTYPE_F32>(cz[i].at(j));
+                    for (int j = 0; j < 4; ++j) y[j] *= cz[i].at(j) * sigmoid(cz[i].at(j));
                 }
                 Four<DT, VEC>::store(p.y.p, (tok0 + t0 + t) * p.y.stride + bc.c0 + c4, bc.n - c4, y);
             }
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm_step(const SsmParams p, int
     if (p.d) y = fmaf(p.d[c], eu.at(0), y);
     if (p.z.p) {
         const float z = ez.at(0);
-        y *= z * sigmoid<DT == SQ_DTYPE_F32>(z);
+        y *= z * sigmoid(z);
     }
     Elems<DT, 1> o;
     o.set(&y);

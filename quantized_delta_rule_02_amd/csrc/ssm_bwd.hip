@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm_ends(const SsmParams p, int
             }
             if (p.z.p) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) g[j] *= ez[i].at(j) * sigmoid<DT == SQ_DTYPE_F32>(ez[i].at(j));
+                for (int j = 0; j < 4; ++j) g[j] *= ez[i].at(j) * sigmoid(ez[i].at(j));
             }
 #pragma unroll
             for (int j = 0; j < 4; j += 2)
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(Grad<N>::kThreads, DT != SQ_DTYPE_F32 && N <= 
                     f32x4 sz;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        sz[j] = sigmoid<DT == SQ_DTYPE_F32>(rz[i].at(j));
+                        sz[j] = sigmoid(rz[i].at(j));
                         g[j] *= rz[i].at(j) * sz[j];
                     }
                     row4(&s_sz[t][c4]) = sz;

@@ -65,3 +65,63 @@ def test_scan_of_many_long_sequences(N, C, n_seq, dev):
     lens = [70 + 37 * i % 130 for i in range(n_seq)]
     assert sum(lens) >= 128 * n_seq and sq.sq_ssm_scan_bytes(BF16, C, N, 1, n_seq, sum(lens)) == 0
     ssm.check(C, N, 1, lens, BF16, dev, grads=False)
+
+
+# A gate's 1 / (1 + e^-z), |z| <= 64, in units of 2^-24 of its value: the hardware's 2^x and reciprocal 2 each, the exponent's remainder 3 (64 times the
+# 2^-28.4 by which float32's ln 2 is off, and its sum), two roundings.  So z s(z) is off by at most 11 units of itself; s (1 + z (1 - s)), with
+# products, sums and 1 - s (10 units of one), by at most 24 of s (1 + |z|).  One token, so no sums over tokens.
+UNIT = 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", (F32, BF16, F16), ids=NAMES.get)
+def test_conv_gradients_in_float32_carry_float32_gates(dtype, dev):
+    """dweight and dbias are float32 for rows of 16 bits too: the gate's exponent is not rounded to less."""
+    C = 4096
+    p = torch.linspace(-64.0, 64.0, C)                          # exactly the sum before the activation
+    one = torch.ones(1, C, dtype=dtype, device=dev)
+    weight, bias = torch.zeros(C, 2, device=dev), p.to(dev)
+    dw, db, dx = torch.empty_like(weight), torch.empty_like(bias), torch.empty_like(one)
+    sq.sq_conv_bwd(1.5 * one, weight, one, dx, dweight=dw, bias=bias, dbias=db)
+    z = p.double()
+    s = z.sigmoid()
+    want, size = s * (1 + z * (1 - s)), s * (1 + z.abs())
+    assert bool(((db.double().cpu() - want).abs() <= 24 * UNIT * size).all())
+    assert bool(((dw[:, 1].double().cpu() - 1.5 * want).abs() <= 25 * UNIT * 1.5 * size).all()) and not dw[:, 0].any()
+
+
+@pytest.mark.parametrize("dtype", (F32, BF16, F16), ids=NAMES.get)
+def test_scan_gradients_in_float32_carry_float32_gates(dtype, dev):
+    """The same of dd: dy z s(z) u."""
+    C, N = 4096, 16
+    z = torch.linspace(-64.0, 64.0, C)[None].to(dtype)
+    g = ssm.put(dict(ref.ssm_inputs(C, N, 1, [1], 5, dtype), z=z), dev)
+    one = torch.ones_like(g["u"])
+    o = {k: torch.empty_like(g[s]) for k, s in (("du", "u"), ("ddt", "dt"), ("da", "a"), ("db", "b"), ("dc", "c"), ("dz", "z"), ("dd", "d"))}
+    sq.sq_ssm_scan_bwd(g["u"], g["dt"], g["a"], g["b"], g["c"], one, o["du"], o["ddt"], o["da"], o["db"], o["dc"], d=g["d"], dt_bias=g["dt_bias"], z=g["z"],
+                       dz=o["dz"], dd=o["dd"])
+    want = (z.double() * z.double().sigmoid() * g["u"].double().cpu())[0]
+    assert bool(((o["dd"].double().cpu() - want).abs() <= 12 * UNIT * want.abs()).all())          # 11 and the product with u
+
+
+@pytest.mark.parametrize("dtype", (F32, BF16, F16), ids=NAMES.get)
+def test_gates_of_all_sizes_are_finite(dtype, dev):
+    """Sums before the activation where its exponential is infinite, zero or next to either.  Below 2^-126 a sigmoid may be lost: 88 x 2^-126 of a product."""
+    p = torch.tensor([float(s) * x for x in (0.0, 1.0, 20.0, 87.0, 88.0, 88.7, 88.8, 89.0, 100.0, 103.0, 104.0, 127.0, 128.0, 150.0, 200.0, 1e4, 1e30, 3e38)
+                      for s in (1, -1)])
+    C = p.numel()
+    one = torch.ones(1, C, dtype=dtype, device=dev)
+    weight, bias = torch.zeros(C, 2, device=dev), p.to(dev)
+    y, dx, db = torch.empty_like(one), torch.empty_like(one), torch.empty_like(bias)
+    sq.sq_conv(one, weight, y, bias=bias)
+    sq.sq_conv_bwd(one, weight, one, dx, bias=bias, dbias=db)
+    z, most = p.double(), torch.finfo(dtype).max
+    want = z * z.sigmoid()
+    fits = want.abs() <= most
+    half = 0.0 if dtype == F32 else torch.finfo(dtype).eps / 2
+    tiny = 2.0 ** -25 if dtype == F16 else 88 * 2.0 ** -126
+    assert bool(((y[0].double().cpu() - want).abs() <= (half + 12 * UNIT) * want.abs() + tiny)[fits].all())
+    want = z.sigmoid() * (1 + z * (1 - z.sigmoid()))
+    assert bool(((db.double().cpu() - want).abs() <= 24 * UNIT * z.sigmoid() * (1 + z.abs().clamp(max=20)) + 88 * 2.0 ** -126).all())
+    step, state = torch.zeros(1, 1, C, dtype=dtype, device=dev), torch.empty_like(y)
+    sq.sq_conv_step(one, weight, step, state, bias=bias)
+    assert torch.equal(state, y)
