@@ -406,6 +406,12 @@ def _dtype_code(dtype) -> int:
     return code
 
 
+def _fits(*numbers):
+    """Refuses what a 32-bit field of a configuration does not hold (ctypes would keep its low bits: another, smaller call)."""
+    if max(numbers) > 0x7fffffff or min(numbers) < -0x80000000:
+        raise ValueError(f"{[n for n in numbers if not -0x80000000 <= n <= 0x7fffffff][0]}: sizes are numbers of 32 bits")
+
+
 _raw_stream = None           # (device index) -> handle of its current stream, and the current device's index
 
 
@@ -507,11 +513,13 @@ def _scan_cfg(form, q, v, seq_start):
             raise ValueError("seq_start must hold n_seq + 1 offsets")
         n_seq = seq_start.numel() - 1
         start = _dev(seq_start, torch.int32, n_seq + 1, "seq_start")
+    _fits(form, H, Hk, dk, dv, n_seq)
     return _lib.SqScanCfg(int(form), _dtype_code(q.dtype), H, Hk, dk, dv, n_seq, T, start)
 
 
 def sq_delta_scan_bytes(form, dtype, n_heads, n_heads_k, d_k, d_v, n_seq, n_tokens, backward=False) -> int:
     """Workspace bytes of sq_delta_scan (or of sq_delta_scan_bwd) for arrays of these sizes."""
+    _fits(form, n_heads, n_heads_k, d_k, d_v, n_seq)
     cfg = _lib.SqScanCfg(int(form), _dtype_code(dtype), n_heads, n_heads_k, d_k, d_v, n_seq, n_tokens, None)
     n = c_size_t(0)
     _check(_lib.load().sq_delta_scan_bytes(byref(cfg), int(backward), byref(n)), "sq_delta_scan_bytes")
@@ -579,6 +587,7 @@ class _NormCall:
         return None if t is None else _plain(t, (self.d,), self.device, name)
 
     def cfg(self, dtype, dtype_out, kind, act, eps, res_scale, out_scale):
+        _fits(kind, act, self.inner, self.d)
         return byref(_lib.SqNormCfg(_dtype_code(dtype), _dtype_code(dtype_out), kind, act, self.outer,
                                     self.inner, self.d, eps, res_scale, out_scale))
 
@@ -590,6 +599,7 @@ class _NormCall:
 
 def sq_norm_bytes(n_rows, d) -> int:
     """Workspace bytes of the norms' backward passes over n_rows rows of d elements."""
+    _fits(d)
     n = c_size_t(0)
     _check(_lib.load().sq_norm_bytes(int(n_rows), int(d), byref(n)), "sq_norm_bytes")
     return n.value
@@ -682,12 +692,14 @@ def _slots(slots, n, device):
 def _conv_cfg(x, weight, act, n_seq, start):
     dev = _first(x, 2, "[tokens, channels]", "x")
     _first(weight, 2, "[channels, width]", "weight")
-    T, C = x.shape
-    return _lib.SqConvCfg(_dtype_code(x.dtype), int(act), C, weight.shape[1], n_seq, T, start), dev
+    (T, C), W = x.shape, weight.shape[1]
+    _fits(act, C, W, n_seq)
+    return _lib.SqConvCfg(_dtype_code(x.dtype), int(act), C, W, n_seq, T, start), dev
 
 
 def sq_conv_bytes(dtype, channels, width, n_seq, n_tokens) -> int:
     """Workspace bytes of sq_conv_bwd for arrays of these sizes."""
+    _fits(channels, width, n_seq)
     cfg = _lib.SqConvCfg(_dtype_code(dtype), SQ_ACT_NONE, channels, width, n_seq, n_tokens, None)
     n = c_size_t(0)
     _check(_lib.load().sq_conv_bytes(byref(cfg), byref(n)), "sq_conv_bytes")
@@ -753,6 +765,7 @@ class _SsmCall:
         self.N, self.G = N, G = a.shape[1], b.shape[1]
         self.dtype = u.dtype
         self.n_seq, start = (0, None) if step else _seqs(seq_start, dev)
+        _fits(C, N, G, self.n_seq)
         self.cfg = _lib.SqSsmCfg(_dtype_code(u.dtype), C, N, G, int(bool(softplus)), self.n_seq, T, start)
         self.inputs = _lib.SqSsmIn(self.rows(u, "u"), self.rows(dt, "dt"), self.bc(b, "b"), self.bc(c, "c"), self.rows(z, "z"),
                                    self.vec(a, (C, N), "a"), self.vec(d, (C,), "d"), self.vec(dt_bias, (C,), "dt_bias"))
@@ -780,6 +793,7 @@ class _SsmCall:
 
 def sq_ssm_scan_bytes(dtype, channels, d_state, n_groups, n_seq, n_tokens, backward=False) -> int:
     """Workspace bytes of sq_ssm_scan (or of sq_ssm_scan_bwd) for arrays of these sizes."""
+    _fits(channels, d_state, n_groups, n_seq)
     cfg = _lib.SqSsmCfg(_dtype_code(dtype), channels, d_state, n_groups, 1, n_seq, n_tokens, None)
     n = c_size_t(0)
     _check(_lib.load().sq_ssm_scan_bytes(byref(cfg), int(backward), byref(n)), "sq_ssm_scan_bytes")
@@ -832,6 +846,7 @@ def _cache_call(rows, codes, scales, slots, format, name):
     S, groups = scales.shape
     if groups < 1 or d % groups:
         raise ValueError(f"scales: {groups} a row of {d} elements")
+    _fits(format, d)
     cfg = _lib.SqCacheCfg(_dtype_code(rows.dtype), int(format), d, d // groups, R, S)
     if codes.dtype not in (torch.uint8, torch.int8):
         raise TypeError(f"codes must be uint8 or int8, got {codes.dtype}")
