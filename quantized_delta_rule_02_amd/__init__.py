@@ -416,11 +416,13 @@ _raw_stream = None           # (device index) -> handle of its current stream, a
 
 
 def _stream_calls():
-    """torch's own lookups behind torch.cuda.current_stream and current_device, without the objects they build (2 us a call)."""
+    """torch's own lookups behind torch.cuda.current_stream and current_device, without the objects they build (2 us a call); the public
+    calls in a torch that has none of these names."""
     global _raw_stream
     import torch
     torch.cuda.current_stream()                          # initialises torch's side
-    _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    raw, current = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    _raw_stream = (raw or (lambda index: torch.cuda.current_stream(index).cuda_stream), current or torch.cuda.current_device)
     return _raw_stream
 
 

@@ -51,3 +51,18 @@ def test_tensors_beyond_32_bits_are_refused():
                  lambda: sq.sq_cache_read(x, Claims(8, 4), x)):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_stream_lookup_without_torchs_short_calls(monkeypatch):
+    """The handle of the current stream and the current device come from torch's public calls where the short ones are missing."""
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(sq, "_raw_stream", None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    got = []
+    sq._call(lambda *args: got.append(args) or 0, "call", torch.device("cuda:3"), None, 5)
+    assert got == [(5, 77)]
