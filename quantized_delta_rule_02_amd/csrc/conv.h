@@ -27,9 +27,10 @@ struct ConvParams {
 };
 
 constexpr int kConvBwdLog = 6, kConvBwdRuns = 8;     // log2 of the tokens of a wave and of a workgroup of the backward pass
-int conv_run_log(int64_t n_tokens, int64_t n_seq, int32_t channels);    // of the forward pass
-// `vec`: every array allows the accesses of `vec` elements at a time (conv_vec) that the kernels make.
-int conv_vec(int32_t dtype);
+constexpr int kConvLog = 4;                          // of a run of the forward pass
+// Bytes that a thread accesses at a time, forward, backward and for one token: adjacent channels of a row, as far as registers allow.
+constexpr int kConvBytes = 8, kConvBwdBytes = 4, kConvStepBytes = 16;
+// `vec`: every array and the channels allow these accesses; otherwise they are of one element.
 hipError_t launch_conv(const ConvParams& p, bool vec, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvParams& p, bool vec, hipStream_t s);
 hipError_t launch_conv_step(const ConvParams& p, bool vec, hipStream_t s);

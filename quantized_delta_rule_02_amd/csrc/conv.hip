@@ -114,9 +114,6 @@ __global__ void __launch_bounds__(kThreads) k_conv_step(const ConvParams p, int 
 
 // ------------------------------------------------------------------ launches
 
-int conv_vec(int32_t dtype) { return dtype == SQ_DTYPE_F32 ? 4 : 8; }
-int conv_run_log(int64_t, int64_t, int32_t) { return 4; }
-
 template <int DT, int W, int V>
 static hipError_t fwd_n(const ConvParams& p, hipStream_t s) {
     const int n_blocks = (p.channels + kThreads * V - 1) / (kThreads * V);
@@ -134,7 +131,7 @@ static hipError_t step_n(const ConvParams& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_conv(const ConvParams& p, bool vec, hipStream_t s) { SQ_CONV_DISPATCH(fwd_n, 4, 2, p, s); }
-hipError_t launch_conv_step(const ConvParams& p, bool vec, hipStream_t s) { SQ_CONV_DISPATCH(step_n, 8, 4, p, s); }
+hipError_t launch_conv(const ConvParams& p, bool vec, hipStream_t s) { SQ_CONV_DISPATCH(fwd_n, kConvBytes, p, s); }
+hipError_t launch_conv_step(const ConvParams& p, bool vec, hipStream_t s) { SQ_CONV_DISPATCH(step_n, kConvStepBytes, p, s); }
 
 }  // namespace sq

@@ -182,7 +182,7 @@ static hipError_t bwd_n(const ConvParams& p, int64_t slots, hipStream_t s) {
     else k_conv_bwd<DT, W, V, false><<<grid, kThreads, 0, s>>>(p, n_blocks);
     return hipGetLastError();
 }
-static hipError_t launch_runs(const ConvParams& p, bool vec, int64_t slots, hipStream_t s) { SQ_CONV_DISPATCH(bwd_n, 2, 1, p, slots, s); }
+static hipError_t launch_runs(const ConvParams& p, bool vec, int64_t slots, hipStream_t s) { SQ_CONV_DISPATCH(bwd_n, kConvBwdBytes, p, slots, s); }
 
 hipError_t launch_conv_bwd(const ConvParams& p, bool vec, hipStream_t s) {
     const int64_t slots = p.runs.n_seq > 0 ? run_slots(p.runs.n_tokens, p.runs.n_seq, p.runs.log) : 0;

@@ -33,7 +33,7 @@ __device__ __forceinline__ void inputs_before(const ConvParams& p, const RunAt& 
     }
 }
 
-// `fn` for the call's taps, type and alignment: V16 or V32 elements a thread (16-bit types, float32), one where the arrays do not allow it.
+// `fn` for the call's taps, type and alignment: BYTES a thread, or one element where the arrays do not allow it.
 #define SQ_CONV_WIDTH(fn, DT, V, ...)                                \
     switch (p.width) {                                               \
         case 2: return fn<DT, 2, V>(__VA_ARGS__);                    \
@@ -45,13 +45,13 @@ __device__ __forceinline__ void inputs_before(const ConvParams& p, const RunAt& 
         case 8: return fn<DT, 8, V>(__VA_ARGS__);                    \
         default: return hipErrorInvalidValue;                        \
     }
-#define SQ_CONV_DISPATCH(fn, V16, V32, ...)                                              \
+#define SQ_CONV_DISPATCH(fn, BYTES, ...)                                                 \
     do {                                                                                 \
-        if (p.dtype == SQ_DTYPE_BF16 && vec) SQ_CONV_WIDTH(fn, SQ_DTYPE_BF16, V16, __VA_ARGS__) \
+        if (p.dtype == SQ_DTYPE_BF16 && vec) SQ_CONV_WIDTH(fn, SQ_DTYPE_BF16, (BYTES) / 2, __VA_ARGS__) \
         if (p.dtype == SQ_DTYPE_BF16) SQ_CONV_WIDTH(fn, SQ_DTYPE_BF16, 1, __VA_ARGS__)    \
-        if (p.dtype == SQ_DTYPE_F16 && vec) SQ_CONV_WIDTH(fn, SQ_DTYPE_F16, V16, __VA_ARGS__) \
+        if (p.dtype == SQ_DTYPE_F16 && vec) SQ_CONV_WIDTH(fn, SQ_DTYPE_F16, (BYTES) / 2, __VA_ARGS__) \
         if (p.dtype == SQ_DTYPE_F16) SQ_CONV_WIDTH(fn, SQ_DTYPE_F16, 1, __VA_ARGS__)      \
-        if (vec) SQ_CONV_WIDTH(fn, SQ_DTYPE_F32, V32, __VA_ARGS__)                        \
+        if (vec) SQ_CONV_WIDTH(fn, SQ_DTYPE_F32, (BYTES) / 4, __VA_ARGS__)                \
         SQ_CONV_WIDTH(fn, SQ_DTYPE_F32, 1, __VA_ARGS__)                                   \
     } while (0)
 

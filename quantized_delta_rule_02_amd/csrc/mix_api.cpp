@@ -116,8 +116,8 @@ extern "C" sq_status sq_conv(const sq_conv_cfg* cfg, const sq_rows* x, const flo
     SQ_TRY(check_start(cfg->n_seq, cfg->d_seq_start));
     SQ_TRY(check_f32(d_weight, "weight", 4));
     SQ_TRY(check_optional(d_bias, "bias"));
-    ConvParams p = conv_params(*cfg, conv_run_log(cfg->n_tokens, cfg->n_seq, cfg->channels), d_weight, d_bias);
-    RowCheck ck{cfg->dtype, cfg->n_tokens, conv_vec(cfg->dtype)};
+    ConvParams p = conv_params(*cfg, kConvLog, d_weight, d_bias);
+    RowCheck ck{cfg->dtype, cfg->n_tokens, kConvBytes / int(esize(cfg->dtype))};
     p.x = ck(x, "x", cfg->channels, cfg->n_tokens > 0);
     p.y = ck(y, "y", cfg->channels, cfg->n_tokens > 0);
     ck.plain(d_s0, "s0");
@@ -141,7 +141,7 @@ extern "C" sq_status sq_conv_bwd(const sq_conv_cfg* cfg, const sq_rows* x, const
     SQ_TRY(check_optional(d_dweight, "dweight"));
     SQ_TRY(check_optional(d_dbias, "dbias"));
     ConvParams p = conv_params(*cfg, kConvBwdRuns, d_weight, d_bias);
-    RowCheck ck{cfg->dtype, cfg->n_tokens, conv_vec(cfg->dtype)};
+    RowCheck ck{cfg->dtype, cfg->n_tokens, kConvBwdBytes / int(esize(cfg->dtype))};
     const bool rows = cfg->n_tokens > 0 && cfg->n_seq > 0;
     p.x = ck(x, "x", cfg->channels, rows);
     p.dy = ck(dy, "dy", cfg->channels, rows);
@@ -174,7 +174,7 @@ extern "C" sq_status sq_conv_step(const sq_conv_cfg* cfg, const sq_rows* x, cons
         return SQ_ERR_ARG;
     }
     ConvParams p = conv_params(*cfg, 0, d_weight, d_bias);
-    RowCheck ck{cfg->dtype, cfg->n_tokens, conv_vec(cfg->dtype)};
+    RowCheck ck{cfg->dtype, cfg->n_tokens, kConvStepBytes / int(esize(cfg->dtype))};
     p.x = ck(x, "x", cfg->channels, true);
     p.y = ck(y, "y", cfg->channels, true);
     if (!d_window && ck.st == SQ_OK) { set_error("window is NULL"); return SQ_ERR_ARG; }

@@ -125,3 +125,39 @@ def test_gates_of_all_sizes_are_finite(dtype, dev):
     step, state = torch.zeros(1, 1, C, dtype=dtype, device=dev), torch.empty_like(y)
     sq.sq_conv_step(one, weight, step, state, bias=bias)
     assert torch.equal(state, y)
+
+
+@pytest.mark.parametrize("C", (2, 4, 6, 12, 258, 2052, 4100))
+@pytest.mark.parametrize("dtype", (F32, BF16, F16), ids=NAMES.get)
+def test_conv_channels_that_are_no_multiple_of_16_bytes(C, dtype, dev):
+    conv.check(C, 4, [3, 40, 0, 1], dtype, dev)
+
+
+@pytest.mark.parametrize("pad,shift", ((4, 0), (4, 4), (2, 0), (2, 2), (6, 4), (10, 2), (1, 0)))
+@pytest.mark.parametrize("dtype", (F32, BF16, F16), ids=NAMES.get)
+def test_conv_rows_of_wider_arrays_at_4_and_8_bytes(pad, shift, dtype, dev):
+    conv.check(52, 4, [5, 37], dtype, dev, pad=pad, shift=shift)
+
+
+@pytest.mark.parametrize("shift", (1, 2, 4))
+def test_conv_states_that_are_aligned_less_than_the_rows(shift, dev):
+    C, W, lens = 16, 4, [20, 2]
+    x = ref.conv_inputs(C, W, lens, 3, BF16)
+    g, start = {k: v.to(dev) for k, v in x.items()}, ref.starts(lens).to(dev)
+
+    def moved(t):
+        flat = torch.full((t.numel() + 2 * 8,), 7.0, dtype=t.dtype, device=dev)
+        flat[shift:shift + t.numel()] = t.reshape(-1)
+        return flat[shift:shift + t.numel()].view(t.shape), flat
+
+    def run(place):
+        s0, s1, ds1, ds0 = (place(g[k])[0] for k in ("s0", "s0", "ds1", "ds1"))
+        y, dx, dw = torch.empty_like(g["x"]), torch.empty_like(g["x"]), torch.empty_like(g["weight"])
+        sq.sq_conv(g["x"], g["weight"], y, bias=g["bias"], seq_start=start, s0=s0, s1=s1)
+        sq.sq_conv_bwd(g["x"], g["weight"], g["dy"], dx, dweight=dw, bias=g["bias"], seq_start=start, s0=s0, ds1=ds1, ds0=ds0)
+        window, step = place(g["s0"])[0], torch.empty_like(g["x"][:2])
+        sq.sq_conv_step(g["x"][:2], g["weight"], window, step, bias=g["bias"])
+        return [t.clone() for t in (y, s1, dx, dw, ds0, window, step)]
+
+    for a, b in zip(run(lambda t: (t.clone(), None)), run(moved)):
+        assert torch.equal(a, b)
