@@ -398,8 +398,8 @@ sq_status sq_norm_out_bwd(const sq_norm_cfg* cfg, const sq_rows* y, const sq_row
  * sq_conv_step y may be x's own array.
  * x, y, the states and all their gradients have the type cfg->dtype; weight [channels][width] and bias [channels] (NULL = 0) are
  * float32, and so is the arithmetic; each output is rounded once.  Row arrays: element (token, c) at d_ptr[token * stride + c], any
- * stride of at least `channels`.  Where addresses, strides and channels are multiples of 8 bytes (sq_conv), 4 (sq_conv_bwd) or 16 (sq_conv_step),
- * rows are accessed that many bytes at a time, otherwise element by element.
+ * stride of at least `channels`.  Where addresses, strides and channels are multiples of 8 bytes (sq_conv) or 4 (sq_conv_bwd, sq_conv_step), rows
+ * are accessed that many bytes at a time, otherwise element by element.
  *
  * sq_conv_bwd: from dy and d_ds1 (of the final states, NULL = zero): dx, and, where not NULL, d_dweight, d_dbias and d_ds0.  Sums over
  * tokens are taken in a fixed order through a workspace of sq_conv_bytes bytes, under the rules of the scan's (used if d_dweight or

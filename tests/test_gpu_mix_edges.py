@@ -161,3 +161,10 @@ def test_conv_states_that_are_aligned_less_than_the_rows(shift, dev):
 
     for a, b in zip(run(lambda t: (t.clone(), None)), run(moved)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("C", (1, 2, 6, 257, 514, 4098))
+@pytest.mark.parametrize("dtype", (F32, BF16, F16), ids=NAMES.get)
+def test_conv_step_of_few_and_odd_channels(C, dtype, dev):
+    conv.test_step(3, C, dtype, dev)
+    conv.test_step(8, C, dtype, dev)
