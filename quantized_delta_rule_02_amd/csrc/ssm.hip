@@ -276,15 +276,25 @@ __global__ void __launch_bounds__(kSsmThreads) k_ssm_step(const SsmParams p, int
 
 // The gradients always go by segments: of 128 tokens where they still give every CU several workgroups (less to join: 16 us instead of 27
 // of 850 for 8190 tokens of 4096 x 16), of 32 where 64 would leave CUs without one (us with 32 / 64 tokens: 500 tokens of 256 x 16: 42/54, of
-// 1024 x 16: 42/55, of 256 x 128: 49/63; 1000 of 1024 x 16: 51/60; 250 of 4096 x 16: 49/61).  The forward pass walks the tokens twice with segments, so it takes them only where whole
-// sequences leave much of the GPU idle, below 352 workgroups (us with segments / without, bfloat16, 16 states, sequences x channels):
-//   1 x 4096 of 777: 41/89   1 x 4096 of 4000: 145/443   2 x 4096 of 2000: 142/335   3 x 4096 of 2000: 188/298   4 x 4096 of 2000: 239/308
-//   1 x 2048 of 2000: 50/218   4 x 2048 of 2000: 131/304   8 x 2048 of 1500: 179/247   8 x 1024 of 1500: 106/246   16 x 256 of 500: 37/85
-//   7 x 4096 of 1757 (448 workgroups): 440/376.
-// Sequences of fewer than 128 tokens have no room for segments.  A segment is at least 64 tokens, longer once 2048 workgroups are there.
+// 1024 x 16: 42/55, of 256 x 128: 49/63; 1000 of 1024 x 16: 51/60; 250 of 4096 x 16: 49/61).
+//
+// The forward pass walks the tokens twice with segments and takes two launches more, so it takes them only where whole sequences leave much of the GPU
+// idle for long.  With g workgroups of whole sequences of L tokens, a sequence takes 0.115 L us whatever g is, up to one a CU, and segments 0.0004 g L
+// and 20 us more: L (288 - g) >= 50000.  Above 256 CUs have two and take longer (from 1563 tokens on), from 352 on segments cost more at equal lengths (us with
+// segments / without, bfloat16, 16 states, sequences x channels of tokens; 256 x 16 states are 4 workgroups):
+//   1 x 4096 of 160: 27/21, 192: 27/25, 224: 26/29, 320: 28/39, 777: 41/89, 4000: 137/448
+//   2 x 4096 of 192: 29/26, 256: 29/32, 320: 35/39, 2000: 127/228      8 x 1024 of 224: 33/29, 256: 35/32, 320: 35/40, 1500: 98/170
+//   40 x 256 of 150: 34/22, 256: 42/33, 320: 43/40, 400: 49/49         3 x 4096 of 2000: 174/229
+//   4 x 4096 of 160: 35/23, 400: 64/51, 2000: 222/231                  8 x 2048 of 1500: 173/174
+//   5 x 4096 of 2000: 280/321    80 x 256 of 400: 75/66                6 x 4096 of 1757: 303/284    7 x 4096 of 1757: 347/286
+// Other numbers of states are alike (C x N = 65536, 1 x 4000, 3 x 2000, 7 x 1757: N = 8: 186/618, 254/330, 508/382; N = 32: 123/387, 156/201, 308/243; N = 64:
+// 116/364, 152/189, 300/235; N = 128: 120/403, 158/209, 307/251).  The rule goes by the mean, since the lengths are on the device: one long sequence among
+// many short ones goes without segments (one of 8000 beside 63 of 8 tokens of 4096 x 16: 1035 us, 247 with them; in a call of its own 233).
+// A segment is at least 64 tokens, longer once 2048 workgroups are there.
 int ssm_segment_log(int64_t n_tokens, int64_t n_seq, int64_t blocks, bool backward) {
     if (backward) return (n_tokens >> 7) * blocks >= 2048 ? 7 : (n_tokens >> 6) * blocks >= 512 ? 6 : 5;
-    if (n_seq < 1 || n_tokens / n_seq < 128 || n_seq * blocks >= 352) return -1;
+    const int64_t groups = n_seq * blocks, left = groups < 256 ? 288 - groups : 32;
+    if (n_seq < 1 || groups >= 352 || n_tokens / n_seq * left < 50000) return -1;
     int log = 6;
     while (log < 12 && (n_tokens >> (log + 1)) * blocks >= 2048) ++log;
     return log;

@@ -168,3 +168,13 @@ def test_conv_states_that_are_aligned_less_than_the_rows(shift, dev):
 def test_conv_step_of_few_and_odd_channels(C, dtype, dev):
     conv.test_step(3, C, dtype, dev)
     conv.test_step(8, C, dtype, dev)
+
+
+@pytest.mark.parametrize("C,N,lens", ((8, 16, [175]), (8, 16, [173]), (40, 128, [190, 178, 0, 400]), (40, 128, [190, 178, 0, 353]), (24, 64, [130] * 9 + [900])), ids=str)
+def test_scan_at_the_border_of_segments(C, N, lens, dev):
+    """Mean lengths on both sides of where whole sequences go in one piece, and a long one among short ones."""
+    g = len(lens) * -(-C // (1024 // N))                       # workgroups of whole sequences
+    cut = sum(lens) // len(lens) * (288 - g) >= 50000
+    assert (sq.sq_ssm_scan_bytes(F32, C, N, 1, len(lens), sum(lens)) > 0) == cut
+    ssm.check(C, N, 1, lens, F32, dev, grads=False)
+    ssm.check(C, N, 1, lens, BF16, dev, grads=False, seed=4)
