@@ -434,7 +434,10 @@ sq_status sq_conv_step(const sq_conv_cfg* cfg, const sq_rows* x, const float* d_
  * output is rounded once.  d_a and the states are aligned to 16 bytes.  Rows that allow accesses of four elements (addresses,
  * strides, channels / n_groups) are accessed so, others element by element.  d_s0 and d_s1 may be the same array; no other two
  * arrays may overlap.  Few long sequences are cut into segments that run side by side (a choice by the call's sizes alone); the
- * result agrees with the token by token order to float32 rounding.  Nothing depends on what else runs (no atomics, fixed orders).
+ * result agrees with the token by token order to float32 rounding for decays of at most one (delta a <= 0), and for larger ones as long
+ * as no product of successive decays of a segment (at most 4096 tokens, 128 in the gradients) leaves float32's range; beyond that what
+ * is finite token by token may not be.  The choice goes by the mean length: a sequence far longer than the others of its call is
+ * walked in one piece beside them, and is faster in a call of its own.  Nothing depends on what else runs (no atomics, fixed orders).
  * A result that the formula makes NaN or infinite is not finite here either.  Such a value in a channel's inputs leaves the other
  * channels and the other sequences as they are, but for the gradients of b and c of its group in its sequence, sums over channels.
  *

@@ -178,3 +178,17 @@ def test_scan_at_the_border_of_segments(C, N, lens, dev):
     assert (sq.sq_ssm_scan_bytes(F32, C, N, 1, len(lens), sum(lens)) > 0) == cut
     ssm.check(C, N, 1, lens, F32, dev, grads=False)
     ssm.check(C, N, 1, lens, BF16, dev, grads=False, seed=4)
+
+
+@pytest.mark.parametrize("lens", ([300, 290], [20, 90]), ids=str)
+def test_scan_with_decays_above_one(lens, dev, monkeypatch):
+    """Rates of both signs up to 0.2.  A channel's steps average at most 0.37, so an exponent grows by 0.074 a token, and a step's error of 32 units
+    makes 2.4 units of the whole a token: the tolerance has 6."""
+    made = ref.ssm_inputs
+
+    def inputs(C, N, *args, **kw):
+        return dict(made(C, N, *args, **kw), a=(0.2 * (ref.rnd(C, N, seed=77)).clamp(-1, 1)).float())
+
+    monkeypatch.setattr(ref, "ssm_inputs", inputs)
+    ssm.check(24, 16, 1, lens, F32, dev)
+    ssm.check(24, 64, 2, lens, BF16, dev, seed=3)
