@@ -6,8 +6,9 @@
 // with the last W - 1 inputs in registers; the only inputs read twice are the W - 1 before each run.  Runs start at a sequence's
 // start, so no run holds two sequences, and the run that reads s0 is also the one that writes s1 (each thread its own channels,
 // after its reads), so that both may be the same array.  12301 tokens of 8192 channels in bfloat16, four taps, new inputs every pass:
-// 84 us, 4.8 TB/s (a copy: 6.0).  Four channels a thread (8-byte accesses) leave 62 registers, so that 8 waves a SIMD hide the
+// 82 us, 4.9 TB/s (a copy: 6.0).  Four channels a thread (8-byte accesses) leave 62 registers, so that 8 waves a SIMD hide the
 // latency: eight channels took 97 us on one set of inputs, four 85.  Runs of 16 tokens with 8 loads in flight: 82 us, of 32: 86, of 8: 92.
+// Single elements, where strides or channels do not allow 8 bytes: 61 us where four take 48 (8190 tokens of 8192 channels, one set of inputs).
 #include <hip/hip_runtime.h>
 
 #include "conv_dev.h"

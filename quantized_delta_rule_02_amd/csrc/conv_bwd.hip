@@ -3,9 +3,10 @@
 //   p_t = bias + sum_j w_j x_{t - W + 1 + j},   y_t = act(p_t)
 //   dp = dy act'(p),  dx_t = sum_j w_j dp_{t + W - 1 - j} (+ ds1),  dw_j = sum_t dp_t x_{t - W + 1 + j},  dbias = sum_t dp_t
 //
-// They are bound by the vector unit, 37 instructions an element (p again, its derivative, W products each for dx and
-// dweight) with 69 to 80 % of its time used: 8190 tokens of 8192 channels 96 us, floor by memory 67.  Two channels a thread (82
-// registers) 89 us, four 97; runs of 64 tokens a wave 87 us, of 32: 89, of 16: 97 (W - 1 more steps each).
+// They are bound by the vector unit, 39 instructions an element (p again, its derivative, W products each for dx and
+// dweight) with 73 % of its time used, beside memory: 8190 tokens of 8192 channels 95 us, floor by memory 67.  Measured at 37 instructions
+// (gates of fewer digits): two channels a thread (82 registers) 89 us, four 97; runs of 64 tokens a wave 87 us, of 32: 89, of 16: 97
+// (W - 1 more steps each).  Single elements: 126 us where two take 95.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

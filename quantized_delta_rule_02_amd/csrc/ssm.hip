@@ -4,9 +4,9 @@
 //
 // There is no matrix product in it: the decay differs from state to state of every channel.  What bounds it is the vector unit,
 // one exponential (at half the rate: 8 cycles a wave) and four operations (4 cycles each) for every token, channel and state, 123 us for
-// 12301 tokens of 4096 channels of 16 states where memory needs 68.  It takes 329 us: 34 instructions for a token of four states a
+// 12301 tokens of 4096 channels of 16 states where memory needs 68.  It takes 333 us: 35 instructions for a token of four states a
 // lane, 20 of them the recurrence, 2 the sum over a channel's lanes, the rest steps, gate and conversions; and whole sequences of
-// different lengths on 448 workgroups keep 59 % of the vector unit busy.  Four states a lane: a channel
+// different lengths on 448 workgroups keep 60 % of the vector unit busy.  Four states a lane: a channel
 // of 16 states is four lanes, so one sequence of 4096 channels is 256 waves.  A workgroup's tile of tokens is prepared in LDS,
 // every step (softplus) and product delta u once; B and C are read from there by all lanes, and y, complete after a sum over a
 // channel's lanes, goes back through LDS so that gate and stores are made in rows.
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(256) k_ssm_join(const SsmParams p, int n_block
 }
 
 // One token of each request, the state in a slot of the pool: bound by reading and writing the states (256 requests of 4096 x 16 float32
-// states: 28.5 us, 5.0 TB/s).
+// states: 28.7 us, 5.0 TB/s).
 template <int DT, int N, bool VEC>
 __global__ void __launch_bounds__(kSsmThreads) k_ssm_step(const SsmParams p, int n_blocks) {
     using L = SsmLane<N>;

@@ -13,13 +13,13 @@
 // and dC are sums over all channels: over the wave's by exchanges that halve the values a lane holds each time, over the
 // workgroup's waves in LDS, over the workgroups by k_ssm_sum_bc, all in a fixed order.
 //
-// The vector unit bounds it: 43 instructions for a token of four states a lane in k_ssm_ends (95 % of its time used), 103 in k_ssm_grad
-// (61 to 77 %).  8190 tokens of 4096 channels of 16 states in bfloat16: 713 us (175 to 190 the ends, 16 joining, 560 to 600 the gradients, 20
-// the sums); floor by memory 79 us, by the vector unit 205.  Keeping the states before every 8th token (8 bytes a token and
-// channel, written and read) instead of walking the segment again: 689 -> 604 us.  What staging makes stays in LDS, and the products of
-// two tokens are scheduled apart, or the loads of all eight move up: three waves a SIMD (168 registers, some 20 of them spilled) 557 us,
+// The vector unit bounds it: 43 instructions for a token of four states a lane in k_ssm_ends (all of its time used), 102 in k_ssm_grad
+// (61 %).  8190 tokens of 4096 channels of 16 states in bfloat16: 711 us a pass; floor by memory 79 us, by the vector unit 205.  Under a
+// tracer, where each kernel runs by itself and some 10 % longer, 181 us are the ends, 16 joining, 579 the gradients, 20 the sums.  Keeping the states before
+// every 8th token (8 bytes a token and channel, written and read) instead of walking the segment again: 689 -> 604 us.  What staging makes stays in LDS, and
+// the products of two tokens are scheduled apart, or the loads of all eight move up: three waves a SIMD (168 registers, some 20 of them spilled) 557 us,
 // two (no spills) 605; in float32 and from 64 states on, where 26 to 44 would spill, two waves are faster (36 against 29 us for 515
-// tokens of 256 x 64 in segments of 64).
+// tokens of 256 x 64 in segments of 64).  Rows of single elements (4095 channels): 1084 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
